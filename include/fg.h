@@ -430,6 +430,100 @@ fg_status fg_gather_gemm_noalloc(const fg_config* cfg, int hip_device, const voi
                                  const fg_route* route, const void* W, void* gathered, void* out, int32_t* status,
                                  uint32_t flags, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Decoding operators: the expert layer of a step of 1 to 64 tokens, beside the
+ * gather-GEMM that serves many. No context: every call launches one or two
+ * kernels on `stream` (of the current device), allocates nothing, keeps nothing
+ * and may be captured into a graph. Pointers are device pointers owned by the
+ * caller; `ld*` is the distance of two rows in elements. Sums, means, softmax
+ * statistics and scales are fp32; results are rounded once, to nearest even,
+ * and do not depend on timing. Rows of 0: FG_OK, nothing is launched.
+ * Errors of every entry: FG_EINVAL (shapes, types, NULLs, alignment), FG_EHIP
+ * (the launch failed). */
+
+enum {                     /* element types */
+  FG_BF16 = 0,
+  FG_I8 = 1,               /* int8 codes, -127..127 */
+  FG_E4M3 = 2,             /* 8-bit floats, 4 exponent and 3 mantissa bits, largest 448, no infinities */
+  FG_F32 = 3
+};
+enum { FG_SCORE_SOFTMAX = 0, FG_SCORE_SIGMOID = 1 };
+
+#define FG_NORM_MAX_N 65536
+#define FG_W4_MAX_ROWS 1048576
+#define FG_MOE_FEW_TOKENS 64
+#define FG_MOE_FEW_TOPK 16
+#define FG_MOE_FEW_EXPERTS 1024
+
+/* Residual addition and RMS norm, with a bf16 output, an 8-bit output, or both:
+ *   h = x (+ residual);  y = h * (mean(h^2) + eps)^(-1/2) * gamma   in fp32,
+ *   sum = bf16(h), y = bf16(y), and with a = max |y| over the row (q_group 0) or
+ *   over each 128 columns (q_group 128), Q = 127 (FG_I8) or 448 (FG_E4M3):
+ *   q_scale = a / Q, q = rne(y * (Q / a)), all codes 0 where a = 0.
+ * A NaN or infinity in a row reaches its y and its q_scale (NaN); codes under
+ * such a scale mean nothing.
+ *   x, residual, sum, y: bf16 [rows][ld]; residual, sum and y may be NULL; sum
+ *            and y may be x or residual themselves (same ld)
+ *   gamma:   bf16 [n]
+ *   q:       8-bit [rows][ldq] or NULL;  q_scale: fp32 [rows] or [rows][n / 128]
+ *   n:       1..FG_NORM_MAX_N, any; rows need no more than element alignment
+ *            (a multiple of 128 for q_group 128) */
+fg_status fg_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* gamma, float eps,
+                         void* sum, int64_t lds, void* y, int64_t ldy, void* q, int64_t ldq, int32_t q_type,
+                         int32_t q_group, float* q_scale, int64_t rows, int32_t n, hipStream_t stream);
+
+/* Router: each token's k largest logits, largest first, equal ones by lowest
+ * index (NaN counts as -infinity), and their gate weights
+ *   p = softmax over all experts, or sigmoid;  weight = p * scale, with renorm
+ *   != 0 divided by the sum of the token's k picks (0 where that sum is 0).
+ * The outputs are what a TOPK route, fg_combine and fg_moe_few take.
+ *   logits:  fp32 or bf16 (logits_type) [rows][ld], experts <= FG_MOE_FEW_EXPERTS
+ *   topk:    int32 [rows][k], k <= min(experts, 64);  weights: fp32 [rows][k] */
+fg_status fg_moe_route(const void* logits, int64_t ld, int32_t logits_type, int64_t rows, int32_t experts, int32_t k,
+                       int32_t score, int32_t renorm, float scale, int32_t* topk, float* weights, hipStream_t stream);
+
+/* Products with 4-bit weights and group scales, for few rows:
+ *   out[t][n] = bf16( sum_k x[t][k] * xs * (w[n][k] - zero[n][k / group]) * w_scale[n][k / group] + bias[n] )
+ *   x:       [rows][ldx] bf16, or FG_I8 / FG_E4M3 codes with fp32 x_scale xs, one
+ *            per row (x_group 0: [rows]) or per 128 columns (x_group 128:
+ *            [rows][k / 128], k % 128 == 0), as fg_add_rmsnorm writes them. Rows
+ *            start on 16-byte (bf16) or 8-byte boundaries: ldx % 8 == 0
+ *   w:       uint8 [n][k / 2], 16-byte aligned; element k of a row is the low
+ *            (even k) or high nibble of byte k / 2
+ *   w_scale: bf16 [n][k / group]; group 32, 64 or 128, k % group == 0
+ *   w_zero:  uint8 [n][k / group] or NULL (8 everywhere)
+ *   bias:    bf16 [n] or NULL;  out: bf16 [rows][ldo], any n
+ *   rows:    any up to FG_W4_MAX_ROWS; made for 1 to 64 (more re-read the weights)
+ * An infinity in x gives NaN in the whole row of out. */
+fg_status fg_w4_linear(const void* x, int64_t ldx, int32_t x_type, const float* x_scale, int32_t x_group, const void* w,
+                       const void* w_scale, const void* w_zero, int32_t group, const void* bias, void* out, int64_t ldo,
+                       int64_t rows, int32_t n, int32_t k, hipStream_t stream);
+
+/* Workspace bytes of fg_moe_few. */
+fg_status fg_moe_few_bytes(int32_t tokens, int32_t k, int32_t F, int64_t* bytes);
+
+/* A whole expert layer for few tokens: gate and up products, SiLU, down product
+ * and the weighted sum over each token's picks, in two kernels:
+ *   y[t] = bf16( sum_j weights[t][j] * W2[e] (silu(W1[e][0:F] x[t]) * (W1[e][F:2F] x[t])) ),
+ *   e = topk[t][j] - expert_base, over the picks with 0 <= e < n_local; a token
+ *   with none gets zeros (other ranks' experts add their own terms).
+ * The picked experts' weights are read once for up to 16 tokens an expert.
+ *   x, ldx, x_type, x_scale, x_group: activations [tokens][K], as fg_w4_linear
+ *   w1, w2:  group 0: bf16 [n_local][2F][K] and [n_local][K][F], 16-byte aligned,
+ *            scales and zeros NULL; group 32, 64, 128: 4-bit weights of the same
+ *            rows in the layout of fg_w4_linear with their scales and zeros (or NULL)
+ *   topk:    int32 [tokens][k], distinct per token (negative: no pick);  weights: fp32 [tokens][k]
+ *   tokens <= FG_MOE_FEW_TOKENS, k <= FG_MOE_FEW_TOPK, n_local <= FG_MOE_FEW_EXPERTS,
+ *   K and F multiples of 32 and of group
+ *   workspace: fg_moe_few_bytes(tokens, k, F) bytes, 16-byte aligned, contents
+ *            free; calls that may overlap need one each
+ *   y:       bf16 [tokens][ldy] */
+fg_status fg_moe_few(const void* x, int64_t ldx, int32_t x_type, const float* x_scale, int32_t x_group, const void* w1,
+                     const void* w1_scale, const void* w1_zero, const void* w2, const void* w2_scale, const void* w2_zero,
+                     int32_t group, const int32_t* topk, const float* weights, int32_t tokens, int32_t k,
+                     int32_t expert_base, int32_t n_local, int32_t K, int32_t F, void* workspace, int64_t workspace_bytes,
+                     void* y, int64_t ldy, hipStream_t stream);
+
 /* Copy the observation counters to *out ("NVLink atomic publish" §7: the
  * observation counter and the small library around the protocol; fields as
  * documented in fg_stats_t). wait != 0 first synchronises the bound stream,

@@ -10,8 +10,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIB_DIR, "libfg.so")
-SOURCES = [os.path.join(CSRC, "fg.hip")]
-HEADERS = [os.path.join(CSRC, n) for n in ("fg_sync.hpp", "fg_gemm.hpp", "fg_plan.hpp", "fg_kernels.hpp", "fg_combine.hpp")] + [
+SOURCES = [os.path.join(CSRC, "fg.hip"), os.path.join(CSRC, "fg_ops.hip")]
+HEADERS = [os.path.join(CSRC, n) for n in ("fg_sync.hpp", "fg_gemm.hpp", "fg_plan.hpp", "fg_kernels.hpp", "fg_combine.hpp",
+                                               "fg_ops.hpp", "fg_norm.hpp", "fg_route.hpp", "fg_w4.hpp", "fg_moe.hpp")] + [
     os.path.join(ROOT, "include", "fg.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

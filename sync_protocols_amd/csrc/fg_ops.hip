@@ -1,0 +1,237 @@
+// Entry points of the decoding operators (include/fg.h): argument checks and
+// launches. Nothing is allocated or kept; every call is one or two kernels on
+// the caller's stream, so all of them can be captured into a graph.
+#include "fg_moe.hpp"
+#include "fg_norm.hpp"
+#include "fg_route.hpp"
+#include "fg_w4.hpp"
+
+using namespace fg::ops;
+
+namespace {
+
+#define HIPCHK_LAUNCH() \
+  do { if (hipGetLastError() != hipSuccess) return FG_EHIP; } while (0)
+
+bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+int pow2_at_least(int v) {
+  int p = 1;
+  while (p < v) p *= 2;
+  return p;
+}
+
+// Activation rows of the products: whole 8-element vectors at aligned addresses.
+bool rows_ok(const void* x, int64_t ldx, int32_t type, const float* scale, int32_t group, int32_t k) {
+  if (!x || (type != FG_BF16 && type != FG_I8 && type != FG_E4M3)) return false;
+  const int bytes = type == FG_BF16 ? 2 : 1;
+  if (ldx < k || ldx % 8 || !aligned(x, 8 * bytes)) return false;
+  if (type == FG_BF16) return !scale && group == 0;
+  return scale && aligned(scale, 4) && (group == 0 || (group == 128 && k % 128 == 0));
+}
+
+bool w4_ok(const void* w, const void* s, int32_t group, int32_t k) {
+  return w && s && (group == 32 || group == 64 || group == 128) && k % group == 0 && aligned(w, 16) && aligned(s, 2);
+}
+
+template <int W>
+void launch_norm(int V, const NormArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)a.rows), block(64 * W);
+  switch (V) {
+    case 1: hipLaunchKernelGGL((add_rmsnorm_kernel<W, 1>), grid, block, 0, stream, a); break;
+    case 2: hipLaunchKernelGGL((add_rmsnorm_kernel<W, 2>), grid, block, 0, stream, a); break;
+    case 4: hipLaunchKernelGGL((add_rmsnorm_kernel<W, 4>), grid, block, 0, stream, a); break;
+    default: hipLaunchKernelGGL((add_rmsnorm_kernel<W, 8>), grid, block, 0, stream, a); break;
+  }
+}
+
+template <bool BF16>
+void launch_route(int epl, const RouteArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.rows + 3) / 4)), block(256);
+  switch (epl) {
+    case 1: hipLaunchKernelGGL((moe_route_kernel<1, BF16>), grid, block, 0, stream, a); break;
+    case 2: hipLaunchKernelGGL((moe_route_kernel<2, BF16>), grid, block, 0, stream, a); break;
+    case 4: hipLaunchKernelGGL((moe_route_kernel<4, BF16>), grid, block, 0, stream, a); break;
+    case 8: hipLaunchKernelGGL((moe_route_kernel<8, BF16>), grid, block, 0, stream, a); break;
+    default: hipLaunchKernelGGL((moe_route_kernel<16, BF16>), grid, block, 0, stream, a); break;
+  }
+}
+
+template <int G, int XK, int MT, int R, int P>
+void launch_w4_tile(const W4Args& a, hipStream_t stream) {
+  const dim3 grid((a.n + 16 * R - 1) / (16 * R), (a.rows + 16 * MT - 1) / (16 * MT));
+  hipLaunchKernelGGL((w4_linear_kernel<G, XK, MT, R, P>), grid, dim3(64 * kProdWaves), 0, stream, a);
+}
+
+template <int G, int XK>
+void launch_w4(const W4Args& a, hipStream_t stream) {
+  if (a.rows <= 16) {
+    launch_w4_tile<G, XK, 1, 1, 4>(a, stream);
+  } else if (a.rows <= 32) {
+    launch_w4_tile<G, XK, 2, 2, 2>(a, stream);
+  } else {
+    launch_w4_tile<G, XK, 4, 2, 2>(a, stream);
+  }
+}
+
+template <int G>
+void launch_w4(const W4Args& a, int type, hipStream_t stream) {
+  if (type == FG_BF16) launch_w4<G, X_BF16>(a, stream);
+  else if (type == FG_I8) launch_w4<G, X_I8>(a, stream);
+  else launch_w4<G, X_E4M3>(a, stream);
+}
+
+template <class WT, int XK>
+void launch_moe_up(const MoeArgs<WT>& a, hipStream_t stream) {
+  const int picks = a.tokens * a.k, experts = picks < a.n_local ? picks : a.n_local;
+  const dim3 grid(experts * ((a.F + 15) / 16)), block(64 * kProdWaves);
+  if (a.tokens <= 16) hipLaunchKernelGGL((moe_up_kernel<WT, XK, 1, 2>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((moe_up_kernel<WT, XK, 2, 2>), grid, block, 0, stream, a);
+}
+
+template <class WT, int MT, bool TAIL>
+void launch_moe_down(const MoeArgs<WT>& a, hipStream_t stream) {
+  const size_t lds = (size_t)kProdWaves * a.tokens * 16 * sizeof(float);
+  hipLaunchKernelGGL((moe_down_kernel<WT, MT, 1, 2, TAIL>), dim3((a.K + 15) / 16), dim3(64 * kProdWaves), lds, stream, a);
+}
+
+template <class WT>
+fg_status launch_moe(const MoeArgs<WT>& a, int type, hipStream_t stream) {
+  if (type == FG_BF16) launch_moe_up<WT, X_BF16>(a, stream);
+  else if (type == FG_I8) launch_moe_up<WT, X_I8>(a, stream);
+  else launch_moe_up<WT, X_E4M3>(a, stream);
+  HIPCHK_LAUNCH();
+  const bool tail = a.F % kStep != 0;
+  if (a.tokens <= 16) tail ? launch_moe_down<WT, 1, true>(a, stream) : launch_moe_down<WT, 1, false>(a, stream);
+  else tail ? launch_moe_down<WT, 2, true>(a, stream) : launch_moe_down<WT, 2, false>(a, stream);
+  HIPCHK_LAUNCH();
+  return FG_OK;
+}
+
+template <class WT>
+MoeArgs<WT> moe_args(const void* x, int64_t ldx, int32_t x_type, const float* x_scale, int32_t x_group, const int32_t* topk,
+                     const float* weights, int32_t tokens, int32_t k, int32_t base, int32_t n_local, int32_t K, int32_t F,
+                     void* workspace, void* y, int64_t ldy) {
+  MoeArgs<WT> a{};
+  a.x = (const char*)x; a.xs = x_scale; a.topk = topk; a.weights = weights;
+  a.hi = (uint16_t*)workspace; a.lo = a.hi + (int64_t)tokens * k * F;
+  a.y = (uint16_t*)y;
+  a.ldx = ldx * (x_type == FG_BF16 ? 2 : 1); a.xs_stride = x_group ? K / x_group : 1; a.xs_step = x_group ? 1 : 0; a.ldy = ldy;
+  a.tokens = tokens; a.k = k; a.base = base; a.n_local = n_local; a.K = K; a.F = F;
+  return a;
+}
+
+template <int G>
+fg_status moe_w4(MoeArgs<W4<G>> a, const void* w1, const void* s1, const void* z1, const void* w2, const void* s2, const void* z2,
+                 int type, hipStream_t stream) {
+  a.w1 = {(const char*)w1, (const uint16_t*)s1, (const uint8_t*)z1, a.K / 2, a.K / G};
+  a.w2 = {(const char*)w2, (const uint16_t*)s2, (const uint8_t*)z2, a.F / 2, a.F / G};
+  return launch_moe<W4<G>>(a, type, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+fg_status fg_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* gamma, float eps,
+                         void* sum, int64_t lds, void* y, int64_t ldy, void* q, int64_t ldq, int32_t q_type,
+                         int32_t q_group, float* q_scale, int64_t rows, int32_t n, hipStream_t stream) {
+  if (rows < 0 || rows > 0x7fffffff || n < 1 || n > FG_NORM_MAX_N || !(eps >= 0.0f)) return FG_EINVAL;
+  if (rows == 0) return FG_OK;
+  if (!y && !q) return FG_EINVAL;
+  if (q && ((q_type != FG_I8 && q_type != FG_E4M3) || !q_scale || (q_group != 0 && (q_group != 128 || n % 128)))) return FG_EINVAL;
+  if (!x || !gamma || ldx < n || (residual && ldr < n) || (sum && lds < n) || (y && ldy < n) || (q && ldq < n)) return FG_EINVAL;
+  if (!aligned(x, 2) || !aligned(residual, 2) || !aligned(gamma, 2) || !aligned(sum, 2) || !aligned(y, 2) || !aligned(q_scale, 4))
+    return FG_EINVAL;
+  NormArgs a{};
+  a.x = (const uint16_t*)x; a.res = (const uint16_t*)residual; a.gamma = (const uint16_t*)gamma;
+  a.sum = (uint16_t*)sum; a.y = (uint16_t*)y; a.q = (uint8_t*)q; a.scale = q_scale;
+  a.ldx = ldx; a.ldr = ldr; a.lds = lds; a.ldy = ldy; a.ldq = ldq; a.rows = rows;
+  a.n = n; a.group = q ? q_group : 0; a.q_type = q_type; a.eps = eps;
+  const int nv = (n + 7) / 8, want = rows < 1024 ? 1 : 4;
+  int W = pow2_at_least((nv + 64 * want - 1) / (64 * want));
+  if (W > 16) W = 16;
+  const int V = pow2_at_least((nv + 64 * W - 1) / (64 * W));
+  switch (W) {
+    case 1: launch_norm<1>(V, a, stream); break;
+    case 2: launch_norm<2>(V, a, stream); break;
+    case 4: launch_norm<4>(V, a, stream); break;
+    case 8: launch_norm<8>(V, a, stream); break;
+    default: launch_norm<16>(V, a, stream); break;
+  }
+  HIPCHK_LAUNCH();
+  return FG_OK;
+}
+
+fg_status fg_moe_route(const void* logits, int64_t ld, int32_t logits_type, int64_t rows, int32_t experts, int32_t k,
+                       int32_t score, int32_t renorm, float scale, int32_t* topk, float* weights, hipStream_t stream) {
+  if (rows < 0 || rows > 0x7fffffff || experts < 1 || experts > FG_MOE_FEW_EXPERTS || k < 1 || k > experts || k > 64) return FG_EINVAL;
+  if ((logits_type != FG_F32 && logits_type != FG_BF16) || (score != FG_SCORE_SOFTMAX && score != FG_SCORE_SIGMOID)) return FG_EINVAL;
+  if (rows == 0) return FG_OK;
+  if (!logits || !topk || !weights || ld < experts) return FG_EINVAL;
+  if (!aligned(logits, logits_type == FG_F32 ? 4 : 2) || !aligned(topk, 4) || !aligned(weights, 4)) return FG_EINVAL;
+  RouteArgs a{logits, topk, weights, ld, rows, experts, k, score, renorm, scale};
+  const int epl = pow2_at_least((experts + 63) / 64);
+  logits_type == FG_BF16 ? launch_route<true>(epl, a, stream) : launch_route<false>(epl, a, stream);
+  HIPCHK_LAUNCH();
+  return FG_OK;
+}
+
+fg_status fg_w4_linear(const void* x, int64_t ldx, int32_t x_type, const float* x_scale, int32_t x_group, const void* w,
+                       const void* w_scale, const void* w_zero, int32_t group, const void* bias, void* out, int64_t ldo,
+                       int64_t rows, int32_t n, int32_t k, hipStream_t stream) {
+  if (rows < 0 || rows > FG_W4_MAX_ROWS || n < 1 || k < 1 || !w4_ok(w, w_scale, group, k)) return FG_EINVAL;
+  if (rows == 0) return FG_OK;
+  if (!rows_ok(x, ldx, x_type, x_scale, x_group, k) || !out || ldo < n || !aligned(out, 2) || !aligned(bias, 2)) return FG_EINVAL;
+  W4Args a{};
+  a.x = (const char*)x; a.xs = x_scale; a.w = (const char*)w; a.s = (const uint16_t*)w_scale; a.z = (const uint8_t*)w_zero;
+  a.bias = (const uint16_t*)bias; a.out = (uint16_t*)out;
+  a.ldx = ldx * (x_type == FG_BF16 ? 2 : 1); a.xs_stride = x_group ? k / x_group : 1; a.ldo = ldo;
+  a.rows = (int32_t)rows; a.n = n; a.k = k; a.xs_step = x_group ? 1 : 0;
+  if (group == 32) launch_w4<32>(a, x_type, stream);
+  else if (group == 64) launch_w4<64>(a, x_type, stream);
+  else launch_w4<128>(a, x_type, stream);
+  HIPCHK_LAUNCH();
+  return FG_OK;
+}
+
+fg_status fg_moe_few_bytes(int32_t tokens, int32_t k, int32_t F, int64_t* bytes) {
+  if (!bytes || tokens < 0 || tokens > FG_MOE_FEW_TOKENS || k < 1 || k > FG_MOE_FEW_TOPK || F < 1) return FG_EINVAL;
+  *bytes = 4 * (int64_t)tokens * k * F;
+  return FG_OK;
+}
+
+fg_status fg_moe_few(const void* x, int64_t ldx, int32_t x_type, const float* x_scale, int32_t x_group, const void* w1,
+                     const void* w1_scale, const void* w1_zero, const void* w2, const void* w2_scale, const void* w2_zero,
+                     int32_t group, const int32_t* topk, const float* weights, int32_t tokens, int32_t k,
+                     int32_t expert_base, int32_t n_local, int32_t K, int32_t F, void* workspace, int64_t workspace_bytes,
+                     void* y, int64_t ldy, hipStream_t stream) {
+  if (tokens < 0 || tokens > FG_MOE_FEW_TOKENS || k < 1 || k > FG_MOE_FEW_TOPK || n_local < 1 || n_local > FG_MOE_FEW_EXPERTS ||
+      expert_base < 0 || expert_base > 0x7fffffff - FG_MOE_FEW_EXPERTS || K < 1 || F < 1 || K % 32 || F % 32)
+    return FG_EINVAL;
+  if (group == 0) {
+    if (!w1 || !w2 || w1_scale || w2_scale || w1_zero || w2_zero || !aligned(w1, 16) || !aligned(w2, 16)) return FG_EINVAL;
+  } else if (!w4_ok(w1, w1_scale, group, K) || !w4_ok(w2, w2_scale, group, F)) {
+    return FG_EINVAL;
+  }
+  if (tokens == 0) return FG_OK;
+  if (!rows_ok(x, ldx, x_type, x_scale, x_group, K) || !topk || !weights || !y || ldy < K) return FG_EINVAL;
+  if (!aligned(topk, 4) || !aligned(weights, 4) || !aligned(y, 2)) return FG_EINVAL;
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < 4 * (int64_t)tokens * k * F) return FG_EINVAL;
+  // a grid of at most 2^31 - 1 workgroups
+  if ((int64_t)n_local * ((F + 15) / 16) > 0x7fffffff) return FG_EINVAL;
+#define FG_MOE_ARGS(WT) \
+  moe_args<WT>(x, ldx, x_type, x_scale, x_group, topk, weights, tokens, k, expert_base, n_local, K, F, workspace, y, ldy)
+  if (group == 0) {
+    MoeArgs<W16> a = FG_MOE_ARGS(W16);
+    a.w1 = {(const char*)w1, 2 * (int64_t)K};
+    a.w2 = {(const char*)w2, 2 * (int64_t)F};
+    return launch_moe<W16>(a, x_type, stream);
+  }
+  if (group == 32) return moe_w4<32>(FG_MOE_ARGS(W4<32>), w1, w1_scale, w1_zero, w2, w2_scale, w2_zero, x_type, stream);
+  if (group == 64) return moe_w4<64>(FG_MOE_ARGS(W4<64>), w1, w1_scale, w1_zero, w2, w2_scale, w2_zero, x_type, stream);
+  return moe_w4<128>(FG_MOE_ARGS(W4<128>), w1, w1_scale, w1_zero, w2, w2_scale, w2_zero, x_type, stream);
+#undef FG_MOE_ARGS
+}
+
+}  // extern "C"

@@ -1,0 +1,81 @@
+// Products of few activation rows with 4-bit weights:
+//   out[t][n] = sum_k x[t][k] xs[t][k / 128 or 0] (q[n][k] - z[n][k / G]) s[n][k / G] + bias[n].
+// A workgroup owns 16 R weight rows over the whole K: its waves take the steps
+// of 128 k in turn, so that together they stream whole lines of every row, and
+// their fp32 sums are joined through LDS in wave order (the result does not
+// depend on timing). No workspace, one launch.
+#pragma once
+
+#include "fg_ops.hpp"
+
+namespace fg {
+namespace ops {
+
+struct W4Args {
+  const char* x; const float* xs; const char* w; const uint16_t* s; const uint8_t* z; const uint16_t* bias;
+  uint16_t* out;
+  int64_t ldx, xs_stride, ldo;      // ldx in bytes
+  int32_t rows, n, k, xs_step;
+};
+
+constexpr int kProdWaves = 8;
+
+// Joins the waves' sums of one tile of 16 tokens x 16 R columns and hands each
+// element to `put(token, column, value)`; red: kProdWaves * 16 * (16 R + 1) floats.
+template <int R, int MT, class Put>
+__device__ __forceinline__ void join_tile(const f32x4 (&acc)[R][MT], int m, float* red, Put put) {
+  constexpr int LD = 16 * R + 1;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[(wave * 16 + 4 * (lane >> 4) + i) * LD + 16 * r + (lane & 15)] = acc[r][m][i];
+  __syncthreads();
+  for (int e = threadIdx.x; e < 256 * R; e += 64 * kProdWaves) {
+    const int tok = e / (16 * R), col = e % (16 * R);
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kProdWaves; ++w) v += red[(w * 16 + tok) * LD + col];
+    put(tok, col, v);
+  }
+  __syncthreads();
+}
+
+template <int G, int XK, int MT, int R, int P>
+__global__ __launch_bounds__(64 * kProdWaves) void w4_linear_kernel(W4Args a) {
+  __shared__ float red[kProdWaves * 16 * (16 * R + 1)];
+  typedef W4<G> WT;
+  typedef Product<WT, XK, MT, R, P> Prod;
+  const int lane = threadIdx.x & 63, q = lane >> 4, wave = threadIdx.x >> 6;
+  const int n0 = blockIdx.x * 16 * R, t0 = blockIdx.y * 16 * MT;
+  const typename WT::Mat mat{a.w, a.s, a.z, a.k / 2, a.k / G};
+  typename WT::Row rows[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) rows[r].at(mat, min(n0 + 16 * r + (lane & 15), a.n - 1), q);
+  XPtr<1, MT> xp;
+  XScale<MT> sc;
+  sc.step = a.xs_step;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    xp.p[0][m] = a.x + (int64_t)min(t0 + 16 * m + (lane & 15), a.rows - 1) * a.ldx;
+    if constexpr (Prod::kScaled) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc.p[m][i] = a.xs + (int64_t)min(t0 + 16 * m + 4 * q + i, a.rows - 1) * a.xs_stride;
+    }
+  }
+  f32x4 acc[R][MT];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[r][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  Prod::run(acc, rows, xp, sc, q, wave, kProdWaves, a.k / kStep, a.k % kStep);
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+    join_tile<R, MT>(acc, m, red, [&](int tok, int col, float v) {
+      const int t = t0 + 16 * m + tok, n = n0 + col;
+      if (t < a.rows && n < a.n) a.out[t * a.ldo + n] = f_bf16(a.bias ? v + bf16_f(a.bias[n]) : v);
+    });
+}
+
+}  // namespace ops
+}  // namespace fg

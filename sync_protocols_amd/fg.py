@@ -35,7 +35,8 @@ ROUTE_CONTIG, ROUTE_EXPLICIT, ROUTE_TOPK = 0, 1, 2
 
 EXPORTS = ("fg_init", "fg_gather_gemm", "fg_gather_gemm_staged", "fg_gather_gemm_ring", "fg_ring_bytes", "fg_barrier",
            "fg_pingpong", "fg_stress", "fg_combine", "fg_litmus", "fg_stats", "fg_views", "fg_capacity",
-           "fg_gather_gemm_noalloc", "fg_destroy", "fg_strerror")
+           "fg_gather_gemm_noalloc", "fg_add_rmsnorm", "fg_moe_route", "fg_w4_linear", "fg_moe_few_bytes", "fg_moe_few",
+           "fg_destroy", "fg_strerror")
 
 
 class FgConfig(C.Structure):
@@ -120,6 +121,13 @@ def load_library() -> C.CDLL:
     lib.fg_capacity.argtypes = [C.POINTER(FgConfig), C.POINTER(C.c_int32)]
     lib.fg_gather_gemm_noalloc.argtypes = [C.POINTER(FgConfig), C.c_int, C.POINTER(vp), C.POINTER(FgRoute), vp,
                                            vp, vp, vp, C.c_uint32, vp]
+    i32, i64, f32 = C.c_int32, C.c_int64, C.c_float
+    lib.fg_add_rmsnorm.argtypes = [vp, i64, vp, i64, vp, f32, vp, i64, vp, i64, vp, i64, i32, i32, vp, i64, i32, vp]
+    lib.fg_moe_route.argtypes = [vp, i64, i32, i64, i32, i32, i32, i32, f32, vp, vp, vp]
+    lib.fg_w4_linear.argtypes = [vp, i64, i32, vp, i32, vp, vp, vp, i32, vp, vp, i64, i64, i32, i32, vp]
+    lib.fg_moe_few_bytes.argtypes = [i32, i32, i32, C.POINTER(i64)]
+    lib.fg_moe_few.argtypes = [vp, i64, i32, vp, i32, vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32,
+                               vp, i64, vp, i64, vp]
     lib.fg_destroy.argtypes = [vp]
     lib.fg_strerror.argtypes = [C.c_int]
     lib.fg_strerror.restype = C.c_char_p
