@@ -218,7 +218,7 @@ def _own(c):
     from sync_protocols_amd import ops
 
     if c["op"] == "norm":
-        r = ops.add_rmsnorm(c["xin"], c["gamma"], residual=c["r"], eps=EPS, out=c["out"], group=c["group"])
+        r = ops.add_rmsnorm(c["xin"], c["gamma"], residual=c["r"], eps=EPS, out=c["out"], group=c["group"] if c["out"] != "bf16" else 0)
         out = {"sum": r.sum} if c["res"] else {}
         if c["out"] == "bf16":
             return out | {"y": r.y}
