@@ -13,6 +13,8 @@ namespace {
 #define HIPCHK_LAUNCH() \
   do { if (hipGetLastError() != hipSuccess) return FG_EHIP; } while (0)
 
+constexpr int kCUs = 256;          // compute units of the part
+
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 int pow2_at_least(int v) {
@@ -57,76 +59,58 @@ void launch_route(int epl, const RouteArgs& a, hipStream_t stream) {
   }
 }
 
-template <int G, int XK, int MT, int R, int P>
+template <int G, int XK, int MT, int R, int P, int W>
 void launch_w4_tile(const W4Args& a, hipStream_t stream) {
   const dim3 grid((a.n + 16 * R - 1) / (16 * R), (a.rows + 16 * MT - 1) / (16 * MT));
-  hipLaunchKernelGGL((w4_linear_kernel<G, XK, MT, R, P>), grid, dim3(64 * kProdWaves), 0, stream, a);
+  hipLaunchKernelGGL((w4_linear_kernel<G, XK, MT, R, P, W>), grid, dim3(64 * W), 0, stream, a);
 }
 
 template <int G, int XK>
 void launch_w4(const W4Args& a, hipStream_t stream) {
   if (a.rows <= 16) {
-    launch_w4_tile<G, XK, 1, 1, 4>(a, stream);
+    if (a.n <= 16 * kCUs) launch_w4_tile<G, XK, 1, 1, 2, 16>(a, stream);
+    else launch_w4_tile<G, XK, 1, 2, 2, 8>(a, stream);
   } else if (a.rows <= 32) {
-    launch_w4_tile<G, XK, 2, 2, 2>(a, stream);
+    launch_w4_tile<G, XK, 2, 2, 2, 8>(a, stream);
   } else {
-    launch_w4_tile<G, XK, 4, 2, 2>(a, stream);
+    launch_w4_tile<G, XK, 4, 2, 2, 8>(a, stream);
   }
 }
 
 template <int G>
-void launch_w4(const W4Args& a, int type, hipStream_t stream) {
+void launch_w4(const W4Args& a, int type, bool grouped, hipStream_t stream) {
   if (type == FG_BF16) launch_w4<G, X_BF16>(a, stream);
-  else if (type == FG_I8) launch_w4<G, X_I8>(a, stream);
-  else launch_w4<G, X_E4M3>(a, stream);
+  else if (type == FG_I8) grouped ? launch_w4<G, X_I8G>(a, stream) : launch_w4<G, X_I8>(a, stream);
+  else grouped ? launch_w4<G, X_E4M3G>(a, stream) : launch_w4<G, X_E4M3>(a, stream);
 }
 
-template <class WT, int XK>
-void launch_moe_up(const MoeArgs<WT>& a, hipStream_t stream) {
+template <int G, int XK>
+void launch_moe_up(const MoeArgs& a, hipStream_t stream) {
+  constexpr int C = 1, W = 8;
   const int picks = a.tokens * a.k, experts = picks < a.n_local ? picks : a.n_local;
-  const dim3 grid(experts * ((a.F + 15) / 16)), block(64 * kProdWaves);
-  if (a.tokens <= 16) hipLaunchKernelGGL((moe_up_kernel<WT, XK, 1, 2>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((moe_up_kernel<WT, XK, 2, 2>), grid, block, 0, stream, a);
+  const dim3 grid(experts * ((a.F + 16 * C - 1) / (16 * C))), block(64 * W);
+  if (a.tokens <= 16) hipLaunchKernelGGL((moe_up_kernel<G, XK, 1, C, 2, W>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((moe_up_kernel<G, XK, 2, C, 2, W>), grid, block, 0, stream, a);
 }
 
-template <class WT, int MT, bool TAIL>
-void launch_moe_down(const MoeArgs<WT>& a, hipStream_t stream) {
-  const size_t lds = (size_t)kProdWaves * a.tokens * 16 * sizeof(float);
-  hipLaunchKernelGGL((moe_down_kernel<WT, MT, 1, 2, TAIL>), dim3((a.K + 15) / 16), dim3(64 * kProdWaves), lds, stream, a);
-}
-
-template <class WT>
-fg_status launch_moe(const MoeArgs<WT>& a, int type, hipStream_t stream) {
-  if (type == FG_BF16) launch_moe_up<WT, X_BF16>(a, stream);
-  else if (type == FG_I8) launch_moe_up<WT, X_I8>(a, stream);
-  else launch_moe_up<WT, X_E4M3>(a, stream);
-  HIPCHK_LAUNCH();
-  const bool tail = a.F % kStep != 0;
-  if (a.tokens <= 16) tail ? launch_moe_down<WT, 1, true>(a, stream) : launch_moe_down<WT, 1, false>(a, stream);
-  else tail ? launch_moe_down<WT, 2, true>(a, stream) : launch_moe_down<WT, 2, false>(a, stream);
-  HIPCHK_LAUNCH();
-  return FG_OK;
-}
-
-template <class WT>
-MoeArgs<WT> moe_args(const void* x, int64_t ldx, int32_t x_type, const float* x_scale, int32_t x_group, const int32_t* topk,
-                     const float* weights, int32_t tokens, int32_t k, int32_t base, int32_t n_local, int32_t K, int32_t F,
-                     void* workspace, void* y, int64_t ldy) {
-  MoeArgs<WT> a{};
-  a.x = (const char*)x; a.xs = x_scale; a.topk = topk; a.weights = weights;
-  a.hi = (uint16_t*)workspace; a.lo = a.hi + (int64_t)tokens * k * F;
-  a.y = (uint16_t*)y;
-  a.ldx = ldx * (x_type == FG_BF16 ? 2 : 1); a.xs_stride = x_group ? K / x_group : 1; a.xs_step = x_group ? 1 : 0; a.ldy = ldy;
-  a.tokens = tokens; a.k = k; a.base = base; a.n_local = n_local; a.K = K; a.F = F;
-  return a;
+template <int G, int MT, int R, bool TAIL>
+void launch_moe_down(const MoeArgs& a, hipStream_t stream) {
+  constexpr int W = 8;
+  const size_t lds = (size_t)W * a.tokens * 16 * R * sizeof(float);
+  hipLaunchKernelGGL((moe_down_kernel<G, MT, R, 2, W, TAIL>), dim3((a.K + 16 * R - 1) / (16 * R)), dim3(64 * W), lds, stream, a);
 }
 
 template <int G>
-fg_status moe_w4(MoeArgs<W4<G>> a, const void* w1, const void* s1, const void* z1, const void* w2, const void* s2, const void* z2,
-                 int type, hipStream_t stream) {
-  a.w1 = {(const char*)w1, (const uint16_t*)s1, (const uint8_t*)z1, a.K / 2, a.K / G};
-  a.w2 = {(const char*)w2, (const uint16_t*)s2, (const uint8_t*)z2, a.F / 2, a.F / G};
-  return launch_moe<W4<G>>(a, type, stream);
+fg_status launch_moe(const MoeArgs& a, int type, bool grouped, hipStream_t stream) {
+  if (type == FG_BF16) launch_moe_up<G, X_BF16>(a, stream);
+  else if (type == FG_I8) grouped ? launch_moe_up<G, X_I8G>(a, stream) : launch_moe_up<G, X_I8>(a, stream);
+  else grouped ? launch_moe_up<G, X_E4M3G>(a, stream) : launch_moe_up<G, X_E4M3>(a, stream);
+  HIPCHK_LAUNCH();
+  const bool tail = a.F % kStep != 0;
+  if (a.tokens <= 16) tail ? launch_moe_down<G, 1, 1, true>(a, stream) : launch_moe_down<G, 1, 1, false>(a, stream);
+  else tail ? launch_moe_down<G, 2, 1, true>(a, stream) : launch_moe_down<G, 2, 1, false>(a, stream);
+  HIPCHK_LAUNCH();
+  return FG_OK;
 }
 
 }  // namespace
@@ -187,10 +171,10 @@ fg_status fg_w4_linear(const void* x, int64_t ldx, int32_t x_type, const float* 
   a.x = (const char*)x; a.xs = x_scale; a.w = (const char*)w; a.s = (const uint16_t*)w_scale; a.z = (const uint8_t*)w_zero;
   a.bias = (const uint16_t*)bias; a.out = (uint16_t*)out;
   a.ldx = ldx * (x_type == FG_BF16 ? 2 : 1); a.xs_stride = x_group ? k / x_group : 1; a.ldo = ldo;
-  a.rows = (int32_t)rows; a.n = n; a.k = k; a.xs_step = x_group ? 1 : 0;
-  if (group == 32) launch_w4<32>(a, x_type, stream);
-  else if (group == 64) launch_w4<64>(a, x_type, stream);
-  else launch_w4<128>(a, x_type, stream);
+  a.rows = (int32_t)rows; a.n = n; a.k = k;
+  if (group == 32) launch_w4<32>(a, x_type, x_group != 0, stream);
+  else if (group == 64) launch_w4<64>(a, x_type, x_group != 0, stream);
+  else launch_w4<128>(a, x_type, x_group != 0, stream);
   HIPCHK_LAUNCH();
   return FG_OK;
 }
@@ -220,18 +204,19 @@ fg_status fg_moe_few(const void* x, int64_t ldx, int32_t x_type, const float* x_
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < 4 * (int64_t)tokens * k * F) return FG_EINVAL;
   // a grid of at most 2^31 - 1 workgroups
   if ((int64_t)n_local * ((F + 15) / 16) > 0x7fffffff) return FG_EINVAL;
-#define FG_MOE_ARGS(WT) \
-  moe_args<WT>(x, ldx, x_type, x_scale, x_group, topk, weights, tokens, k, expert_base, n_local, K, F, workspace, y, ldy)
-  if (group == 0) {
-    MoeArgs<W16> a = FG_MOE_ARGS(W16);
-    a.w1 = {(const char*)w1, 2 * (int64_t)K};
-    a.w2 = {(const char*)w2, 2 * (int64_t)F};
-    return launch_moe<W16>(a, x_type, stream);
-  }
-  if (group == 32) return moe_w4<32>(FG_MOE_ARGS(W4<32>), w1, w1_scale, w1_zero, w2, w2_scale, w2_zero, x_type, stream);
-  if (group == 64) return moe_w4<64>(FG_MOE_ARGS(W4<64>), w1, w1_scale, w1_zero, w2, w2_scale, w2_zero, x_type, stream);
-  return moe_w4<128>(FG_MOE_ARGS(W4<128>), w1, w1_scale, w1_zero, w2, w2_scale, w2_zero, x_type, stream);
-#undef FG_MOE_ARGS
+  MoeArgs a{};
+  a.x = (const char*)x; a.xs = x_scale; a.topk = topk; a.weights = weights;
+  a.w1 = (const char*)w1; a.s1 = (const uint16_t*)w1_scale; a.z1 = (const uint8_t*)w1_zero;
+  a.w2 = (const char*)w2; a.s2 = (const uint16_t*)w2_scale; a.z2 = (const uint8_t*)w2_zero;
+  a.hi = (uint16_t*)workspace; a.lo = a.hi + (int64_t)tokens * k * F;
+  a.y = (uint16_t*)y;
+  a.ldx = ldx * (x_type == FG_BF16 ? 2 : 1); a.xs_stride = x_group ? K / x_group : 1; a.ldy = ldy;
+  a.tokens = tokens; a.k = k; a.base = expert_base; a.n_local = n_local; a.K = K; a.F = F;
+  const bool grouped = x_group != 0;
+  if (group == 0) return launch_moe<0>(a, x_type, grouped, stream);
+  if (group == 32) return launch_moe<32>(a, x_type, grouped, stream);
+  if (group == 64) return launch_moe<64>(a, x_type, grouped, stream);
+  return launch_moe<128>(a, x_type, grouped, stream);
 }
 
 }  // extern "C"

@@ -15,14 +15,12 @@ struct W4Args {
   const char* x; const float* xs; const char* w; const uint16_t* s; const uint8_t* z; const uint16_t* bias;
   uint16_t* out;
   int64_t ldx, xs_stride, ldo;      // ldx in bytes
-  int32_t rows, n, k, xs_step;
+  int32_t rows, n, k;
 };
 
-constexpr int kProdWaves = 8;
-
-// Joins the waves' sums of one tile of 16 tokens x 16 R columns and hands each
-// element to `put(token, column, value)`; red: kProdWaves * 16 * (16 R + 1) floats.
-template <int R, int MT, class Put>
+// Joins the sums that W waves have of one tile of 16 tokens x 16 R columns and
+// hands each element to `put(token, column, value)`; red: W * 16 * (16 R + 1) floats.
+template <int R, int MT, int W, class Put>
 __device__ __forceinline__ void join_tile(const f32x4 (&acc)[R][MT], int m, float* red, Put put) {
   constexpr int LD = 16 * R + 1;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -31,49 +29,48 @@ __device__ __forceinline__ void join_tile(const f32x4 (&acc)[R][MT], int m, floa
 #pragma unroll
     for (int i = 0; i < 4; ++i) red[(wave * 16 + 4 * (lane >> 4) + i) * LD + 16 * r + (lane & 15)] = acc[r][m][i];
   __syncthreads();
-  for (int e = threadIdx.x; e < 256 * R; e += 64 * kProdWaves) {
+  for (int e = threadIdx.x; e < 256 * R; e += 64 * W) {
     const int tok = e / (16 * R), col = e % (16 * R);
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kProdWaves; ++w) v += red[(w * 16 + tok) * LD + col];
+    for (int w = 0; w < W; ++w) v += red[(w * 16 + tok) * LD + col];
     put(tok, col, v);
   }
   __syncthreads();
 }
 
-template <int G, int XK, int MT, int R, int P>
-__global__ __launch_bounds__(64 * kProdWaves) void w4_linear_kernel(W4Args a) {
-  __shared__ float red[kProdWaves * 16 * (16 * R + 1)];
-  typedef W4<G> WT;
-  typedef Product<WT, XK, MT, R, P> Prod;
-  const int lane = threadIdx.x & 63, q = lane >> 4, wave = threadIdx.x >> 6;
+template <int G, int XK, int MT, int R, int P, int W>
+__global__ __launch_bounds__(64 * W) void w4_linear_kernel(W4Args a) {
+  __shared__ float red[W * 16 * (16 * R + 1)];
+  typedef Quant4<G, XK, MT, R, P> Prod;
+  const int lane = threadIdx.x & 63, q = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = blockIdx.x * 16 * R, t0 = blockIdx.y * 16 * MT;
-  const typename WT::Mat mat{a.w, a.s, a.z, a.k / 2, a.k / G};
-  typename WT::Row rows[R];
+  const typename Prod::Mat mat = typename Prod::Mat{a.w, a.s, a.z, a.k / 2, a.k / G}.at(n0);
+  typename Prod::Row rows[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) rows[r].at(mat, min(n0 + 16 * r + (lane & 15), a.n - 1), q);
+  for (int r = 0; r < R; ++r) rows[r].set(mat, min(16 * r + (lane & 15), a.n - 1 - n0), q);
   XPtr<1, MT> xp;
   XScale<MT> sc;
-  sc.step = a.xs_step;
+  sc.base = a.xs + t0 * a.xs_stride;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     xp.p[0][m] = a.x + (int64_t)min(t0 + 16 * m + (lane & 15), a.rows - 1) * a.ldx;
-    if constexpr (Prod::kScaled) {
+    if constexpr (Prod::kGrouped) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sc.p[m][i] = a.xs + (int64_t)min(t0 + 16 * m + 4 * q + i, a.rows - 1) * a.xs_stride;
+      for (int i = 0; i < 4; ++i) sc.at[m][i] = (uint32_t)min(16 * m + 4 * q + i, a.rows - 1 - t0) * (uint32_t)a.xs_stride;
     }
   }
   f32x4 acc[R][MT];
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[r][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-  Prod::run(acc, rows, xp, sc, q, wave, kProdWaves, a.k / kStep, a.k % kStep);
+  clear<Prod>(acc);
+  run_steps<Prod>(acc, mat, rows, xp, sc, q, wave, W, a.k / kStep, a.k % kStep);
 #pragma unroll
   for (int m = 0; m < MT; ++m)
-    join_tile<R, MT>(acc, m, red, [&](int tok, int col, float v) {
+    join_tile<R, MT, W>(acc, m, red, [&](int tok, int col, float v) {
       const int t = t0 + 16 * m + tok, n = n0 + col;
-      if (t < a.rows && n < a.n) a.out[t * a.ldo + n] = f_bf16(a.bias ? v + bf16_f(a.bias[n]) : v);
+      if (t < a.rows && n < a.n) {
+        if constexpr (x_row_scaled(XK)) v *= a.xs[t];
+        a.out[t * a.ldo + n] = f_bf16(a.bias ? v + bf16_f(a.bias[n]) : v);
+      }
     });
 }
 
