@@ -23,10 +23,11 @@ struct MoeArgs {
   const char* x; const float* xs; const int32_t* topk; const float* weights;
   const char* w1; const uint16_t* s1; const uint8_t* z1;
   const char* w2; const uint16_t* s2; const uint8_t* z2;
-  uint16_t* hi; uint16_t* lo;        // [tokens * k][F], in paired() order for 4-bit weights
+  char* h;                           // SplitRows: this GPU's picks by expert, by pick within an expert
   uint16_t* y;
   int64_t ldx, xs_stride, ldy;       // ldx in bytes
   int32_t tokens, k, base, n_local, K, F;
+  uint32_t plane;                    // of h
 };
 
 // This GPU's expert of a pick, >= n_local for one that is not here (unsigned: no
@@ -41,32 +42,30 @@ __device__ __forceinline__ Mat matrix(const char* w, const uint16_t* s, const ui
 
 // ---- kernel 1: workgroup (a, f) = 16 C columns of the a-th picked expert
 template <int G, int XK, int MT, int C, int P, int W>
-__device__ __forceinline__ void moe_up_pass(const MoeArgs& a, int e, int f0, const uint16_t* list, int s0, int cnt, float* red) {
+__device__ __forceinline__ void moe_up_pass(const MoeArgs& a, int e, int f0, const uint16_t* list, int start, int s0, int cnt, float* red) {
   typedef typename ProductOf<G, XK, MT, 2 * C, P>::T Prod;
-  const int lane = threadIdx.x & 63, q = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Lanes ln;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const typename Prod::Mat mat = matrix<G, typename Prod::Mat>(a.w1, a.s1, a.z1, a.K).at((int64_t)e * 2 * a.F + f0);
   typename Prod::Row rows[2 * C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int f = min(16 * c + (lane & 15), a.F - 1 - f0);
-    rows[c].set(mat, f, q);
-    rows[C + c].set(mat, a.F + f, q);
+    const int last = a.F - 1 - f0, f = min(16 * c + ln.load_row(), last), sf = min(16 * c + (ln.lane & 15), last);
+    rows[c].set(mat, f, sf, ln);
+    rows[C + c].set(mat, a.F + f, a.F + sf, ln);
   }
-  XPtr<1, MT> xp;
-  XScale<MT> sc;
-  sc.base = a.xs;
+  XPtr<MT> xp;
+  xp.scale = a.xs;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    xp.p[0][m] = a.x + (int64_t)(list[min(s0 + 16 * m + (lane & 15), cnt - 1)] / a.k) * a.ldx;
-    if constexpr (Prod::kGrouped) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        sc.at[m][i] = (uint32_t)(list[min(s0 + 16 * m + 4 * q + i, cnt - 1)] / a.k) * (uint32_t)a.xs_stride;
-    }
+    xp.p[m] = a.x + (int64_t)(list[min(s0 + 16 * m + ln.load_row(), cnt - 1)] / a.k) * a.ldx + x_piece<G, XK>(ln);
+    xp.at[m] = (uint32_t)(list[min(s0 + 16 * m + (ln.lane & 15), cnt - 1)] / a.k) * (uint32_t)a.xs_stride;
   }
   f32x4 acc[2 * C][MT];
   clear<Prod>(acc);
-  run_steps<Prod>(acc, mat, rows, xp, sc, q, wave, W, a.K / kStep, a.K % kStep);
+  const int steps = a.K / kStep;
+  run_steps<Prod>(acc, mat, rows, xp, ln, wave, W, (steps - wave + W - 1) / W);
+  if (a.K % kStep && steps % W == wave) run_tail<Prod>(acc, mat, rows, xp, ln, steps, a.K % kStep);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     if (s0 + 16 * m >= cnt) break;
@@ -74,7 +73,7 @@ __device__ __forceinline__ void moe_up_pass(const MoeArgs& a, int e, int f0, con
 #pragma unroll
     for (int r = 0; r < 2 * C; ++r)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) red[(wave * 16 + 4 * q + i) * LD + 16 * r + (lane & 15)] = acc[r][m][i];
+      for (int i = 0; i < 4; ++i) red[(wave * 16 + 4 * ln.quarter + i) * LD + 16 * r + (ln.lane & 15)] = acc[r][m][i];
     __syncthreads();
     for (int o = threadIdx.x; o < 256 * C; o += 64 * W) {
       const int tok = o / (16 * C), col = o % (16 * C), slot = s0 + 16 * m + tok;
@@ -93,10 +92,10 @@ __device__ __forceinline__ void moe_up_pass(const MoeArgs& a, int e, int f0, con
       }
       const float h = g / (1.0f + __expf(-g)) * u * a.weights[p];
       const uint16_t hi = f_bf16(h);
-      const int64_t at = (int64_t)p * a.F + (G == 0 ? f0 + col : paired_place(f0 + col));
-      a.hi[at] = hi;
+      char* to = a.h + SplitRows::at(start + slot, G == 0 ? f0 + col : paired_place(f0 + col), a.plane);
+      *(uint16_t*)to = hi;
       // an infinite hi has no remainder
-      a.lo[at] = fabsf(bf16_f(hi)) < __builtin_inff() ? f_bf16(h - bf16_f(hi)) : 0;
+      *(uint16_t*)(to + a.plane) = fabsf(bf16_f(hi)) < __builtin_inff() ? f_bf16(h - bf16_f(hi)) : 0;
     }
     __syncthreads();
   }
@@ -106,13 +105,11 @@ template <int G, int XK, int MT, int C, int P, int W>
 __global__ __launch_bounds__(64 * W) void moe_up_kernel(MoeArgs a) {
   __shared__ uint32_t bits[FG_MOE_FEW_EXPERTS / 32];
   __shared__ uint16_t list[kMaxPicks];
-  __shared__ int count;
   __shared__ float red[W * 16 * (32 * C + 1)];
   const int tid = threadIdx.x, lane = tid & 63;
   const int picks = a.tokens * a.k, ft = (a.F + 16 * C - 1) / (16 * C);
   const int nth = blockIdx.x / ft, f0 = (blockIdx.x % ft) * 16 * C;
   if (tid < FG_MOE_FEW_EXPERTS / 32) bits[tid] = 0;
-  if (tid == 0) count = 0;
   __syncthreads();
   for (int p = tid; p < picks; p += 64 * W) {
     const uint32_t e = local_expert(a.topk[p], a.base);
@@ -133,36 +130,39 @@ __global__ __launch_bounds__(64 * W) void moe_up_kernel(MoeArgs a) {
   uint32_t rest = __shfl(word, at);
   for (int i = nth - (__shfl(upto, at) - __popc(rest)); i > 0; --i) rest &= rest - 1;
   const int e = __builtin_amdgcn_readfirstlane(32 * at + __ffs(rest) - 1);
-  // its picks, in no particular order: each is a row of its own in the products
-  for (int p = tid; p < picks; p += 64 * W)
-    if (local_expert(a.topk[p], a.base) == (uint32_t)e) list[atomicAdd(&count, 1)] = (uint16_t)p;
+  // its picks in order, and how many belong to experts before it: its place among h's rows
+  int cnt = 0, start = 0;
+  for (int p0 = 0; p0 < picks; p0 += 64) {
+    const uint32_t l = p0 + lane < picks ? local_expert(a.topk[p0 + lane], a.base) : 0xffffffffu;
+    const unsigned long long here = __ballot(l == (uint32_t)e);
+    if (tid < 64 && l == (uint32_t)e) list[cnt + __popcll(here & ((1ull << lane) - 1))] = (uint16_t)(p0 + lane);
+    cnt += __popcll(here);
+    start += __popcll(__ballot(l < (uint32_t)e));
+  }
   __syncthreads();
-  const int cnt = count;
   if (cnt <= 16 || MT == 1) {
-    for (int s0 = 0; s0 < cnt; s0 += 16) moe_up_pass<G, XK, 1, C, P, W>(a, e, f0, list, s0, cnt, red);
+    for (int s0 = 0; s0 < cnt; s0 += 16) moe_up_pass<G, XK, 1, C, P, W>(a, e, f0, list, start, s0, cnt, red);
   } else if constexpr (MT > 1) {
-    for (int s0 = 0; s0 < cnt; s0 += 16 * MT) moe_up_pass<G, XK, MT, C, 2, W>(a, e, f0, list, s0, cnt, red);
+    for (int s0 = 0; s0 < cnt; s0 += 16 * MT) moe_up_pass<G, XK, MT, C, P, W>(a, e, f0, list, start, s0, cnt, red);
   }
 }
 
 // ---- kernel 2: workgroup = 16 R columns of y over every picked expert.
 // Its work is a list of entries, each up to 16 MT picks of one expert, sorted by
-// expert and within it by pick; the waves take equal, contiguous shares of the
-// list's steps, so that they stay level whatever the number of experts, with P
-// steps in flight across the borders between entries.
-template <int MT>
+// expert and within it by pick, as the rows of h are; the waves take equal,
+// contiguous shares of the list's steps, so that they stay level whatever the
+// number of experts.
 struct DownPlan {
   unsigned long long mask[FG_MOE_FEW_EXPERTS];     // tokens that picked an expert
   uint16_t start[FG_MOE_FEW_EXPERTS];
-  uint16_t order[kMaxPicks];                       // picks in the list's order
-  uint8_t token[kMaxPicks];                        // and their tokens
-  uint16_t ent_e[kMaxPicks], ent_s[kMaxPicks];     // entry: expert, first pick, picks
+  uint16_t ent_e[kMaxPicks], ent_s[kMaxPicks];     // entry: expert, first row of h, rows
   uint8_t ent_c[kMaxPicks];
+  uint8_t token[kMaxPicks];                        // of a row of h
   int entries, again;
 };
 
 template <int MT, int W>
-__device__ __forceinline__ void down_plan(const MoeArgs& a, DownPlan<MT>& pl) {
+__device__ __forceinline__ void down_plan(const MoeArgs& a, DownPlan& pl) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int picks = a.tokens * a.k;
   for (int i = tid; i < a.n_local; i += 64 * W) pl.mask[i] = 0;
@@ -209,90 +209,58 @@ __device__ __forceinline__ void down_plan(const MoeArgs& a, DownPlan<MT>& pl) {
     const uint32_t e = local_expert(a.topk[p], a.base);
     if (e >= (uint32_t)a.n_local) continue;
     const int t = p / a.k;
-    const int at = pl.start[e] + (again ? same_before(e, p) : __popcll(pl.mask[e] & ((1ull << t) - 1)));
-    pl.order[at] = (uint16_t)p;
-    pl.token[at] = (uint8_t)t;
+    pl.token[pl.start[e] + (again ? same_before(e, p) : __popcll(pl.mask[e] & ((1ull << t) - 1)))] = (uint8_t)t;
   }
   __syncthreads();
 }
 
-template <int G, int MT, int R, int P, int W, bool TAIL>
+template <int G, int MT, int R, int P, int W>
 __global__ __launch_bounds__(64 * W) void moe_down_kernel(MoeArgs a) {
   typedef typename ProductOf<G, X_SPLIT, MT, R, P>::T Prod;
-  __shared__ DownPlan<MT> pl;
+  __shared__ DownPlan pl;
   extern __shared__ float sums[];                  // [wave][token][16 R]
-  const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, col = lane & 15;
+  const Lanes ln;
+  const int tid = threadIdx.x, col = ln.lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n0 = blockIdx.x * 16 * R;
   for (int i = tid; i < W * a.tokens * 16 * R; i += 64 * W) sums[i] = 0.0f;
   down_plan<MT, W>(a, pl);
-  const int steps = (a.F + kStep - 1) / kStep;
+  const int steps = (a.F + kStep - 1) / kStep, full = a.F / kStep;
   const int64_t units = (int64_t)__builtin_amdgcn_readfirstlane(pl.entries) * steps;
-  const int64_t from = units * wave / W, mine = units * (wave + 1) / W - from;
-  if (mine > 0) {
-    const typename Prod::Mat all = matrix<G, typename Prod::Mat>(a.w2, a.s2, a.z2, a.F).at(n0);
-    typename Prod::Row rows[R];
+  const int64_t from = units * wave / W, to = units * (wave + 1) / W;
+  const typename Prod::Mat all = matrix<G, typename Prod::Mat>(a.w2, a.s2, a.z2, a.F).at(n0);
+  typename Prod::Row rows[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) rows[r].set(all, min(16 * r + col, a.K - 1 - n0), q);
+  for (int r = 0; r < R; ++r) {
+    const int last = a.K - 1 - n0;
+    rows[r].set(all, min(16 * r + ln.load_row(), last), min(16 * r + col, last), ln);
+  }
+  XPtr<MT> xp;
+  xp.plane = a.plane;
+  int ent = (int)(from / steps), step = (int)(from % steps);
+  for (int64_t left = to - from; left > 0; ++ent, step = 0) {
+    const int s = __builtin_amdgcn_readfirstlane(pl.ent_s[ent]), c = __builtin_amdgcn_readfirstlane(pl.ent_c[ent]);
+    const typename Prod::Mat mat = all.at((int64_t)__builtin_amdgcn_readfirstlane(pl.ent_e[ent]) * a.K);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)                   // past the entry: its last row, whose results are not used again
+      xp.p[m] = a.h + SplitRows::at(s + min(16 * m + col, c - 1), 8 * ln.quarter, a.plane);
+    const int end = steps - step < left ? steps : step + (int)left;
+    left -= end - step;
     f32x4 acc[R][MT];
     clear<Prod>(acc);
-    XScale<MT> sc;
-    int ce = (int)(from / steps), cs = (int)(from % steps);   // next step to use
-    int le = ce, ls = cs;                                     // next step to load, from
-    typename Prod::Mat mat;                                   // this matrix and these rows
-    XPtr<2, MT> xp;
-    auto enter = [&](int ent) {
-      const int s = pl.ent_s[ent], c = pl.ent_c[ent];
-      mat = all.at((int64_t)__builtin_amdgcn_readfirstlane(pl.ent_e[ent]) * a.K);
+    run_steps<Prod>(acc, mat, rows, xp, ln, step, 1, min(end, full) - step);
+    if (end > full) run_tail<Prod>(acc, mat, rows, xp, ln, full, a.F % kStep);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int64_t p = pl.order[s + min(16 * m + col, c - 1)];
-        xp.p[0][m] = (const char*)(a.hi + p * a.F);
-        xp.p[1][m] = (const char*)(a.lo + p * a.F);
-      }
-    };
-    int64_t loaded = 0;
-    typename Prod::Stage st[P];
-    auto next = [&](typename Prod::Stage& to) {    // past the end: the last step again, unused
-      Prod::template load<TAIL>(to, mat, rows, xp, sc, q, ls, TAIL ? a.F - ls * kStep : kStep);
-      if (++loaded < mine && ++ls == steps) {
-        ls = 0;
-        enter(++le);
-      }
-    };
-    auto use = [&](const typename Prod::Stage& from, bool last) {
-      Prod::template consume<TAIL>(from, acc, TAIL ? a.F - cs * kStep : kStep);
-      if (++cs < steps && !last) return;
-      const int s = pl.ent_s[ce], c = pl.ent_c[ce];
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int i = 0; i < 4; ++i) {
+        const int slot = 16 * m + 4 * ln.quarter + i;
+        if (slot < c) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int slot = 16 * m + 4 * q + i;
-          if (slot < c) {
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-              unsafeAtomicAdd(&sums[(wave * a.tokens + pl.token[s + slot]) * 16 * R + 16 * r + col], acc[r][m][i]);
-          }
+          for (int r = 0; r < R; ++r)
+            unsafeAtomicAdd(&sums[(wave * a.tokens + pl.token[s + slot]) * 16 * R + 16 * r + col], acc[r][m][i]);
         }
-      clear<Prod>(acc);
-      cs = 0;
-      ++ce;
-    };
-    enter(le);
-#pragma unroll
-    for (int p = 0; p < P; ++p) next(st[p]);
-    int64_t i = 0;
-    for (; i + P < mine; i += P) {
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        use(st[p], false);
-        next(st[p]);
       }
-    }
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-      if (i + p < mine) use(st[p], i + p + 1 == mine);
   }
   __syncthreads();
   for (int i = tid; i < a.tokens * 16 * R; i += 64 * W) {

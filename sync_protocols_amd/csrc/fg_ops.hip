@@ -65,16 +65,17 @@ void launch_w4_tile(const W4Args& a, hipStream_t stream) {
   hipLaunchKernelGGL((w4_linear_kernel<G, XK, MT, R, P, W>), grid, dim3(64 * W), 0, stream, a);
 }
 
+// The tile of 16 MT rows by 16 R columns. Up to 16 rows one column tile a
+// workgroup spreads the weights evenly over the compute units (5 x 8199 x 7200:
+// 18 us, with two 21 us); where that leaves most of them with one workgroup or
+// none, 16 waves share its steps. More rows take two column tiles, so that the
+// activations are read half as often (64 x 8192 x 8192: 22 us, with one 29 us).
 template <int G, int XK>
 void launch_w4(const W4Args& a, hipStream_t stream) {
-  if (a.rows <= 16) {
-    if (a.n <= 16 * kCUs) launch_w4_tile<G, XK, 1, 1, 2, 16>(a, stream);
-    else launch_w4_tile<G, XK, 1, 2, 2, 8>(a, stream);
-  } else if (a.rows <= 32) {
-    launch_w4_tile<G, XK, 2, 2, 2, 8>(a, stream);
-  } else {
-    launch_w4_tile<G, XK, 4, 2, 2, 8>(a, stream);
-  }
+  if (a.rows > 32) launch_w4_tile<G, XK, 4, 2, 2, 8>(a, stream);
+  else if (a.rows > 16) launch_w4_tile<G, XK, 2, 2, 1, 8>(a, stream);
+  else if (a.n <= 16 * kCUs) launch_w4_tile<G, XK, 1, 1, 1, 16>(a, stream);
+  else launch_w4_tile<G, XK, 1, 1, 2, 8>(a, stream);
 }
 
 template <int G>
@@ -84,20 +85,40 @@ void launch_w4(const W4Args& a, int type, bool grouped, hipStream_t stream) {
   else grouped ? launch_w4<G, X_E4M3G>(a, stream) : launch_w4<G, X_E4M3>(a, stream);
 }
 
-template <int G, int XK>
-void launch_moe_up(const MoeArgs& a, hipStream_t stream) {
-  constexpr int C = 1, W = 8;
+// More than 16 rows an expert on average, were all picks here: two row tiles, so
+// that an expert's weights are still read once or twice; else one, whose fewer
+// registers leave room for more waves (64 tokens over 64 experts: 230 us, with two
+// row tiles 258 us).
+bool many_rows(const MoeArgs& a) { return a.tokens > 16 && a.tokens * a.k > 16 * a.n_local; }
+
+template <int G, int XK, int MT, int C, int P, int W>
+void launch_moe_up_tile(const MoeArgs& a, hipStream_t stream) {
   const int picks = a.tokens * a.k, experts = picks < a.n_local ? picks : a.n_local;
-  const dim3 grid(experts * ((a.F + 16 * C - 1) / (16 * C))), block(64 * W);
-  if (a.tokens <= 16) hipLaunchKernelGGL((moe_up_kernel<G, XK, 1, C, 2, W>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((moe_up_kernel<G, XK, 2, C, 2, W>), grid, block, 0, stream, a);
+  const dim3 grid(experts * ((a.F + 16 * C - 1) / (16 * C)));
+  hipLaunchKernelGGL((moe_up_kernel<G, XK, MT, C, P, W>), grid, dim3(64 * W), 0, stream, a);
 }
 
-template <int G, int MT, int R, bool TAIL>
-void launch_moe_down(const MoeArgs& a, hipStream_t stream) {
-  constexpr int W = 8;
+template <int G, int XK>
+void launch_moe_up(const MoeArgs& a, hipStream_t stream) {
+  if constexpr (G == 0) many_rows(a) ? launch_moe_up_tile<G, XK, 2, 1, 2, 4>(a, stream) : launch_moe_up_tile<G, XK, 1, 1, 2, 4>(a, stream);
+  else many_rows(a) ? launch_moe_up_tile<G, XK, 2, 2, 2, 8>(a, stream) : launch_moe_up_tile<G, XK, 1, 2, 1, 4>(a, stream);
+}
+
+template <int G, int MT, int R, int P, int W>
+void launch_moe_down_tile(const MoeArgs& a, hipStream_t stream) {
   const size_t lds = (size_t)W * a.tokens * 16 * R * sizeof(float);
-  hipLaunchKernelGGL((moe_down_kernel<G, MT, R, 2, W, TAIL>), dim3((a.K + 16 * R - 1) / (16 * R)), dim3(64 * W), lds, stream, a);
+  hipLaunchKernelGGL((moe_down_kernel<G, MT, R, P, W>), dim3((a.K + 16 * R - 1) / (16 * R)), dim3(64 * W), lds, stream, a);
+}
+
+// Two column tiles halve the reads of h (64 tokens over 64 experts: 192 us, with
+// one 283 us), unless there are too few columns to give every second compute unit
+// a workgroup then.
+template <int G>
+void launch_moe_down(const MoeArgs& a, hipStream_t stream) {
+  if (many_rows(a)) launch_moe_down_tile<G, 2, 2, 1, 8>(a, stream);
+  else if (a.K < 32 * kCUs / 2) launch_moe_down_tile<G, 1, 1, 1, 8>(a, stream);
+  else if (G == 0 && a.tokens <= 16) launch_moe_down_tile<G, 1, 2, 1, 16>(a, stream);
+  else launch_moe_down_tile<G, 1, 2, 2, 8>(a, stream);
 }
 
 template <int G>
@@ -106,9 +127,7 @@ fg_status launch_moe(const MoeArgs& a, int type, bool grouped, hipStream_t strea
   else if (type == FG_I8) grouped ? launch_moe_up<G, X_I8G>(a, stream) : launch_moe_up<G, X_I8>(a, stream);
   else grouped ? launch_moe_up<G, X_E4M3G>(a, stream) : launch_moe_up<G, X_E4M3>(a, stream);
   HIPCHK_LAUNCH();
-  const bool tail = a.F % kStep != 0;
-  if (a.tokens <= 16) tail ? launch_moe_down<G, 1, 1, true>(a, stream) : launch_moe_down<G, 1, 1, false>(a, stream);
-  else tail ? launch_moe_down<G, 2, 1, true>(a, stream) : launch_moe_down<G, 2, 1, false>(a, stream);
+  launch_moe_down<G>(a, stream);
   HIPCHK_LAUNCH();
   return FG_OK;
 }
@@ -208,7 +227,7 @@ fg_status fg_moe_few(const void* x, int64_t ldx, int32_t x_type, const float* x_
   a.x = (const char*)x; a.xs = x_scale; a.topk = topk; a.weights = weights;
   a.w1 = (const char*)w1; a.s1 = (const uint16_t*)w1_scale; a.z1 = (const uint8_t*)w1_zero;
   a.w2 = (const char*)w2; a.s2 = (const uint16_t*)w2_scale; a.z2 = (const uint8_t*)w2_zero;
-  a.hi = (uint16_t*)workspace; a.lo = a.hi + (int64_t)tokens * k * F;
+  a.h = (char*)workspace; a.plane = 16 * (uint32_t)(tokens * k);
   a.y = (uint16_t*)y;
   a.ldx = ldx * (x_type == FG_BF16 ? 2 : 1); a.xs_stride = x_group ? K / x_group : 1; a.ldy = ldy;
   a.tokens = tokens; a.k = k; a.base = expert_base; a.n_local = n_local; a.K = K; a.F = F;

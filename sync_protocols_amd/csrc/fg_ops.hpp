@@ -69,8 +69,8 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 }
 
 // ------------------------------------------------------------- activations
-// X_SPLIT: two bf16 rows whose sum is the activation (the expert layer's own
-// intermediate, in the element order of paired()); X_I8G, X_E4M3G: 8-bit rows
+// X_SPLIT: two bf16 numbers whose sum is the activation (the expert layer's own
+// intermediate, see SplitRows); X_I8G, X_E4M3G: 8-bit rows
 // with one scale per 128 k, the others have one per row, which the caller
 // applies to the finished sums.
 enum { X_BF16 = FG_BF16, X_I8 = FG_I8, X_E4M3 = FG_E4M3, X_SPLIT = 16, X_I8G = 17, X_E4M3G = 18 };
@@ -119,32 +119,106 @@ __device__ __forceinline__ bf16x8 widen8(u32x2 v) {
   return __builtin_bit_cast(bf16x8, r);
 }
 
-// Where a lane finds its activations: lane l's pointer is that of token
-// 16 m + l % 16 (clamped by the caller to a token that exists; rows of D that
-// belong to no token are never stored). Scales per 128 k: lane l needs those of
-// tokens 4 (l / 16) + 0..3 of each tile, because that is what its sums are.
-template <int KXR, int MT>
-struct XPtr {
-  const char* p[KXR][MT];
+constexpr int kStep = 128;                      // k of a step of the products
+
+// Loads and operands. A matrix instruction wants row l % 16 and k 8 (l / 16) + 0..7
+// in lane l; four lanes next to each other would then read from four rows, and
+// the address unit takes one row's piece per clock, 64 clocks for a load of 1 KB.
+// So lane l loads 16 bytes at 16 (l % 4) of row l / 4, 64 contiguous bytes by four
+// lanes (16 clocks), and ds_bpermute carries every word to the lane that needs it.
+struct Lanes {
+  int lane, quarter;
+  int to_operand;                               // ds_bpermute index: lane 4 (l % 16) + l / 16
+  int to_pairs;                                 // the same with the pieces in the order 0, 2, 1, 3
+  __device__ __forceinline__ Lanes() {
+    lane = threadIdx.x & 63;
+    quarter = lane >> 4;
+    to_operand = 16 * (lane & 15) + 4 * quarter;
+    to_pairs = 16 * (lane & 15) + 4 * (2 * (quarter & 1) + (quarter >> 1));
+  }
+  __device__ __forceinline__ int load_row() const { return lane >> 2; }
+  __device__ __forceinline__ int piece() const { return lane & 3; }
 };
+__device__ __forceinline__ uint32_t from_lane(int index, uint32_t v) { return (uint32_t)__builtin_amdgcn_ds_bpermute(index, (int)v); }
+__device__ __forceinline__ u32x4 from_lane(int index, u32x4 v) {
+  return u32x4{from_lane(index, v[0]), from_lane(index, v[1]), from_lane(index, v[2]), from_lane(index, v[3])};
+}
+__device__ __forceinline__ u32x2 from_lane(int index, u32x2 v) { return u32x2{from_lane(index, v[0]), from_lane(index, v[1])}; }
+
+// Activations of a tile: p[m] is the row that this lane loads from (16 m + l / 4,
+// clamped by the caller to one that exists; rows of D that belong to no token are
+// never stored) and its piece of it. Scales per 128 k: base + at[m] is that of row
+// 16 m + l % 16.
 template <int MT>
-struct XScale {
-  const float* base;
-  uint32_t at[MT][4];
+struct XPtr {
+  const char* p[MT];
+  const float* scale;
+  uint32_t at[MT];
+  uint32_t plane;                               // X_SPLIT: bytes of 8 elements of all rows
+};
+
+// X_SPLIT rows: for every 8 elements the first parts of all rows, 16 bytes each,
+// then the seconds. Rows that are used together lie side by side, so lanes load
+// straight into the operand's places: p[m] is row 16 m + l % 16 at 8 (l / 16).
+// Elements in paired() order for 4-bit weights.
+struct SplitRows {
+  static __device__ __forceinline__ int64_t at(int64_t row, int k, uint32_t plane) {    // bytes to the first part
+    return (int64_t)(k >> 3) * 2 * plane + 16 * row + 2 * (k & 7);
+  }
+};
+
+template <int XK, int MT>
+struct XRows {
+  static constexpr int kXR = XK == X_SPLIT ? 2 : 1;
+  static constexpr bool k8 = x_is_8bit(XK);
+  typedef typename std::conditional<k8, u32x2, u32x4>::type V;      // eight elements
+  V v[kXR][MT][4];
+  // PAIRS: elements 64 (j / 2) + 32 (q % 2) + 16 (q / 2) + 8 (j % 2) in v[..][j], else 32 j + 8 q; those at or past lim: any
+  template <bool PAIRS, bool TAIL>
+  __device__ __forceinline__ void load(const XPtr<MT>& xp, int step, int lim) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int jj = TAIL && (PAIRS ? 64 * (j / 2) : 32 * j) >= lim ? (PAIRS ? j % 2 : 0) : j;
+        if constexpr (XK == X_SPLIT) {
+          const char* p = xp.p[m] + (uint64_t)(16 * (uint32_t)step + 4 * jj) * 2 * xp.plane;
+          v[0][m][j] = *(const u32x4*)p;
+          v[1][m][j] = *(const u32x4*)(p + xp.plane);
+        } else if constexpr (PAIRS) {
+          if (j % 2) continue;
+          const u32x4 t = *(const u32x4_a8*)(xp.p[m] + (int64_t)step * kStep + 32 * jj);
+          v[0][m][j] = u32x2{t[0], t[1]};
+          v[0][m][j + 1] = u32x2{t[2], t[3]};
+        } else {
+          v[0][m][j] = *(const V*)(xp.p[m] + (k8 ? 1 : 2) * ((int64_t)step * kStep + 32 * jj));
+        }
+      }
+  }
+  template <bool PAIRS>
+  __device__ __forceinline__ V get(const Lanes& ln, int r, int m, int j) const {
+    return XK == X_SPLIT ? v[r][m][j] : from_lane(PAIRS ? ln.to_pairs : ln.to_operand, v[r][m][j]);
+  }
 };
 
 // ----------------------------------------------------------------- products
-// One step of a wave is kStep = 128 k of 16 R weight rows; lane l holds row
-// l % 16 of each 16. A weight matrix is a uniform base (Mat) and a 32-bit
-// distance per lane (Row), so that an address costs no vector arithmetic.
-constexpr int kStep = 128;
+// The scale that quarter t's lane of row 4 (l / 16) + i holds.
+__device__ __forceinline__ float row_scale(float v, const Lanes& ln, int t, int i) {
+  return __uint_as_float(from_lane(64 * t + 16 * ln.quarter + 4 * i, __float_as_uint(v)));
+}
+
+// One step of a wave is kStep = 128 k of 16 R weight rows. A weight matrix is a
+// uniform base (Mat) and 32-bit distances per lane (Row), so that an address costs
+// no vector arithmetic. What a step needs besides weights and activations, the
+// scales (Aux), comes for four steps at once: lane quarter t loads those of the
+// t-th of them, for its row l % 16.
 
 // 16-bit weights [rows][K]: four 16-byte loads, each 64 contiguous bytes of a
 // row. 8-bit activations are widened to bf16 (the weights' bytes bound this
 // form, the conversion hides behind them).
 template <int XK, int MT, int R, int P>
 struct Dense {
-  static constexpr int kR = R, kMT = MT, kP = P, kUnit = 32;
+  static constexpr int kR = R, kMT = MT, kP = P;
   static constexpr bool kGrouped = x_grouped(XK);
   static constexpr int kXR = XK == X_SPLIT ? 2 : 1;
   static constexpr bool k8 = x_is_8bit(XK);
@@ -155,42 +229,37 @@ struct Dense {
   };
   struct Row {
     uint32_t w;
-    __device__ __forceinline__ void set(const Mat& m, int row, int q) { w = (uint32_t)row * (uint32_t)m.stride + 16 * q; }
+    // loads of `row`, scales of row `srow`
+    __device__ __forceinline__ void set(const Mat& m, int row, int, const Lanes& ln) {
+      w = (uint32_t)row * (uint32_t)m.stride + 16 * ln.piece();
+    }
   };
-  typedef typename std::conditional<k8, u32x2, u32x4>::type XV;
   struct Stage {
     u32x4 w[R][4];
-    XV x[kXR][MT][4];
-    float xs[MT][4];
+    XRows<XK, MT> x;
+  };
+  struct Aux {
+    float xs[MT];
   };
 
+  static __device__ __forceinline__ void load_aux(Aux& a, const Mat&, const Row (&)[R], const XPtr<MT>& xp, int step, int) {
+    if constexpr (kGrouped) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) a.xs[m] = xp.scale[xp.at[m] + (uint32_t)step];
+    }
+  }
   template <bool TAIL>
-  static __device__ __forceinline__ void load(Stage& st, const Mat& mat, const Row (&rows)[R], const XPtr<kXR, MT>& xp,
-                                              const XScale<MT>& sc, int q, int step, int lim) {
+  static __device__ __forceinline__ void load(Stage& st, const Mat& mat, const Row (&rows)[R], const XPtr<MT>& xp, const Lanes& ln, int step, int lim) {
     const char* base = mat.w + 256 * (int64_t)step;
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int j = 0; j < 4; ++j) st.w[r][j] = *(const u32x4*)(base + rows[r].w + 64 * (TAIL && 32 * j >= lim ? 0 : j));
-#pragma unroll
-    for (int v = 0; v < kXR; ++v)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t k = (int64_t)step * kStep + 32 * (TAIL && 32 * j >= lim ? 0 : j) + 8 * q;
-          st.x[v][m][j] = *(const XV*)(xp.p[v][m] + (k8 ? 1 : 2) * k);
-        }
-    if constexpr (kGrouped) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) st.xs[m][i] = (sc.base + step)[sc.at[m][i]];
-    }
+    st.x.template load<false, TAIL>(xp, step, lim);
   }
 
   template <bool TAIL>
-  static __device__ __forceinline__ void consume(const Stage& st, f32x4 (&acc)[R][MT], int lim) {
+  static __device__ __forceinline__ void consume(const Stage& st, const Aux& aux, int t, f32x4 (&acc)[R][MT], const Lanes& ln, int lim) {
     f32x4 part[R][MT];
     if constexpr (kGrouped) {
 #pragma unroll
@@ -201,27 +270,33 @@ struct Dense {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (TAIL && 32 * j >= lim) break;
+      u32x4 w[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) w[r] = from_lane(ln.to_operand, st.w[r][j]);
 #pragma unroll
       for (int v = 0; v < kXR; ++v)
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
+          const auto xv = st.x.template get<false>(ln, v, m, j);
           bf16x8 x;
-          if constexpr (k8) x = widen8<x_is_i8(XK)>(st.x[v][m][j]);
-          else x = __builtin_bit_cast(bf16x8, st.x[v][m][j]);
+          if constexpr (k8) x = widen8<x_is_i8(XK)>(xv);
+          else x = __builtin_bit_cast(bf16x8, xv);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             f32x4& d = kGrouped ? part[r][m] : acc[r][m];
-            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, __builtin_bit_cast(bf16x8, st.w[r][j]), d, 0, 0, 0);
+            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, __builtin_bit_cast(bf16x8, w[r]), d, 0, 0, 0);
           }
         }
     }
     if constexpr (kGrouped) {
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int i = 0; i < 4; ++i) {
+          const float xs = row_scale(aux.xs[m], ln, t, i);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[r][m][i] = __builtin_fmaf(part[r][m][i], st.xs[m][i], acc[r][m][i]);
+          for (int r = 0; r < R; ++r) acc[r][m][i] = __builtin_fmaf(part[r][m][i], xs, acc[r][m][i]);
+        }
     }
   }
 };
@@ -229,12 +304,13 @@ struct Dense {
 // 4-bit weights [rows][K / 2] (low nibble of a byte first) with one bf16 scale
 // and optionally one zero point per G consecutive k of a row.
 //
-// Layout. A lane loads 16 bytes, 32 consecutive weights, so that a wave's load
-// covers 64 contiguous bytes of 16 rows. A matrix instruction sums over lanes
-// l, l + 16, l + 32, l + 48 and must stay inside one group, for the scale to be
-// applied to its fp32 result: for G = 32 and 64 the words change places between
-// those lanes (two v_permlane*_swap per two words). Word j of lane quarter q then
-// holds k = koff(j, q) + 0..7.
+// Layout. Four lanes load 64 bytes, 128 consecutive weights of a row. When every
+// word is in its row's lanes, lane quarter q holds 32 k, a group or less, but a
+// matrix instruction sums over the quarters and must stay inside one group, for
+// the scale to be applied to its fp32 result: so words change places between
+// lanes l, l + 16, l + 32, l + 48 (v_permlane*_swap) until word j of quarter q
+// holds k = 32 j + 8 q + 0..7, or for 8-bit rows and groups of 64 and 128, where
+// one activation load serves two words, 64 (j / 2) + 32 (q % 2) + 16 (q / 2) + 8 (j % 2).
 //
 // Arithmetic, exact up to the sums, by the activations' type:
 //   bf16: a nibble q becomes the bf16 number 128 + q by one and-or (0x4300 | q),
@@ -250,10 +326,11 @@ struct Dense {
 //     leaves a byte); int32 sums are exact and below 2^24.
 template <int G, int XK, int MT, int R, int P>
 struct Quant4 {
-  static constexpr int kR = R, kMT = MT, kP = P, kUnit = G;
+  static constexpr int kR = R, kMT = MT, kP = P;
   static constexpr bool kGrouped = x_grouped(XK);
   static constexpr int kXR = XK == X_SPLIT ? 2 : 1;
   static constexpr bool k8 = x_is_8bit(XK);
+  static constexpr bool kPairs = k8 && G >= 64;
   static constexpr int kGroups = kStep / G;     // groups of a step
   static constexpr int kWords = G / 32;         // words of a lane in a group
   struct Mat {
@@ -267,92 +344,81 @@ struct Quant4 {
   };
   struct Row {
     uint32_t w, s;
-    __device__ __forceinline__ void set(const Mat& m, int row, int q) {
-      w = (uint32_t)row * (uint32_t)m.stride + 16 * q;
-      s = (uint32_t)row * (uint32_t)m.gstride;
+    __device__ __forceinline__ void set(const Mat& m, int row, int srow, const Lanes& ln) {
+      w = (uint32_t)row * (uint32_t)m.stride + 16 * ln.piece();
+      s = (uint32_t)srow * (uint32_t)m.gstride;
     }
   };
   struct Stage {
     u32x4 w[R];
-    uint32_t s[R][(kGroups + 1) / 2], z[R];     // bf16 pairs, bytes
-    u32x4 x[kXR][MT][k8 ? 2 : 4];
-    float xs[MT][4];
+    XRows<XK, MT> x;
   };
-  static __device__ __forceinline__ int koff(int j, int q) {
-    return G == 128 ? 32 * q + 8 * j : G == 64 ? 64 * (j / 2) + 8 * (j % 2) + 32 * (q % 2) + 16 * (q / 2) : 32 * j + 8 * q;
-  }
+  struct Aux {
+    uint32_t s[R][(kGroups + 1) / 2], z[R];     // bf16 pairs, bytes
+    float xs[MT];
+  };
 
-  template <bool TAIL>
-  static __device__ __forceinline__ void load(Stage& st, const Mat& mat, const Row (&rows)[R], const XPtr<kXR, MT>& xp,
-                                              const XScale<MT>& sc, int q, int step, int lim) {
-    const char* base = mat.w + 64 * (int64_t)step;
-    const int64_t g0 = (int64_t)step * kGroups;
+  // lim: k of the step that exist; scales of the others are not read
+  static __device__ __forceinline__ void load_aux(Aux& a, const Mat& mat, const Row (&rows)[R], const XPtr<MT>& xp, int step, int lim) {
+    const uint32_t g0 = (uint32_t)step * kGroups;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      // past the end of a row: the last 32 weights again, in groups that are not used
-      const uint32_t back = TAIL && 32 * q >= lim ? 16 * (q + 1) - lim / 2 : 0;
-      st.w[r] = *(const u32x4*)(base + (rows[r].w - back));
-      const char* sp = (const char*)(mat.s + g0) + 2 * (uint64_t)rows[r].s;
-      if constexpr (TAIL) {
+      const uint16_t* sp = mat.s + (rows[r].s + (uint64_t)g0);
+      const uint8_t* zp = mat.z + (rows[r].s + (uint64_t)g0);
+      a.z[r] = 0x08080808u;
+      if (lim < kStep) {
 #pragma unroll
-        for (int i = 0; i < (kGroups + 1) / 2; ++i) st.s[r][i] = 0;
-        st.z[r] = 0;
+        for (int i = 0; i < (kGroups + 1) / 2; ++i) a.s[r][i] = 0;
 #pragma unroll
         for (int h = 0; h < kGroups; ++h) {
           if (G * h >= lim) break;
-          st.s[r][h / 2] |= (uint32_t)((const uint16_t*)sp)[h] << (16 * (h % 2));
-          st.z[r] |= (mat.z ? (uint32_t)mat.z[g0 + h + rows[r].s] : 8u) << (8 * h);
+          a.s[r][h / 2] |= (uint32_t)sp[h] << (16 * (h % 2));
+        }
+        if (mat.z) {
+          a.z[r] = 0;
+#pragma unroll
+          for (int h = 0; h < kGroups; ++h) {
+            if (G * h >= lim) break;
+            a.z[r] |= (uint32_t)zp[h] << (8 * h);
+          }
         }
       } else {
         if constexpr (kGroups == 4) {
           const u32x2 v = *(const u32x2_a1*)sp;
-          st.s[r][0] = v[0]; st.s[r][1] = v[1];
+          a.s[r][0] = v[0]; a.s[r][1] = v[1];
+          if (mat.z) a.z[r] = *(const u32_a1*)zp;
         } else if constexpr (kGroups == 2) {
-          st.s[r][0] = *(const u32_a1*)sp;
+          a.s[r][0] = *(const u32_a1*)sp;
+          if (mat.z) a.z[r] = *(const u16_a1*)zp;
         } else {
-          st.s[r][0] = *(const uint16_t*)sp;
-        }
-        st.z[r] = 0x08080808u;
-        if (mat.z) {
-          const uint8_t* zp = mat.z + g0 + rows[r].s;
-          if constexpr (kGroups == 4) st.z[r] = *(const u32_a1*)zp;
-          else if constexpr (kGroups == 2) st.z[r] = *(const u16_a1*)zp;
-          else st.z[r] = *zp;
+          a.s[r][0] = *sp;
+          if (mat.z) a.z[r] = *zp;
         }
       }
+      if constexpr (kGroups == 1) a.s[r][0] = a.s[r][0] << 16 | (a.z[r] & 0xffu);      // one word carries both
     }
-#pragma unroll
-    for (int v = 0; v < kXR; ++v)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int jj = TAIL && (j / kWords) * G >= lim ? j % kWords : j;
-          const char* p = xp.p[v][m] + (k8 ? 1 : 2) * ((int64_t)step * kStep + koff(jj, q));
-          if constexpr (!k8) {
-            st.x[v][m][j] = *(const u32x4*)p;
-          } else if (G == 32) {                // eight bytes a word; else two words are neighbours
-            const u32x2 t = *(const u32x2*)p;
-            st.x[v][m][j / 2][2 * (j % 2)] = t[0];
-            st.x[v][m][j / 2][2 * (j % 2) + 1] = t[1];
-          } else if (j % 2 == 0) {
-            st.x[v][m][j / 2] = *(const u32x4_a8*)p;
-          }
-        }
     if constexpr (kGrouped) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) st.xs[m][i] = (sc.base + step)[sc.at[m][i]];
+      for (int m = 0; m < MT; ++m) a.xs[m] = xp.scale[xp.at[m] + (uint32_t)step];
     }
   }
 
-  // The words of a lane, group by group.
-  static __device__ __forceinline__ u32x4 gather(u32x4 w) {
-    if constexpr (G == 128) return w;
+  template <bool TAIL>
+  static __device__ __forceinline__ void load(Stage& st, const Mat& mat, const Row (&rows)[R], const XPtr<MT>& xp, const Lanes& ln, int step, int lim) {
+    const char* base = mat.w + 64 * (int64_t)step;
+    // past the end of a row: its last 32 weights again, in groups that are not used
+    const int piece = ln.piece();
+    const uint32_t back = TAIL && 32 * piece >= lim ? 16 * (piece + 1) - lim / 2 : 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) st.w[r] = *(const u32x4*)(base + (rows[r].w - back));
+    st.x.template load<kPairs, TAIL>(xp, step, lim);
+  }
+
+  static __device__ __forceinline__ u32x4 gather(u32x4 v, const Lanes& ln) {
+    const u32x4 w = from_lane(ln.to_operand, v);
     const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
     const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-    if constexpr (G == 64) return u32x4{a[0], b[0], a[1], b[1]};
+    if constexpr (kPairs) return u32x4{a[0], b[0], a[1], b[1]};
     const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
     const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
     return u32x4{c[0], c[1], d[0], d[1]};
@@ -367,10 +433,25 @@ struct Quant4 {
   static __device__ __forceinline__ long as_long(u32x2 v) { return __builtin_bit_cast(long, v); }
 
   template <bool TAIL>
-  static __device__ __forceinline__ void consume(const Stage& st, f32x4 (&acc)[R][MT], int lim) {
+  static __device__ __forceinline__ void consume(const Stage& st, const Aux& aux, int t, f32x4 (&acc)[R][MT], const Lanes& ln, int lim) {
     u32x4 w[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) w[r] = gather(st.w[r]);
+    for (int r = 0; r < R; ++r) w[r] = gather(st.w[r], ln);
+    const int row = 64 * t + 4 * (ln.lane & 15);          // quarter t's lane of this lane's weight row
+    uint32_t sw[R][(kGroups + 1) / 2], zw[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int i = 0; i < (kGroups + 1) / 2; ++i) sw[r][i] = from_lane(row, aux.s[r][i]);
+      zw[r] = kGroups == 1 ? sw[r][0] : from_lane(row, aux.z[r]);
+    }
+    f32x4 xs[MT];
+    if constexpr (kGrouped) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xs[m][i] = row_scale(aux.xs[m], ln, t, i);
+    }
 #pragma unroll
     for (int h = 0; h < kGroups; ++h) {
       if (TAIL && G * h >= lim) break;
@@ -387,14 +468,16 @@ struct Quant4 {
         for (int m = 0; m < MT; ++m) {
           const int j = h * kWords + f;
           if constexpr (k8) {
-            x8[m][f] = even_odd(st.x[0][m][j / 2][2 * (j % 2)], st.x[0][m][j / 2][2 * (j % 2) + 1]);
+            const u32x2 v = st.x.template get<kPairs>(ln, 0, m, j);
+            x8[m][f] = even_odd(v[0], v[1]);
             if constexpr (x_is_e4m3(XK))
               sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(as_long(x8[m][f]), 0x3838383838383838l, sum[m], 0, 0, 0);
           } else {
             const u32x4 one = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
 #pragma unroll
             for (int v = 0; v < kXR; ++v) {
-              x16[v][m][f] = XK == X_SPLIT ? st.x[v][m][j] : paired(st.x[v][m][j]);
+              x16[v][m][f] = st.x.template get<false>(ln, v, m, j);
+              if constexpr (XK != X_SPLIT) x16[v][m][f] = paired(x16[v][m][f]);
               sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x16[v][m][f]),
                                                                __builtin_bit_cast(bf16x8, one), sum[m], 0, 0, 0);
             }
@@ -402,8 +485,8 @@ struct Quant4 {
         }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const uint32_t sw = st.s[r][h / 2], z = (st.z[r] >> (8 * h)) & 0xffu;
-        float s = h % 2 ? bf16_hi(sw) : bf16_lo(sw);
+        const uint32_t z = (zw[r] >> (8 * h)) & 0xffu;
+        float s = kGroups == 1 || h % 2 ? bf16_hi(sw[r][h / 2]) : bf16_lo(sw[r][h / 2]);
         f32x4 part[MT];
         if constexpr (x_is_i8(XK)) {
           const uint32_t up = 0x80808080u - z * 0x01010101u;
@@ -461,7 +544,7 @@ struct Quant4 {
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            acc[r][m][i] = __builtin_fmaf(part[m][i], kGrouped ? s * st.xs[m][i] : s, acc[r][m][i]);
+            acc[r][m][i] = __builtin_fmaf(part[m][i], kGrouped ? s * xs[m][i] : s, acc[r][m][i]);
         // one row tile and group at a time: all of them at once would not fit in the registers
         if constexpr (MT > 1) __builtin_amdgcn_sched_barrier(0);
       }
@@ -470,38 +553,53 @@ struct Quant4 {
   }
 };
 
-// acc[r][m] += products over the steps first, first + by, ... < n_steps of 128 k
-// and, if `tail` (0..127, a multiple of the weights' unit) is not 0 and this wave
-// owns the step after the last full one, over the tail.
-// P steps are kept in flight in registers.
+// acc[r][m] += products over the n steps first, first + by, ... of 128 k. P steps
+// are kept in flight in registers, the scales of four more.
 template <class Prod>
 __device__ __forceinline__ void run_steps(f32x4 (&acc)[Prod::kR][Prod::kMT], const typename Prod::Mat& mat,
-                                          const typename Prod::Row (&rows)[Prod::kR], const XPtr<Prod::kXR, Prod::kMT>& xp,
-                                          const XScale<Prod::kMT>& sc, int q, int first, int by, int n_steps, int tail) {
+                                          const typename Prod::Row (&rows)[Prod::kR], const XPtr<Prod::kMT>& xp, const Lanes& ln,
+                                          int first, int by, int n) {
   constexpr int P = Prod::kP;
-  const int n = first < n_steps ? (n_steps - first + by - 1) / by : 0;
-  if (n > 0) {
-    typename Prod::Stage st[P];
+  static_assert(P == 1 || P == 2 || P == 4, "stages");
+  if (n <= 0) return;
+  typename Prod::Stage st[P];
+  typename Prod::Aux cur, nxt;
+  auto aux = [&](typename Prod::Aux& a, int i) { Prod::load_aux(a, mat, rows, xp, first + by * min(i + ln.quarter, n - 1), kStep); };
+  aux(cur, 0);
 #pragma unroll
-    for (int p = 0; p < P; ++p) Prod::template load<false>(st[p], mat, rows, xp, sc, q, first + by * (p < n ? p : n - 1), kStep);
-    int i = 0;
-    for (; i + P < n; i += P) {
+  for (int p = 0; p < P; ++p)
+    if (p < n) Prod::template load<false>(st[p], mat, rows, xp, ln, first + by * p, kStep);
+  int i = 0;
+  for (; i + 4 + P <= n; i += 4) {      // no branches in here: the compiler's waits count the loads in flight
+    aux(nxt, i + 4);
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        Prod::template consume<false>(st[p], acc, kStep);
-        const int nx = i + P + p;
-        Prod::template load<false>(st[p], mat, rows, xp, sc, q, first + by * (nx < n ? nx : n - 1), kStep);
-      }
+    for (int t = 0; t < 4; ++t) {
+      Prod::template consume<false>(st[t % P], cur, t, acc, ln, kStep);
+      Prod::template load<false>(st[t % P], mat, rows, xp, ln, first + by * (i + t + P), kStep);
     }
+    cur = nxt;
+  }
+  for (; i < n; i += 4) {
+    if (i + 4 < n) aux(nxt, i + 4);
 #pragma unroll
-    for (int p = 0; p < P; ++p)
-      if (i + p < n) Prod::template consume<false>(st[p], acc, kStep);
+    for (int t = 0; t < 4; ++t) {
+      if (i + t >= n) break;
+      Prod::template consume<false>(st[t % P], cur, t, acc, ln, kStep);
+      if (i + t + P < n) Prod::template load<false>(st[t % P], mat, rows, xp, ln, first + by * (i + t + P), kStep);
+    }
+    cur = nxt;
   }
-  if (tail && n_steps % by == first) {
-    typename Prod::Stage st;
-    Prod::template load<true>(st, mat, rows, xp, sc, q, n_steps, tail);
-    Prod::template consume<true>(st, acc, tail);
-  }
+}
+// The same for the last `lim` < 128 k of the rows, which are those of `step`.
+template <class Prod>
+__device__ __forceinline__ void run_tail(f32x4 (&acc)[Prod::kR][Prod::kMT], const typename Prod::Mat& mat,
+                                         const typename Prod::Row (&rows)[Prod::kR], const XPtr<Prod::kMT>& xp, const Lanes& ln,
+                                         int step, int lim) {
+  typename Prod::Stage st;
+  typename Prod::Aux aux;
+  Prod::load_aux(aux, mat, rows, xp, step, lim);
+  Prod::template load<true>(st, mat, rows, xp, ln, step, lim);
+  Prod::template consume<true>(st, aux, 0, acc, ln, lim);
 }
 
 template <class Prod>
@@ -510,6 +608,12 @@ __device__ __forceinline__ void clear(f32x4 (&acc)[Prod::kR][Prod::kMT]) {
   for (int r = 0; r < Prod::kR; ++r)
 #pragma unroll
     for (int m = 0; m < Prod::kMT; ++m) acc[r][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+}
+
+// Bytes to the piece of an activation row that a lane loads.
+template <int G, int XK>
+__device__ __forceinline__ int x_piece(const Lanes& ln) {
+  return !x_is_8bit(XK) || G >= 64 ? 16 * ln.piece() : 8 * ln.piece();
 }
 
 // Which product serves weights of group size G (0: 16-bit).

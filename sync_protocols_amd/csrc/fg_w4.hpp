@@ -43,26 +43,28 @@ template <int G, int XK, int MT, int R, int P, int W>
 __global__ __launch_bounds__(64 * W) void w4_linear_kernel(W4Args a) {
   __shared__ float red[W * 16 * (16 * R + 1)];
   typedef Quant4<G, XK, MT, R, P> Prod;
-  const int lane = threadIdx.x & 63, q = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Lanes ln;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = blockIdx.x * 16 * R, t0 = blockIdx.y * 16 * MT;
   const typename Prod::Mat mat = typename Prod::Mat{a.w, a.s, a.z, a.k / 2, a.k / G}.at(n0);
   typename Prod::Row rows[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) rows[r].set(mat, min(16 * r + (lane & 15), a.n - 1 - n0), q);
-  XPtr<1, MT> xp;
-  XScale<MT> sc;
-  sc.base = a.xs + t0 * a.xs_stride;
+  for (int r = 0; r < R; ++r) {
+    const int last = a.n - 1 - n0;
+    rows[r].set(mat, min(16 * r + ln.load_row(), last), min(16 * r + (ln.lane & 15), last), ln);
+  }
+  XPtr<MT> xp;
+  xp.scale = a.xs + t0 * a.xs_stride;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    xp.p[0][m] = a.x + (int64_t)min(t0 + 16 * m + (lane & 15), a.rows - 1) * a.ldx;
-    if constexpr (Prod::kGrouped) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sc.at[m][i] = (uint32_t)min(16 * m + 4 * q + i, a.rows - 1 - t0) * (uint32_t)a.xs_stride;
-    }
+    xp.p[m] = a.x + (int64_t)min(t0 + 16 * m + ln.load_row(), a.rows - 1) * a.ldx + x_piece<G, XK>(ln);
+    xp.at[m] = (uint32_t)min(16 * m + (ln.lane & 15), a.rows - 1 - t0) * (uint32_t)a.xs_stride;
   }
   f32x4 acc[R][MT];
   clear<Prod>(acc);
-  run_steps<Prod>(acc, mat, rows, xp, sc, q, wave, W, a.k / kStep, a.k % kStep);
+  const int steps = a.k / kStep;
+  run_steps<Prod>(acc, mat, rows, xp, ln, wave, W, (steps - wave + W - 1) / W);
+  if (a.k % kStep && steps % W == wave) run_tail<Prod>(acc, mat, rows, xp, ln, steps, a.k % kStep);
 #pragma unroll
   for (int m = 0; m < MT; ++m)
     join_tile<R, MT, W>(acc, m, red, [&](int tok, int col, float v) {
