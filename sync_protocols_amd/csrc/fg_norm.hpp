@@ -19,6 +19,7 @@ struct NormArgs {
   int32_t n, group;             // group: 0 (row) or 128
   int32_t q_type;
   float eps;
+  int32_t past;                 // outputs are larger than the caches: store past them
 };
 
 // Eight elements at p, `left` of them valid.
@@ -32,12 +33,13 @@ __device__ __forceinline__ void load8(const uint16_t* p, int left, float (&f)[8]
     for (int i = 0; i < 8; ++i) f[i] = i < left ? bf16_f(p[i]) : 0.0f;
   }
 }
-__device__ __forceinline__ void store8(uint16_t* p, int left, const float (&f)[8]) {
+__device__ __forceinline__ void store8(uint16_t* p, int left, int past, const float (&f)[8]) {
   if (left >= 8) {
     u32x4 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = f2_bf16(f[2 * i], f[2 * i + 1]);
-    *(u32x4_a2*)p = v;
+    if (past) __builtin_nontemporal_store(v, (u32x4_a2*)p);
+    else *(u32x4_a2*)p = v;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -49,7 +51,7 @@ __device__ __forceinline__ void store8(uint16_t* p, int left, const float (&f)[8
 // is used once per row, so one barrier per reduction is enough.
 template <int W>
 __device__ __forceinline__ float row_sum(float v, float* buf) {
-  v = wave_sum(v);
+  v = lanes_sum(v);
   if constexpr (W > 1) {
     if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -61,7 +63,7 @@ __device__ __forceinline__ float row_sum(float v, float* buf) {
 }
 template <int W>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* buf) {
-  v = wave_max(v);
+  v = lanes_max(v);
   if constexpr (W > 1) {
     if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -97,7 +99,8 @@ __device__ __forceinline__ void quantise8(const NormArgs& a, int64_t row, int e,
   }
   uint8_t* p = a.q + row * a.ldq + e;
   if (left >= 8) {
-    *(u32x2_a1*)p = v;
+    if (a.past) __builtin_nontemporal_store(v, (u32x2_a1*)p);
+    else *(u32x2_a1*)p = v;
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -105,16 +108,24 @@ __device__ __forceinline__ void quantise8(const NormArgs& a, int64_t row, int e,
   }
 }
 
-// One workgroup of W waves per row; thread t holds elements 8 (t + 64 W i) + 0..7.
+// W waves per row; thread t of them holds elements 8 (t + 64 W i) + 0..7. Workgroups
+// of one row, or of four where a wave has one to itself.
 // The maximum is taken over the bit patterns of |y| as integers: their order is
 // that of the numbers, and a NaN counts as larger than infinity, so that it
 // reaches the scale instead of being dropped.
+template <int W>
+struct NormShape {
+  static constexpr int kRows = W == 1 ? 4 : 1;
+  static constexpr int kThreads = 64 * W * kRows;
+};
 template <int W, int V>
-__global__ __launch_bounds__(64 * W) void add_rmsnorm_kernel(NormArgs a) {
+__global__ __launch_bounds__(NormShape<W>::kThreads) void add_rmsnorm_kernel(NormArgs a) {
   __shared__ float sbuf[W];
   __shared__ uint32_t mbuf[W];
-  const int64_t row = blockIdx.x;
-  const int t = threadIdx.x;
+  const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  const int64_t row = W == 1 ? 4 * block + (threadIdx.x >> 6) : block;
+  if (row >= a.rows) return;               // the same for all waves of a row
+  const int t = W == 1 ? threadIdx.x & 63 : threadIdx.x;
   float h[V][8];
   float ss = 0.0f;
 #pragma unroll
@@ -144,12 +155,12 @@ __global__ __launch_bounds__(64 * W) void add_rmsnorm_kernel(NormArgs a) {
     const int e = 8 * (t + 64 * W * i);
     const int left = a.n - e;
     if (left > 0) {
-      if (a.sum) store8(a.sum + row * a.lds + e, left, h[i]);
+      if (a.sum) store8(a.sum + row * a.lds + e, left, a.past, h[i]);
       float g[8];
       load8(a.gamma + e, left, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * rstd * g[j];
-      if (a.y) store8(a.y + row * a.ldy + e, left, h[i]);
+      if (a.y) store8(a.y + row * a.ldy + e, left, a.past, h[i]);
       if (!a.q) continue;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -160,11 +171,7 @@ __global__ __launch_bounds__(64 * W) void add_rmsnorm_kernel(NormArgs a) {
     }
     if (a.q && a.group) {
       // 16 lanes hold one group of 128 columns (n is a multiple of 128)
-#pragma unroll
-      for (int d = 1; d < 16; d <<= 1) {
-        const uint32_t o = __shfl_xor(amax, d);
-        amax = o > amax ? o : amax;
-      }
+      amax = lanes_max<16>(amax);
     }
     if (a.q && a.group && left > 0) {
       const float m = __uint_as_float(amax), top = a.q_type == FG_I8 ? 127.0f : 448.0f;

@@ -53,19 +53,40 @@ __device__ __forceinline__ uint32_t f2_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// Reductions over the 64 lanes of a wave; every lane gets the result.
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  return v;
-}
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t o = __shfl_xor(v, d);
-    v = v > o ? v : o;
+// Reductions over L = 16 neighbouring lanes or all 64 of a wave; every lane gets
+// the result. Within 16 lanes by rotations in the instruction itself, then by lane
+// swaps: a tenth of the latency of going through LDS.
+template <int L, class T, class Op>
+__device__ __forceinline__ T lanes_reduce(T v, Op op) {
+  static_assert(L == 16 || L == 64, "lanes");
+  auto turned = [](T x, auto ctrl) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, 0xf, 0xf, false));
+  };
+  v = op(v, turned(v, std::integral_constant<int, 0x128>()));      // row_ror:8
+  v = op(v, turned(v, std::integral_constant<int, 0x124>()));
+  v = op(v, turned(v, std::integral_constant<int, 0x122>()));
+  v = op(v, turned(v, std::integral_constant<int, 0x121>()));
+  if constexpr (L == 64) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    v = op(__builtin_bit_cast(T, (uint32_t)a[0]), __builtin_bit_cast(T, (uint32_t)a[1]));
+    const uint32_t w = __builtin_bit_cast(uint32_t, v);
+    const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    v = op(__builtin_bit_cast(T, (uint32_t)b[0]), __builtin_bit_cast(T, (uint32_t)b[1]));
   }
   return v;
+}
+template <int L = 64>
+__device__ __forceinline__ float lanes_sum(float v) {
+  return lanes_reduce<L>(v, [](float a, float b) { return a + b; });
+}
+template <int L = 64>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  return lanes_reduce<L>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+template <int L = 64>
+__device__ __forceinline__ uint32_t lanes_min(uint32_t v) {
+  return lanes_reduce<L>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
 }
 
 // ------------------------------------------------------------- activations

@@ -32,65 +32,96 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return k == 1u ? -__builtin_inff() : __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-// One wave per token; lane l holds logits l * EPL + 0..EPL-1, so that the lowest
-// lane with the maximum and the lowest of its elements are the lowest index.
-template <int EPL, bool BF16>
-__global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= a.rows) return;
-  uint32_t key[EPL];
-  float v[EPL];
+// N consecutive logits of which `left` exist, in one load where they all do (rows
+// need no more than element alignment); the others count as taken.
+template <int N, bool BF16>
+__device__ __forceinline__ void load_logits(const char* p, int left, uint32_t (&key)[N], float (&v)[N]) {
+  constexpr int kBytes = BF16 ? 2 : 4, kWords = N * kBytes / 4 ? N * kBytes / 4 : 1;
+  float x[N];
+  if (N * kBytes >= 4 && left >= N) {
+    uint32_t w[kWords];
+    __builtin_memcpy(w, p, sizeof w);
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const int e = lane * EPL + j;
-    key[j] = 0;
-    v[j] = -__builtin_inff();
-    if (e < a.experts) {
-      const float x = BF16 ? bf16_f(((const uint16_t*)a.logits)[row * a.ld + e]) : ((const float*)a.logits)[row * a.ld + e];
-      key[j] = order_key(x);
-      v[j] = x == x ? x : -__builtin_inff();
-    }
+    for (int j = 0; j < N; ++j) x[j] = BF16 ? (j % 2 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2])) : __uint_as_float(w[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = j >= left ? 0.0f : BF16 ? bf16_f(((const uint16_t*)p)[j]) : ((const float*)p)[j];
   }
-  uint32_t best = 0;
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) best = key[j] > best ? key[j] : best;
-  uint32_t top = wave_max(best);
+  for (int j = 0; j < N; ++j) {
+    key[j] = j < left ? order_key(x[j]) : 0;
+    v[j] = j < left && x[j] == x[j] ? x[j] : -__builtin_inff();
+  }
+}
+
+// L lanes per token; lane l of them holds logits l * N + 0..N-1. A pick is the
+// largest key of the lanes' largest and then the lowest index among those equal to
+// it. 16 lanes with up to 16 logits each need the fewest instructions (8192 tokens,
+// 256 experts, 8 picks: 6.7 us; with 64 lanes of 4 logits 11.8 us); more experts take 64 lanes.
+// Lane j % 16 keeps the j-th pick, so that scores are computed once, side by side.
+template <int L, int N, bool BF16>
+__global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {
+  const int l = threadIdx.x % L, l16 = threadIdx.x & 15;
+  const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (256 / L) + threadIdx.x / L;
+  if (row >= a.rows) return;               // whole groups of lanes: reductions stay among those that are left
+  const int e0 = l * N;
+  uint32_t key[N];
+  float v[N];
+  load_logits<N, BF16>((const char*)a.logits + (row * a.ld + e0) * (BF16 ? 2 : 4), a.experts - e0, key, v);
+  uint32_t best, at;
+  auto find_best = [&]() {
+    best = key[0];
+    at = e0;
+#pragma unroll
+    for (int i = 1; i < N; ++i) {
+      at = key[i] > best ? e0 + i : at;
+      best = key[i] > best ? key[i] : best;
+    }
+  };
+  find_best();
+  uint32_t top = lanes_max<L>(best);
   float m = 0.0f, denom = 1.0f;
   if (a.score == FG_SCORE_SOFTMAX) {
     m = key_value(top);
     float s = 0.0f;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) s += v[j] == -__builtin_inff() ? 0.0f : expf(v[j] - m);
-    denom = wave_sum(s);
+    for (int j = 0; j < N; ++j) s += v[j] == -__builtin_inff() ? 0.0f : expf(v[j] - m);
+    denom = lanes_sum<L>(s);
   }
-  float mine = 0.0f;        // lane j: score of the j-th pick
-  int32_t mine_e = 0;
-  float total = 0.0f;
-  for (int j = 0; j < a.k; ++j) {
-    const int owner = __ffsll((unsigned long long)__ballot(best == top)) - 1;
-    int at = 0;
+  constexpr int kKept = 4;                 // 64 picks over 16 lanes
+  uint32_t kept[kKept], kept_e[kKept];
 #pragma unroll
-    for (int i = EPL - 1; i >= 0; --i) at = key[i] == top ? i : at;
-    const int e = __shfl(lane * EPL + at, owner);
-    const float l = key_value(top);
-    float p = 0.0f;
-    if (l != -__builtin_inff()) p = a.score == FG_SCORE_SOFTMAX ? expf(l - m) / denom : 1.0f / (1.0f + expf(-l));
-    total += p;
-    if (lane == j) { mine = p; mine_e = e; }
-    if (lane == owner) {
+  for (int g = 0; g < kKept; ++g) {
+    kept[g] = 1;
+    for (int j = 16 * g; j < min(a.k, 16 * g + 16); ++j) {
+      const uint32_t e = lanes_min<L>(best == top ? at : 0xffffffffu);
+      if (l16 == j % 16) {
+        kept[g] = top;
+        kept_e[g] = e;
+      }
 #pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (i == at) key[i] = 0;
-      best = 0;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) best = key[i] > best ? key[i] : best;
+      for (int i = 0; i < N; ++i) key[i] = e == (uint32_t)(e0 + i) ? 0 : key[i];
+      find_best();
+      top = lanes_max<L>(best);
     }
-    top = wave_max(best);
   }
-  if (lane < a.k) {
-    a.topk[row * a.k + lane] = mine_e;
-    a.weights[row * a.k + lane] = a.renorm ? (total == 0.0f ? 0.0f : mine / total * a.scale) : mine * a.scale;
+  float p[kKept], total = 0.0f;
+#pragma unroll
+  for (int g = 0; g < kKept; ++g) {
+    const float x = key_value(kept[g]);
+    p[g] = 0.0f;
+    if (16 * g < a.k && x != -__builtin_inff())
+      p[g] = a.score == FG_SCORE_SOFTMAX ? expf(x - m) / denom : 1.0f / (1.0f + expf(-x));
+    total += p[g];
+  }
+  total = lanes_sum<16>(total);
+  if (l >= 16) return;
+#pragma unroll
+  for (int g = 0; g < kKept; ++g) {
+    const int j = 16 * g + l;
+    if (j >= a.k) break;
+    a.topk[row * a.k + j] = (int32_t)kept_e[g];
+    a.weights[row * a.k + j] = a.renorm ? (total == 0.0f ? 0.0f : p[g] / total * a.scale) : p[g] * a.scale;
   }
 }
 
