@@ -55,10 +55,11 @@ __device__ __forceinline__ void moe_up_pass(const MoeArgs& a, int e, int f0, con
     rows[C + c].set(mat, a.F + f, a.F + sf, ln);
   }
   XPtr<MT> xp;
+  xp.base = a.x;
   xp.scale = a.xs;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    xp.p[m] = a.x + (int64_t)(list[min(s0 + 16 * m + ln.load_row(), cnt - 1)] / a.k) * a.ldx + x_piece<G, XK>(ln);
+    xp.row[m] = (uint32_t)(list[min(s0 + 16 * m + ln.load_row(), cnt - 1)] / a.k) * (uint32_t)a.ldx + x_piece<G, XK>(ln);
     xp.at[m] = (uint32_t)(list[min(s0 + 16 * m + (ln.lane & 15), cnt - 1)] / a.k) * (uint32_t)a.xs_stride;
   }
   f32x4 acc[2 * C][MT];
@@ -236,6 +237,7 @@ __global__ __launch_bounds__(64 * W) void moe_down_kernel(MoeArgs a) {
     rows[r].set(all, min(16 * r + ln.load_row(), last), min(16 * r + col, last), ln);
   }
   XPtr<MT> xp;
+  xp.base = a.h;
   xp.plane = a.plane;
   int ent = (int)(from / steps), step = (int)(from % steps);
   for (int64_t left = to - from; left > 0; ++ent, step = 0) {
@@ -243,7 +245,7 @@ __global__ __launch_bounds__(64 * W) void moe_down_kernel(MoeArgs a) {
     const typename Prod::Mat mat = all.at((int64_t)__builtin_amdgcn_readfirstlane(pl.ent_e[ent]) * a.K);
 #pragma unroll
     for (int m = 0; m < MT; ++m)                   // past the entry: its last row, whose results are not used again
-      xp.p[m] = a.h + SplitRows::at(s + min(16 * m + col, c - 1), 8 * ln.quarter, a.plane);
+      xp.row[m] = (uint32_t)SplitRows::at(s + min(16 * m + col, c - 1), 8 * ln.quarter, a.plane);
     const int end = steps - step < left ? steps : step + (int)left;
     left -= end - step;
     f32x4 acc[R][MT];

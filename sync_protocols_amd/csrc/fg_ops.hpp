@@ -166,13 +166,15 @@ __device__ __forceinline__ u32x4 from_lane(int index, u32x4 v) {
 }
 __device__ __forceinline__ u32x2 from_lane(int index, u32x2 v) { return u32x2{from_lane(index, v[0]), from_lane(index, v[1])}; }
 
-// Activations of a tile: p[m] is the row that this lane loads from (16 m + l / 4,
-// clamped by the caller to one that exists; rows of D that belong to no token are
-// never stored) and its piece of it. Scales per 128 k: base + at[m] is that of row
-// 16 m + l % 16.
+// Activations of a tile: base + row[m] is the row that this lane loads from (16 m +
+// l / 4, clamped by the caller to one that exists; rows of D that belong to no token
+// are never stored) and its piece of it. The base is uniform and the rest of an
+// address 32 bits, as for the weights. Scales per 128 k: scale + at[m] is that of
+// row 16 m + l % 16.
 template <int MT>
 struct XPtr {
-  const char* p[MT];
+  const char* base;
+  uint32_t row[MT];
   const float* scale;
   uint32_t at[MT];
   uint32_t plane;                               // X_SPLIT: bytes of 8 elements of all rows
@@ -180,7 +182,7 @@ struct XPtr {
 
 // X_SPLIT rows: for every 8 elements the first parts of all rows, 16 bytes each,
 // then the seconds. Rows that are used together lie side by side, so lanes load
-// straight into the operand's places: p[m] is row 16 m + l % 16 at 8 (l / 16).
+// straight into the operand's places: row[m] is row 16 m + l % 16 at 8 (l / 16).
 // Elements in paired() order for 4-bit weights.
 struct SplitRows {
   static __device__ __forceinline__ int64_t at(int64_t row, int k, uint32_t plane) {    // bytes to the first part
@@ -188,35 +190,37 @@ struct SplitRows {
   }
 };
 
-template <int XK, int MT>
+template <int XK, int MT, bool PAIRS>
 struct XRows {
   static constexpr int kXR = XK == X_SPLIT ? 2 : 1;
   static constexpr bool k8 = x_is_8bit(XK);
   typedef typename std::conditional<k8, u32x2, u32x4>::type V;      // eight elements
   V v[kXR][MT][4];
-  // PAIRS: elements 64 (j / 2) + 32 (q % 2) + 16 (q / 2) + 8 (j % 2) in v[..][j], else 32 j + 8 q; those at or past lim: any
-  template <bool PAIRS, bool TAIL>
-  __device__ __forceinline__ void load(const XPtr<MT>& xp, int step, int lim) {
+  // Elements 64 (j / 2) + 32 (q % 2) + 16 (q / 2) + 8 (j % 2) of the step (PAIRS; one load for two j) or 32 j + 8 q
+  // into v[..][j]; those at or past lim: any.
+  template <bool TAIL>
+  __device__ __forceinline__ void load(int j, const XPtr<MT>& xp, int step, int lim) {
+    const int jj = TAIL && (PAIRS ? 64 * (j / 2) : 32 * j) >= lim ? 0 : j;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int jj = TAIL && (PAIRS ? 64 * (j / 2) : 32 * j) >= lim ? (PAIRS ? j % 2 : 0) : j;
-        if constexpr (XK == X_SPLIT) {
-          const char* p = xp.p[m] + (uint64_t)(16 * (uint32_t)step + 4 * jj) * 2 * xp.plane;
-          v[0][m][j] = *(const u32x4*)p;
-          v[1][m][j] = *(const u32x4*)(p + xp.plane);
-        } else if constexpr (PAIRS) {
-          if (j % 2) continue;
-          const u32x4 t = *(const u32x4_a8*)(xp.p[m] + (int64_t)step * kStep + 32 * jj);
-          v[0][m][j] = u32x2{t[0], t[1]};
-          v[0][m][j + 1] = u32x2{t[2], t[3]};
-        } else {
-          v[0][m][j] = *(const V*)(xp.p[m] + (k8 ? 1 : 2) * ((int64_t)step * kStep + 32 * jj));
-        }
+    for (int m = 0; m < MT; ++m) {
+      if constexpr (XK == X_SPLIT) {
+        const char* p = xp.base + (uint64_t)(16 * (uint32_t)step + 4 * jj) * 2 * xp.plane;
+        v[0][m][j] = *(const u32x4*)(p + xp.row[m]);
+        v[1][m][j] = *(const u32x4*)(p + xp.plane + xp.row[m]);
+      } else if constexpr (PAIRS) {
+        const u32x4 t = *(const u32x4_a8*)(xp.base + (int64_t)step * kStep + 32 * (jj & ~1) + xp.row[m]);
+        v[0][m][j & ~1] = u32x2{t[0], t[1]};
+        v[0][m][j | 1] = u32x2{t[2], t[3]};
+      } else {
+        v[0][m][j] = *(const V*)(xp.base + (k8 ? 1 : 2) * ((int64_t)step * kStep + 32 * jj) + xp.row[m]);
       }
+    }
   }
-  template <bool PAIRS>
+  template <bool TAIL>
+  __device__ __forceinline__ void load_all(const XPtr<MT>& xp, int step, int lim) {
+#pragma unroll
+    for (int j = 0; j < 4; j += PAIRS ? 2 : 1) load<TAIL>(j, xp, step, lim);
+  }
   __device__ __forceinline__ V get(const Lanes& ln, int r, int m, int j) const {
     return XK == X_SPLIT ? v[r][m][j] : from_lane(PAIRS ? ln.to_pairs : ln.to_operand, v[r][m][j]);
   }
@@ -233,6 +237,10 @@ __device__ __forceinline__ float row_scale(float v, const Lanes& ln, int t, int 
 // no vector arithmetic. What a step needs besides weights and activations, the
 // scales (Aux), comes for four steps at once: lane quarter t loads those of the
 // t-th of them, for its row l % 16.
+//
+// Loads in flight. What a step has taken out of its registers is loaded for a later
+// step at once: activations of the next one, weights of the P-th next. Loads return
+// in order, so activations are asked for before the weights of the same step.
 
 // 16-bit weights [rows][K]: four 16-byte loads, each 64 contiguous bytes of a
 // row. 8-bit activations are widened to bf16 (the weights' bytes bound this
@@ -255,10 +263,10 @@ struct Dense {
       w = (uint32_t)row * (uint32_t)m.stride + 16 * ln.piece();
     }
   };
-  struct Stage {
+  struct Weights {
     u32x4 w[R][4];
-    XRows<XK, MT> x;
   };
+  typedef XRows<XK, MT, false> X;
   struct Aux {
     float xs[MT];
   };
@@ -270,17 +278,18 @@ struct Dense {
     }
   }
   template <bool TAIL>
-  static __device__ __forceinline__ void load(Stage& st, const Mat& mat, const Row (&rows)[R], const XPtr<MT>& xp, const Lanes& ln, int step, int lim) {
+  static __device__ __forceinline__ void load(Weights& w, const Mat& mat, const Row (&rows)[R], const Lanes&, int step, int lim) {
     const char* base = mat.w + 256 * (int64_t)step;
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) st.w[r][j] = *(const u32x4*)(base + rows[r].w + 64 * (TAIL && 32 * j >= lim ? 0 : j));
-    st.x.template load<false, TAIL>(xp, step, lim);
+      for (int j = 0; j < 4; ++j) w.w[r][j] = *(const u32x4*)(base + rows[r].w + 64 * (TAIL && 32 * j >= lim ? 0 : j));
   }
 
-  template <bool TAIL>
-  static __device__ __forceinline__ void consume(const Stage& st, const Aux& aux, int t, f32x4 (&acc)[R][MT], const Lanes& ln, int lim) {
+  // acc += the products of a step; x and then w are loaded for the steps nx and nw (MAYBE: unless negative).
+  template <bool TAIL, bool MAYBE>
+  static __device__ __forceinline__ void consume(Weights& wt, X& x, const Aux& aux, int t, f32x4 (&acc)[R][MT], const Mat& mat,
+                                                 const Row (&rows)[R], const XPtr<MT>& xp, const Lanes& ln, int lim, int nx, int nw) {
     f32x4 part[R][MT];
     if constexpr (kGrouped) {
 #pragma unroll
@@ -288,24 +297,34 @@ struct Dense {
 #pragma unroll
         for (int m = 0; m < MT; ++m) part[r][m] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
+    u32x4 w[R][4];
+    typename X::V xv[kXR][MT][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (TAIL && 32 * j >= lim) break;
-      u32x4 w[R];
 #pragma unroll
-      for (int r = 0; r < R; ++r) w[r] = from_lane(ln.to_operand, st.w[r][j]);
+      for (int r = 0; r < R; ++r) w[r][j] = from_lane(ln.to_operand, wt.w[r][j]);
+#pragma unroll
+      for (int v = 0; v < kXR; ++v)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) xv[v][m][j] = x.get(ln, v, m, j);
+    }
+    if (!MAYBE || nx >= 0) x.template load_all<false>(xp, nx, kStep);
+    if (!MAYBE || nw >= 0) load<false>(wt, mat, rows, ln, nw, kStep);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (TAIL && 32 * j >= lim) break;
 #pragma unroll
       for (int v = 0; v < kXR; ++v)
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          const auto xv = st.x.template get<false>(ln, v, m, j);
-          bf16x8 x;
-          if constexpr (k8) x = widen8<x_is_i8(XK)>(xv);
-          else x = __builtin_bit_cast(bf16x8, xv);
+          bf16x8 xo;
+          if constexpr (k8) xo = widen8<x_is_i8(XK)>(xv[v][m][j]);
+          else xo = __builtin_bit_cast(bf16x8, xv[v][m][j]);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             f32x4& d = kGrouped ? part[r][m] : acc[r][m];
-            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, __builtin_bit_cast(bf16x8, w[r]), d, 0, 0, 0);
+            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, __builtin_bit_cast(bf16x8, w[r][j]), d, 0, 0, 0);
           }
         }
     }
@@ -370,10 +389,10 @@ struct Quant4 {
       s = (uint32_t)srow * (uint32_t)m.gstride;
     }
   };
-  struct Stage {
+  struct Weights {
     u32x4 w[R];
-    XRows<XK, MT> x;
   };
+  typedef XRows<XK, MT, kPairs> X;
   struct Aux {
     uint32_t s[R][(kGroups + 1) / 2], z[R];     // bf16 pairs, bytes
     float xs[MT];
@@ -425,14 +444,13 @@ struct Quant4 {
   }
 
   template <bool TAIL>
-  static __device__ __forceinline__ void load(Stage& st, const Mat& mat, const Row (&rows)[R], const XPtr<MT>& xp, const Lanes& ln, int step, int lim) {
+  static __device__ __forceinline__ void load(Weights& w, const Mat& mat, const Row (&rows)[R], const Lanes& ln, int step, int lim) {
     const char* base = mat.w + 64 * (int64_t)step;
     // past the end of a row: its last 32 weights again, in groups that are not used
     const int piece = ln.piece();
     const uint32_t back = TAIL && 32 * piece >= lim ? 16 * (piece + 1) - lim / 2 : 0;
 #pragma unroll
-    for (int r = 0; r < R; ++r) st.w[r] = *(const u32x4*)(base + (rows[r].w - back));
-    st.x.template load<kPairs, TAIL>(xp, step, lim);
+    for (int r = 0; r < R; ++r) w.w[r] = *(const u32x4*)(base + (rows[r].w - back));
   }
 
   static __device__ __forceinline__ u32x4 gather(u32x4 v, const Lanes& ln) {
@@ -452,12 +470,17 @@ struct Quant4 {
   }
   static __device__ __forceinline__ u32x2 bytes8(uint32_t v) { return u32x2{v & 0x0f0f0f0fu, (v >> 4) & 0x0f0f0f0fu}; }
   static __device__ __forceinline__ long as_long(u32x2 v) { return __builtin_bit_cast(long, v); }
+  static __device__ __forceinline__ i32x4 as_i32x4(u32x2 a, u32x2 b) { return i32x4{(int)a[0], (int)a[1], (int)b[0], (int)b[1]}; }
 
-  template <bool TAIL>
-  static __device__ __forceinline__ void consume(const Stage& st, const Aux& aux, int t, f32x4 (&acc)[R][MT], const Lanes& ln, int lim) {
+  // acc += the products of a step; x and then w are loaded for the steps nx and nw (MAYBE: unless negative).
+  template <bool TAIL, bool MAYBE>
+  static __device__ __forceinline__ void consume(Weights& wt, X& x, const Aux& aux, int t, f32x4 (&acc)[R][MT], const Mat& mat,
+                                                 const Row (&rows)[R], const XPtr<MT>& xp, const Lanes& ln, int lim, int nx, int nw) {
+    typedef typename std::conditional<x_is_i8(XK), i32x4, f32x4>::type Sum;
+    constexpr int kBlock = x_is_i8(XK) && kWords > 1 ? 2 : 1;      // words a matrix instruction takes
     u32x4 w[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) w[r] = gather(st.w[r], ln);
+    for (int r = 0; r < R; ++r) w[r] = gather(wt.w[r], ln);
     const int row = 64 * t + 4 * (ln.lane & 15);          // quarter t's lane of this lane's weight row
     uint32_t sw[R][(kGroups + 1) / 2], zw[R];
 #pragma unroll
@@ -466,138 +489,129 @@ struct Quant4 {
       for (int i = 0; i < (kGroups + 1) / 2; ++i) sw[r][i] = from_lane(row, aux.s[r][i]);
       zw[r] = kGroups == 1 ? sw[r][0] : from_lane(row, aux.z[r]);
     }
-    f32x4 xs[MT];
-    if constexpr (kGrouped) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) xs[m][i] = row_scale(aux.xs[m], ln, t, i);
-    }
 #pragma unroll
     for (int h = 0; h < kGroups; ++h) {
       if (TAIL && G * h >= lim) break;
-      f32x4 sum[MT];                            // of x over the group
-      u32x4 x16[kXR][MT][kWords];
-      u32x2 x8[MT][kWords];
-      if constexpr (!x_is_i8(XK)) {
+      Sum part[R][MT], sum[MT];                 // of the group: products, and x alone
 #pragma unroll
-        for (int m = 0; m < MT; ++m) sum[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int m = 0; m < MT; ++m) {
+        sum[m] = Sum{0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < R; ++r) part[r][m] = Sum{0, 0, 0, 0};
       }
 #pragma unroll
-      for (int f = 0; f < kWords; ++f)
+      for (int f = 0; f < kWords; f += kBlock) {
+        const int j = h * kWords + f;
+        typename X::V xv[kXR][MT][kBlock];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const int j = h * kWords + f;
-          if constexpr (k8) {
-            const u32x2 v = st.x.template get<kPairs>(ln, 0, m, j);
-            x8[m][f] = even_odd(v[0], v[1]);
-            if constexpr (x_is_e4m3(XK))
-              sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(as_long(x8[m][f]), 0x3838383838383838l, sum[m], 0, 0, 0);
-          } else {
-            const u32x4 one = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-#pragma unroll
-            for (int v = 0; v < kXR; ++v) {
-              x16[v][m][f] = st.x.template get<false>(ln, v, m, j);
-              if constexpr (XK != X_SPLIT) x16[v][m][f] = paired(x16[v][m][f]);
-              sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x16[v][m][f]),
-                                                               __builtin_bit_cast(bf16x8, one), sum[m], 0, 0, 0);
-            }
-          }
-        }
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const uint32_t z = (zw[r] >> (8 * h)) & 0xffu;
-        float s = kGroups == 1 || h % 2 ? bf16_hi(sw[r][h / 2]) : bf16_lo(sw[r][h / 2]);
-        f32x4 part[MT];
-        if constexpr (x_is_i8(XK)) {
-          const uint32_t up = 0x80808080u - z * 0x01010101u;
-          i32x4 ip[MT];
-#pragma unroll
-          for (int m = 0; m < MT; ++m) ip[m] = i32x4{0, 0, 0, 0};
-          u32x2 d[kWords];
-#pragma unroll
-          for (int f = 0; f < kWords; ++f) {
-            const u32x2 b = bytes8(w[r][h * kWords + f]);
-            d[f] = u32x2{(b[0] + up) ^ 0x80808080u, (b[1] + up) ^ 0x80808080u};
-          }
-          if constexpr (kWords == 1) {
-#pragma unroll
-            for (int m = 0; m < MT; ++m) ip[m] = __builtin_amdgcn_mfma_i32_16x16x32_i8(as_long(x8[m][0]), as_long(d[0]), ip[m], 0, 0, 0);
-          } else {
-#pragma unroll
-            for (int f = 0; f < kWords; f += 2)
-#pragma unroll
-              for (int m = 0; m < MT; ++m)
-                ip[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-                    i32x4{(int)x8[m][f][0], (int)x8[m][f][1], (int)x8[m][f + 1][0], (int)x8[m][f + 1][1]},
-                    i32x4{(int)d[f][0], (int)d[f][1], (int)d[f + 1][0], (int)d[f + 1][1]}, ip[m], 0, 0, 0);
-          }
+        for (int v = 0; v < kXR; ++v)
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) part[m][i] = (float)ip[m][i];
+            for (int i = 0; i < kBlock; ++i) {
+              xv[v][m][i] = x.get(ln, v, m, j + i);
+              if constexpr (k8) xv[v][m][i] = even_odd(xv[v][m][i][0], xv[v][m][i][1]);
+              else if constexpr (XK != X_SPLIT) xv[v][m][i] = paired(xv[v][m][i]);
+            }
+        // both words of a load have been taken
+        if ((!kPairs || kBlock == 2 || j % 2 == 1) && (!MAYBE || nx >= 0)) x.template load<false>(j, xp, nx, kStep);
+        if constexpr (x_is_i8(XK)) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const uint32_t up = 0x80808080u - ((zw[r] >> (8 * h)) & 0xffu) * 0x01010101u;
+            u32x2 d[kBlock];
+#pragma unroll
+            for (int i = 0; i < kBlock; ++i) {
+              const u32x2 b = bytes8(w[r][j + i]);
+              d[i] = u32x2{(b[0] + up) ^ 0x80808080u, (b[1] + up) ^ 0x80808080u};
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              if constexpr (kBlock == 1)
+                part[r][m] = __builtin_amdgcn_mfma_i32_16x16x32_i8(as_long(xv[0][m][0]), as_long(d[0]), part[r][m], 0, 0, 0);
+              else
+                part[r][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(as_i32x4(xv[0][m][0], xv[0][m][kBlock - 1]),
+                                                                   as_i32x4(d[0], d[kBlock - 1]), part[r][m], 0, 0, 0);
+            }
+          }
         } else if constexpr (x_is_e4m3(XK)) {
-          const float nz = (float)z * -0x1p-9f;
-          s *= 512.0f;
 #pragma unroll
-          for (int m = 0; m < MT; ++m) part[m] = sum[m] * nz;
+          for (int m = 0; m < MT; ++m)
+            sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(as_long(xv[0][m][0]), 0x3838383838383838l, sum[m], 0, 0, 0);
 #pragma unroll
-          for (int f = 0; f < kWords; ++f) {
-            const long b = as_long(bytes8(w[r][h * kWords + f]));
+          for (int r = 0; r < R; ++r) {
+            const long b = as_long(bytes8(w[r][j]));
 #pragma unroll
-            for (int m = 0; m < MT; ++m) part[m] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(as_long(x8[m][f]), b, part[m], 0, 0, 0);
+            for (int m = 0; m < MT; ++m)
+              part[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(as_long(xv[0][m][0]), b, part[r][m], 0, 0, 0);
           }
         } else {
-          const float nz = -128.0f - (float)z;
+          const u32x4 one = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
 #pragma unroll
-          for (int m = 0; m < MT; ++m) part[m] = sum[m] * nz;
+          for (int v = 0; v < kXR; ++v)
 #pragma unroll
-          for (int f = 0; f < kWords; ++f) {
-            const bf16x8 b = frag16(w[r][h * kWords + f]);
+            for (int m = 0; m < MT; ++m)
+              sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv[v][m][0]), __builtin_bit_cast(bf16x8, one),
+                                                               sum[m], 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const bf16x8 b = frag16(w[r][j]);
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
               for (int v = 0; v < kXR; ++v)
-                part[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x16[v][m][f]), b, part[m], 0, 0, 0);
+                part[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv[v][m][0]), b, part[r][m], 0, 0, 0);
           }
         }
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[r][m][i] = __builtin_fmaf(part[m][i], kGrouped ? s * xs[m][i] : s, acc[r][m][i]);
-        // one row tile and group at a time: all of them at once would not fit in the registers
+        // a word at a time: all of a step at once would not fit in the registers
         if constexpr (MT > 1) __builtin_amdgcn_sched_barrier(0);
       }
+      if (h == kGroups - 1 && (!MAYBE || nw >= 0)) load<false>(wt, mat, rows, ln, nw, kStep);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float xs = kGrouped ? row_scale(aux.xs[m], ln, t, i) : 1.0f;
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float z = (float)((zw[r] >> (8 * h)) & 0xffu);
+            const float s = kGroups == 1 || h % 2 ? bf16_hi(sw[r][h / 2]) : bf16_lo(sw[r][h / 2]);
+            float v;
+            if constexpr (x_is_i8(XK)) v = (float)part[r][m][i];
+            else if constexpr (x_is_e4m3(XK)) v = __builtin_fmaf(sum[m][i], z * -0x1p-9f, part[r][m][i]) * 512.0f;
+            else v = __builtin_fmaf(sum[m][i], -128.0f - z, part[r][m][i]);
+            acc[r][m][i] = __builtin_fmaf(v, kGrouped ? s * xs : s, acc[r][m][i]);
+          }
+        }
       __builtin_amdgcn_sched_barrier(0);
     }
   }
 };
 
-// acc[r][m] += products over the n steps first, first + by, ... of 128 k. P steps
-// are kept in flight in registers, the scales of four more.
+// acc[r][m] += products over the n steps first, first + by, ... of 128 k.
 template <class Prod>
 __device__ __forceinline__ void run_steps(f32x4 (&acc)[Prod::kR][Prod::kMT], const typename Prod::Mat& mat,
                                           const typename Prod::Row (&rows)[Prod::kR], const XPtr<Prod::kMT>& xp, const Lanes& ln,
                                           int first, int by, int n) {
   constexpr int P = Prod::kP;
-  static_assert(P == 1 || P == 2 || P == 4, "stages");
+  static_assert(P == 1 || P == 2 || P == 4, "weights in flight");
   if (n <= 0) return;
-  typename Prod::Stage st[P];
+  typename Prod::Weights w[P];
+  typename Prod::X x;
   typename Prod::Aux cur, nxt;
   auto aux = [&](typename Prod::Aux& a, int i) { Prod::load_aux(a, mat, rows, xp, first + by * min(i + ln.quarter, n - 1), kStep); };
   aux(cur, 0);
+  x.template load_all<false>(xp, first, kStep);
 #pragma unroll
   for (int p = 0; p < P; ++p)
-    if (p < n) Prod::template load<false>(st[p], mat, rows, xp, ln, first + by * p, kStep);
+    if (p < n) Prod::template load<false>(w[p], mat, rows, ln, first + by * p, kStep);
   int i = 0;
   for (; i + 4 + P <= n; i += 4) {      // no branches in here: the compiler's waits count the loads in flight
     aux(nxt, i + 4);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      Prod::template consume<false>(st[t % P], cur, t, acc, ln, kStep);
-      Prod::template load<false>(st[t % P], mat, rows, xp, ln, first + by * (i + t + P), kStep);
-    }
+    for (int t = 0; t < 4; ++t)
+      Prod::template consume<false, false>(w[t % P], x, cur, t, acc, mat, rows, xp, ln, kStep, first + by * (i + t + 1),
+                                           first + by * (i + t + P));
     cur = nxt;
   }
   for (; i < n; i += 4) {
@@ -605,8 +619,8 @@ __device__ __forceinline__ void run_steps(f32x4 (&acc)[Prod::kR][Prod::kMT], con
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       if (i + t >= n) break;
-      Prod::template consume<false>(st[t % P], cur, t, acc, ln, kStep);
-      if (i + t + P < n) Prod::template load<false>(st[t % P], mat, rows, xp, ln, first + by * (i + t + P), kStep);
+      Prod::template consume<false, true>(w[t % P], x, cur, t, acc, mat, rows, xp, ln, kStep, i + t + 1 < n ? first + by * (i + t + 1) : -1,
+                                    i + t + P < n ? first + by * (i + t + P) : -1);
     }
     cur = nxt;
   }
@@ -616,11 +630,13 @@ template <class Prod>
 __device__ __forceinline__ void run_tail(f32x4 (&acc)[Prod::kR][Prod::kMT], const typename Prod::Mat& mat,
                                          const typename Prod::Row (&rows)[Prod::kR], const XPtr<Prod::kMT>& xp, const Lanes& ln,
                                          int step, int lim) {
-  typename Prod::Stage st;
+  typename Prod::Weights w;
+  typename Prod::X x;
   typename Prod::Aux aux;
   Prod::load_aux(aux, mat, rows, xp, step, lim);
-  Prod::template load<true>(st, mat, rows, xp, ln, step, lim);
-  Prod::template consume<true>(st, aux, 0, acc, ln, lim);
+  x.template load_all<true>(xp, step, lim);
+  Prod::template load<true>(w, mat, rows, ln, step, lim);
+  Prod::template consume<true, true>(w, x, aux, 0, acc, mat, rows, xp, ln, lim, -1, -1);
 }
 
 template <class Prod>

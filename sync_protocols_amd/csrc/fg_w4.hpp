@@ -54,10 +54,11 @@ __global__ __launch_bounds__(64 * W) void w4_linear_kernel(W4Args a) {
     rows[r].set(mat, min(16 * r + ln.load_row(), last), min(16 * r + (ln.lane & 15), last), ln);
   }
   XPtr<MT> xp;
+  xp.base = a.x + t0 * a.ldx;
   xp.scale = a.xs + t0 * a.xs_stride;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    xp.p[m] = a.x + (int64_t)min(t0 + 16 * m + ln.load_row(), a.rows - 1) * a.ldx + x_piece<G, XK>(ln);
+    xp.row[m] = (uint32_t)min(16 * m + ln.load_row(), a.rows - 1 - t0) * (uint32_t)a.ldx + x_piece<G, XK>(ln);
     xp.at[m] = (uint32_t)min(16 * m + (ln.lane & 15), a.rows - 1 - t0) * (uint32_t)a.xs_stride;
   }
   f32x4 acc[R][MT];
