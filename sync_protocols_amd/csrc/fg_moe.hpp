@@ -8,8 +8,10 @@
 // launch of its own would. Kernel 1 forms c * silu(gate) * up per pick; it is
 // kept as the sum of two bf16 numbers (16 mantissa bits), so that the second
 // product takes it on the matrix unit without the rounding of one bf16, which
-// would be as large as that of the result. Kernel 2 sums all picks of a token in
-// a fixed order.
+// would be as large as that of the result. The two are rows of their own in that
+// product, next to each other, and their results are added: few picks, as a
+// decoding step has per expert, leave half of the 16 rows of a matrix instruction
+// free anyway. Kernel 2 sums all picks of a token in a fixed order.
 #pragma once
 
 #include "fg_w4.hpp"
@@ -23,7 +25,7 @@ struct MoeArgs {
   const char* x; const float* xs; const int32_t* topk; const float* weights;
   const char* w1; const uint16_t* s1; const uint8_t* z1;
   const char* w2; const uint16_t* s2; const uint8_t* z2;
-  char* h;                           // SplitRows: this GPU's picks by expert, by pick within an expert
+  char* h;                           // PackedRows: two rows a pick, by expert, by pick within an expert
   uint16_t* y;
   int64_t ldx, xs_stride, ldy;       // ldx in bytes
   int32_t tokens, k, base, n_local, K, F;
@@ -50,17 +52,18 @@ __device__ __forceinline__ void moe_up_pass(const MoeArgs& a, int e, int f0, con
   typename Prod::Row rows[2 * C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int last = a.F - 1 - f0, f = min(16 * c + ln.load_row(), last), sf = min(16 * c + (ln.lane & 15), last);
-    rows[c].set(mat, f, sf, ln);
-    rows[C + c].set(mat, a.F + f, a.F + sf, ln);
+    const int f = min(16 * c + ln.load_row(), a.F - 1 - f0);
+    rows[c].set(mat, f, ln);
+    rows[C + c].set(mat, a.F + f, ln);
   }
   XPtr<MT> xp;
   xp.base = a.x;
   xp.scale = a.xs;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    xp.row[m] = (uint32_t)(list[min(s0 + 16 * m + ln.load_row(), cnt - 1)] / a.k) * (uint32_t)a.ldx + x_piece<G, XK>(ln);
-    xp.at[m] = (uint32_t)(list[min(s0 + 16 * m + (ln.lane & 15), cnt - 1)] / a.k) * (uint32_t)a.xs_stride;
+    const uint32_t token = list[min(s0 + 16 * m + ln.load_row(), cnt - 1)] / a.k;
+    xp.row[m] = token * (uint32_t)a.ldx + x_piece<G, XK>(ln);
+    xp.at[m] = token * (uint32_t)a.xs_stride;
   }
   f32x4 acc[2 * C][MT];
   clear<Prod>(acc);
@@ -93,17 +96,17 @@ __device__ __forceinline__ void moe_up_pass(const MoeArgs& a, int e, int f0, con
       }
       const float h = g / (1.0f + __expf(-g)) * u * a.weights[p];
       const uint16_t hi = f_bf16(h);
-      char* to = a.h + SplitRows::at(start + slot, G == 0 ? f0 + col : paired_place(f0 + col), a.plane);
+      char* to = a.h + PackedRows::at(2 * (start + slot), G == 0 ? f0 + col : paired_place(f0 + col), a.plane);
       *(uint16_t*)to = hi;
       // an infinite hi has no remainder
-      *(uint16_t*)(to + a.plane) = fabsf(bf16_f(hi)) < __builtin_inff() ? f_bf16(h - bf16_f(hi)) : 0;
+      *(uint16_t*)(to + 16) = fabsf(bf16_f(hi)) < __builtin_inff() ? f_bf16(h - bf16_f(hi)) : 0;
     }
     __syncthreads();
   }
 }
 
-template <int G, int XK, int MT, int C, int P, int W>
-__global__ __launch_bounds__(64 * W) void moe_up_kernel(MoeArgs a) {
+template <int G, int XK, int MT, int C, int P, int W, int MIN_WAVES = (W > 8 ? W / 4 : 2)>
+__global__ __launch_bounds__(64 * W, MIN_WAVES) void moe_up_kernel(MoeArgs a) {
   __shared__ uint32_t bits[FG_MOE_FEW_EXPERTS / 32];
   __shared__ uint16_t list[kMaxPicks];
   __shared__ float red[W * 16 * (32 * C + 1)];
@@ -149,16 +152,18 @@ __global__ __launch_bounds__(64 * W) void moe_up_kernel(MoeArgs a) {
 }
 
 // ---- kernel 2: workgroup = 16 R columns of y over every picked expert.
-// Its work is a list of entries, each up to 16 MT picks of one expert, sorted by
-// expert and within it by pick, as the rows of h are; the waves take equal,
-// contiguous shares of the list's steps, so that they stay level whatever the
-// number of experts.
+// Its work is a list of entries, each up to 8 MT picks (16 MT rows) of one expert,
+// sorted by expert and within it by pick, as the rows of h are; the waves take
+// equal, contiguous shares of the list's steps, so that they stay level whatever the
+// number of experts. The rows of an entry's tile start at a multiple of four, the
+// one before its first pick if that is odd: the 64 bytes that four lanes load are
+// then one piece for the address unit (unaligned, the loads of h took twice as long).
 struct DownPlan {
   unsigned long long mask[FG_MOE_FEW_EXPERTS];     // tokens that picked an expert
   uint16_t start[FG_MOE_FEW_EXPERTS];
-  uint16_t ent_e[kMaxPicks], ent_s[kMaxPicks];     // entry: expert, first row of h, rows
+  uint16_t ent_e[kMaxPicks], ent_s[kMaxPicks];     // entry: expert, first pick, picks
   uint8_t ent_c[kMaxPicks];
-  uint8_t token[kMaxPicks];                        // of a row of h
+  uint8_t token[kMaxPicks];                        // of a pick
   int entries, again;
 };
 
@@ -186,22 +191,27 @@ __device__ __forceinline__ void down_plan(const MoeArgs& a, DownPlan& pl) {
     for (int e0 = 0; e0 < a.n_local; e0 += 64) {
       const int e = e0 + lane;
       const int c = e >= a.n_local ? 0 : again ? same_before(e, picks) : __popcll(pl.mask[e]);
-      const int n = (c + 16 * MT - 1) / (16 * MT);
-      int cs = c, ns = n;
+      auto before = [&](int v) {   // sum over the lanes before this one
+        int s = v;
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(cs, d), w = __shfl_up(ns, d);
-        if (lane >= d) { cs += o; ns += w; }
-      }
-      const int start = at + cs - c, first = ent + ns - n;
+        for (int d = 1; d < 64; d <<= 1) {
+          const int o = __shfl_up(s, d);
+          if (lane >= d) s += o;
+        }
+        return s - v;
+      };
+      const int cs = before(c), start = at + cs, tile = start & ~1;
+      const int n = c ? (start + c - tile + 8 * MT - 1) / (8 * MT) : 0;
+      const int ns = before(n), first = ent + ns;
       for (int i = 0; i < n; ++i) {
+        const int s = max(start, tile + 8 * MT * i);
         pl.ent_e[first + i] = (uint16_t)e;
-        pl.ent_s[first + i] = (uint16_t)(start + 16 * MT * i);
-        pl.ent_c[first + i] = (uint8_t)min(c - 16 * MT * i, 16 * MT);
+        pl.ent_s[first + i] = (uint16_t)s;
+        pl.ent_c[first + i] = (uint8_t)(min(start + c, tile + 8 * MT * (i + 1)) - s);
       }
       if (e < a.n_local) pl.start[e] = (uint16_t)start;
-      at += __shfl(cs, 63);
-      ent += __shfl(ns, 63);
+      at += __shfl(cs + c, 63);
+      ent += __shfl(ns + n, 63);
     }
     if (lane == 0) pl.entries = ent;
   }
@@ -215,54 +225,61 @@ __device__ __forceinline__ void down_plan(const MoeArgs& a, DownPlan& pl) {
   __syncthreads();
 }
 
-template <int G, int MT, int R, int P, int W>
-__global__ __launch_bounds__(64 * W) void moe_down_kernel(MoeArgs a) {
-  typedef typename ProductOf<G, X_SPLIT, MT, R, P>::T Prod;
+// Steps `step`..`end` - 1 of an entry with picks s..s + c - 1, into sums [token][16 R].
+template <int G, int MT, int R, int P>
+__device__ __forceinline__ void moe_down_pass(const MoeArgs& a, int e, int s, int c, int n0, int step, int end, const uint8_t* token,
+                                              float* sums) {
+  typedef typename ProductOf<G, X_PACKED, MT, R, P>::T Prod;
+  const Lanes ln;
+  const int col = ln.lane & 15, tile = s & ~1, full = a.F / kStep;
+  const typename Prod::Mat mat = matrix<G, typename Prod::Mat>(a.w2, a.s2, a.z2, a.F).at((int64_t)e * a.K + n0);
+  typename Prod::Row rows[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) rows[r].set(mat, min(16 * r + ln.load_row(), a.K - 1 - n0), ln);
+  XPtr<MT> xp;
+  xp.base = a.h;
+  xp.plane = a.plane;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)                   // past the entry: its last row; results of rows outside it are not used
+    xp.row[m] = (uint32_t)PackedRows::at(min(2 * tile + 16 * m + col, 2 * (s + c) - 1), 8 * ln.quarter, a.plane);
+  f32x4 acc[R][MT];
+  clear<Prod>(acc);
+  run_steps<Prod>(acc, mat, rows, xp, ln, step, 1, min(end, full) - step);
+  if (end > full) run_tail<Prod>(acc, mat, rows, xp, ln, full, a.F % kStep);
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const int pick = tile + (16 * m + 4 * ln.quarter + i) / 2;
+      if (pick >= s && pick < s + c) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          unsafeAtomicAdd(&sums[token[pick] * 16 * R + 16 * r + col], acc[r][m][i] + acc[r][m][i + 1]);
+      }
+    }
+}
+
+template <int G, int MT, int R, int P, int W, int MIN_WAVES = (W > 8 ? W / 4 : 2)>
+__global__ __launch_bounds__(64 * W, MIN_WAVES) void moe_down_kernel(MoeArgs a) {
   __shared__ DownPlan pl;
   extern __shared__ float sums[];                  // [wave][token][16 R]
-  const Lanes ln;
-  const int tid = threadIdx.x, col = ln.lane & 15;
+  const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n0 = blockIdx.x * 16 * R;
   for (int i = tid; i < W * a.tokens * 16 * R; i += 64 * W) sums[i] = 0.0f;
   down_plan<MT, W>(a, pl);
-  const int steps = (a.F + kStep - 1) / kStep, full = a.F / kStep;
+  const int steps = (a.F + kStep - 1) / kStep;
   const int64_t units = (int64_t)__builtin_amdgcn_readfirstlane(pl.entries) * steps;
   const int64_t from = units * wave / W, to = units * (wave + 1) / W;
-  const typename Prod::Mat all = matrix<G, typename Prod::Mat>(a.w2, a.s2, a.z2, a.F).at(n0);
-  typename Prod::Row rows[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int last = a.K - 1 - n0;
-    rows[r].set(all, min(16 * r + ln.load_row(), last), min(16 * r + col, last), ln);
-  }
-  XPtr<MT> xp;
-  xp.base = a.h;
-  xp.plane = a.plane;
   int ent = (int)(from / steps), step = (int)(from % steps);
   for (int64_t left = to - from; left > 0; ++ent, step = 0) {
-    const int s = __builtin_amdgcn_readfirstlane(pl.ent_s[ent]), c = __builtin_amdgcn_readfirstlane(pl.ent_c[ent]);
-    const typename Prod::Mat mat = all.at((int64_t)__builtin_amdgcn_readfirstlane(pl.ent_e[ent]) * a.K);
-#pragma unroll
-    for (int m = 0; m < MT; ++m)                   // past the entry: its last row, whose results are not used again
-      xp.row[m] = (uint32_t)SplitRows::at(s + min(16 * m + col, c - 1), 8 * ln.quarter, a.plane);
+    const int e = __builtin_amdgcn_readfirstlane(pl.ent_e[ent]), s = __builtin_amdgcn_readfirstlane(pl.ent_s[ent]);
+    const int c = __builtin_amdgcn_readfirstlane(pl.ent_c[ent]);
     const int end = steps - step < left ? steps : step + (int)left;
     left -= end - step;
-    f32x4 acc[R][MT];
-    clear<Prod>(acc);
-    run_steps<Prod>(acc, mat, rows, xp, ln, step, 1, min(end, full) - step);
-    if (end > full) run_tail<Prod>(acc, mat, rows, xp, ln, full, a.F % kStep);
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int slot = 16 * m + 4 * ln.quarter + i;
-        if (slot < c) {
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-            unsafeAtomicAdd(&sums[(wave * a.tokens + pl.token[s + slot]) * 16 * R + 16 * r + col], acc[r][m][i]);
-        }
-      }
+    float* to_sums = sums + wave * a.tokens * 16 * R;
+    if (MT == 1 || (s & 1) + c <= 8) moe_down_pass<G, 1, R, P>(a, e, s, c, n0, step, end, pl.token, to_sums);
+    else moe_down_pass<G, MT, R, P>(a, e, s, c, n0, step, end, pl.token, to_sums);
   }
   __syncthreads();
   for (int i = tid; i < a.tokens * 16 * R; i += 64 * W) {

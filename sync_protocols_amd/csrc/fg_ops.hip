@@ -126,9 +126,8 @@ void launch_moe_down_tile(const MoeArgs& a, hipStream_t stream) {
 // a workgroup then.
 template <int G>
 void launch_moe_down(const MoeArgs& a, hipStream_t stream) {
-  if (many_rows(a)) launch_moe_down_tile<G, 2, 2, 1, 8>(a, stream);
+  if (many_rows(a)) launch_moe_down_tile<G, 4, 2, 1, 8>(a, stream);
   else if (a.K < 32 * kCUs / 2) launch_moe_down_tile<G, 1, 1, 1, 8>(a, stream);
-  else if (G == 0 && a.tokens <= 16) launch_moe_down_tile<G, 1, 2, 1, 16>(a, stream);
   else launch_moe_down_tile<G, 1, 2, 2, 8>(a, stream);
 }
 
@@ -242,7 +241,7 @@ fg_status fg_moe_few(const void* x, int64_t ldx, int32_t x_type, const float* x_
   a.x = (const char*)x; a.xs = x_scale; a.topk = topk; a.weights = weights;
   a.w1 = (const char*)w1; a.s1 = (const uint16_t*)w1_scale; a.z1 = (const uint8_t*)w1_zero;
   a.w2 = (const char*)w2; a.s2 = (const uint16_t*)w2_scale; a.z2 = (const uint8_t*)w2_zero;
-  a.h = (char*)workspace; a.plane = 16 * (uint32_t)(tokens * k);
+  a.h = (char*)workspace; a.plane = 32 * (uint32_t)(tokens * k);
   a.y = (uint16_t*)y;
   a.ldx = ldx * (x_type == FG_BF16 ? 2 : 1); a.xs_stride = x_group ? K / x_group : 1; a.ldy = ldy;
   a.tokens = tokens; a.k = k; a.base = expert_base; a.n_local = n_local; a.K = K; a.F = F;

@@ -90,11 +90,11 @@ __device__ __forceinline__ uint32_t lanes_min(uint32_t v) {
 }
 
 // ------------------------------------------------------------- activations
-// X_SPLIT: two bf16 numbers whose sum is the activation (the expert layer's own
-// intermediate, see SplitRows); X_I8G, X_E4M3G: 8-bit rows
+// X_PACKED: bf16 in operand order (the expert layer's own intermediate, see
+// PackedRows); X_I8G, X_E4M3G: 8-bit rows
 // with one scale per 128 k, the others have one per row, which the caller
 // applies to the finished sums.
-enum { X_BF16 = FG_BF16, X_I8 = FG_I8, X_E4M3 = FG_E4M3, X_SPLIT = 16, X_I8G = 17, X_E4M3G = 18 };
+enum { X_BF16 = FG_BF16, X_I8 = FG_I8, X_E4M3 = FG_E4M3, X_PACKED = 16, X_I8G = 17, X_E4M3G = 18 };
 constexpr bool x_is_i8(int xk) { return xk == X_I8 || xk == X_I8G; }
 constexpr bool x_is_e4m3(int xk) { return xk == X_E4M3 || xk == X_E4M3G; }
 constexpr bool x_is_8bit(int xk) { return x_is_i8(xk) || x_is_e4m3(xk); }
@@ -169,33 +169,32 @@ __device__ __forceinline__ u32x2 from_lane(int index, u32x2 v) { return u32x2{fr
 // Activations of a tile: base + row[m] is the row that this lane loads from (16 m +
 // l / 4, clamped by the caller to one that exists; rows of D that belong to no token
 // are never stored) and its piece of it. The base is uniform and the rest of an
-// address 32 bits, as for the weights. Scales per 128 k: scale + at[m] is that of
-// row 16 m + l % 16.
+// address 32 bits, as for the weights. Scales per 128 k: those of the row start at
+// scale + at[m].
 template <int MT>
 struct XPtr {
   const char* base;
   uint32_t row[MT];
   const float* scale;
   uint32_t at[MT];
-  uint32_t plane;                               // X_SPLIT: bytes of 8 elements of all rows
+  uint32_t plane;                               // X_PACKED: bytes of 8 elements of all rows
 };
 
-// X_SPLIT rows: for every 8 elements the first parts of all rows, 16 bytes each,
-// then the seconds. Rows that are used together lie side by side, so lanes load
-// straight into the operand's places: row[m] is row 16 m + l % 16 at 8 (l / 16).
-// Elements in paired() order for 4-bit weights.
-struct SplitRows {
-  static __device__ __forceinline__ int64_t at(int64_t row, int k, uint32_t plane) {    // bytes to the first part
-    return (int64_t)(k >> 3) * 2 * plane + 16 * row + 2 * (k & 7);
+// X_PACKED rows: for every 8 elements those of all rows, 16 bytes each. Rows that
+// are used together lie side by side, so lanes load straight into the operand's
+// places: row[m] is row 16 m + l % 16 at 8 (l / 16). Elements in paired() order for
+// 4-bit weights.
+struct PackedRows {
+  static __device__ __forceinline__ int64_t at(int64_t row, int k, uint32_t plane) {
+    return (int64_t)(k >> 3) * plane + 16 * row + 2 * (k & 7);
   }
 };
 
 template <int XK, int MT, bool PAIRS>
 struct XRows {
-  static constexpr int kXR = XK == X_SPLIT ? 2 : 1;
   static constexpr bool k8 = x_is_8bit(XK);
   typedef typename std::conditional<k8, u32x2, u32x4>::type V;      // eight elements
-  V v[kXR][MT][4];
+  V v[MT][4];
   // Elements 64 (j / 2) + 32 (q % 2) + 16 (q / 2) + 8 (j % 2) of the step (PAIRS; one load for two j) or 32 j + 8 q
   // into v[..][j]; those at or past lim: any.
   template <bool TAIL>
@@ -203,16 +202,14 @@ struct XRows {
     const int jj = TAIL && (PAIRS ? 64 * (j / 2) : 32 * j) >= lim ? 0 : j;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      if constexpr (XK == X_SPLIT) {
-        const char* p = xp.base + (uint64_t)(16 * (uint32_t)step + 4 * jj) * 2 * xp.plane;
-        v[0][m][j] = *(const u32x4*)(p + xp.row[m]);
-        v[1][m][j] = *(const u32x4*)(p + xp.plane + xp.row[m]);
+      if constexpr (XK == X_PACKED) {
+        v[m][j] = *(const u32x4*)(xp.base + (uint64_t)(16 * (uint32_t)step + 4 * jj) * xp.plane + xp.row[m]);
       } else if constexpr (PAIRS) {
         const u32x4 t = *(const u32x4_a8*)(xp.base + (int64_t)step * kStep + 32 * (jj & ~1) + xp.row[m]);
-        v[0][m][j & ~1] = u32x2{t[0], t[1]};
-        v[0][m][j | 1] = u32x2{t[2], t[3]};
+        v[m][j & ~1] = u32x2{t[0], t[1]};
+        v[m][j | 1] = u32x2{t[2], t[3]};
       } else {
-        v[0][m][j] = *(const V*)(xp.base + (k8 ? 1 : 2) * ((int64_t)step * kStep + 32 * jj) + xp.row[m]);
+        v[m][j] = *(const V*)(xp.base + (k8 ? 1 : 2) * ((int64_t)step * kStep + 32 * jj) + xp.row[m]);
       }
     }
   }
@@ -221,22 +218,23 @@ struct XRows {
 #pragma unroll
     for (int j = 0; j < 4; j += PAIRS ? 2 : 1) load<TAIL>(j, xp, step, lim);
   }
-  __device__ __forceinline__ V get(const Lanes& ln, int r, int m, int j) const {
-    return XK == X_SPLIT ? v[r][m][j] : from_lane(PAIRS ? ln.to_pairs : ln.to_operand, v[r][m][j]);
+  __device__ __forceinline__ V get(const Lanes& ln, int m, int j) const {
+    return XK == X_PACKED ? v[m][j] : from_lane(PAIRS ? ln.to_pairs : ln.to_operand, v[m][j]);
   }
 };
 
 // ----------------------------------------------------------------- products
-// The scale that quarter t's lane of row 4 (l / 16) + i holds.
+// The scale of step t that the lanes of row 4 (l / 16) + i hold.
 __device__ __forceinline__ float row_scale(float v, const Lanes& ln, int t, int i) {
-  return __uint_as_float(from_lane(64 * t + 16 * ln.quarter + 4 * i, __float_as_uint(v)));
+  return __uint_as_float(from_lane(64 * ln.quarter + 16 * i + 4 * t, __float_as_uint(v)));
 }
 
 // One step of a wave is kStep = 128 k of 16 R weight rows. A weight matrix is a
 // uniform base (Mat) and 32-bit distances per lane (Row), so that an address costs
 // no vector arithmetic. What a step needs besides weights and activations, the
-// scales (Aux), comes for four steps at once: lane quarter t loads those of the
-// t-th of them, for its row l % 16.
+// scales (Aux), comes for four steps at once: lane l loads those of row l / 4 for the
+// l % 4-th of them, which lie close together (with a row a lane side by side they took
+// as many of the address unit's clocks as the weights).
 //
 // Loads in flight. What a step has taken out of its registers is loaded for a later
 // step at once: activations of the next one, weights of the P-th next. Loads return
@@ -249,7 +247,6 @@ template <int XK, int MT, int R, int P>
 struct Dense {
   static constexpr int kR = R, kMT = MT, kP = P;
   static constexpr bool kGrouped = x_grouped(XK);
-  static constexpr int kXR = XK == X_SPLIT ? 2 : 1;
   static constexpr bool k8 = x_is_8bit(XK);
   struct Mat {
     const char* w;                              // bf16 [rows][K]
@@ -258,8 +255,7 @@ struct Dense {
   };
   struct Row {
     uint32_t w;
-    // loads of `row`, scales of row `srow`
-    __device__ __forceinline__ void set(const Mat& m, int row, int, const Lanes& ln) {
+    __device__ __forceinline__ void set(const Mat& m, int row, const Lanes& ln) {
       w = (uint32_t)row * (uint32_t)m.stride + 16 * ln.piece();
     }
   };
@@ -274,9 +270,10 @@ struct Dense {
   static __device__ __forceinline__ void load_aux(Aux& a, const Mat&, const Row (&)[R], const XPtr<MT>& xp, int step, int) {
     if constexpr (kGrouped) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) a.xs[m] = xp.scale[xp.at[m] + (uint32_t)step];
+      for (int m = 0; m < MT; ++m) a.xs[m] = *(const float*)((const char*)xp.scale + 4 * (xp.at[m] + (uint32_t)step));
     }
   }
+  static __device__ __forceinline__ void finish_aux(Aux&, const Mat&) {}
   template <bool TAIL>
   static __device__ __forceinline__ void load(Weights& w, const Mat& mat, const Row (&rows)[R], const Lanes&, int step, int lim) {
     const char* base = mat.w + 256 * (int64_t)step;
@@ -298,16 +295,14 @@ struct Dense {
         for (int m = 0; m < MT; ++m) part[r][m] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     u32x4 w[R][4];
-    typename X::V xv[kXR][MT][4];
+    typename X::V xv[MT][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (TAIL && 32 * j >= lim) break;
 #pragma unroll
       for (int r = 0; r < R; ++r) w[r][j] = from_lane(ln.to_operand, wt.w[r][j]);
 #pragma unroll
-      for (int v = 0; v < kXR; ++v)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) xv[v][m][j] = x.get(ln, v, m, j);
+      for (int m = 0; m < MT; ++m) xv[m][j] = x.get(ln, m, j);
     }
     if (!MAYBE || nx >= 0) x.template load_all<false>(xp, nx, kStep);
     if (!MAYBE || nw >= 0) load<false>(wt, mat, rows, ln, nw, kStep);
@@ -315,18 +310,16 @@ struct Dense {
     for (int j = 0; j < 4; ++j) {
       if (TAIL && 32 * j >= lim) break;
 #pragma unroll
-      for (int v = 0; v < kXR; ++v)
+      for (int m = 0; m < MT; ++m) {
+        bf16x8 xo;
+        if constexpr (k8) xo = widen8<x_is_i8(XK)>(xv[m][j]);
+        else xo = __builtin_bit_cast(bf16x8, xv[m][j]);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          bf16x8 xo;
-          if constexpr (k8) xo = widen8<x_is_i8(XK)>(xv[v][m][j]);
-          else xo = __builtin_bit_cast(bf16x8, xv[v][m][j]);
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            f32x4& d = kGrouped ? part[r][m] : acc[r][m];
-            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, __builtin_bit_cast(bf16x8, w[r][j]), d, 0, 0, 0);
-          }
+        for (int r = 0; r < R; ++r) {
+          f32x4& d = kGrouped ? part[r][m] : acc[r][m];
+          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, __builtin_bit_cast(bf16x8, w[r][j]), d, 0, 0, 0);
         }
+      }
     }
     if constexpr (kGrouped) {
 #pragma unroll
@@ -368,7 +361,6 @@ template <int G, int XK, int MT, int R, int P>
 struct Quant4 {
   static constexpr int kR = R, kMT = MT, kP = P;
   static constexpr bool kGrouped = x_grouped(XK);
-  static constexpr int kXR = XK == X_SPLIT ? 2 : 1;
   static constexpr bool k8 = x_is_8bit(XK);
   static constexpr bool kPairs = k8 && G >= 64;
   static constexpr int kGroups = kStep / G;     // groups of a step
@@ -384,9 +376,9 @@ struct Quant4 {
   };
   struct Row {
     uint32_t w, s;
-    __device__ __forceinline__ void set(const Mat& m, int row, int srow, const Lanes& ln) {
+    __device__ __forceinline__ void set(const Mat& m, int row, const Lanes& ln) {
       w = (uint32_t)row * (uint32_t)m.stride + 16 * ln.piece();
-      s = (uint32_t)srow * (uint32_t)m.gstride;
+      s = (uint32_t)row * (uint32_t)m.gstride;
     }
   };
   struct Weights {
@@ -400,46 +392,53 @@ struct Quant4 {
 
   // lim: k of the step that exist; scales of the others are not read
   static __device__ __forceinline__ void load_aux(Aux& a, const Mat& mat, const Row (&rows)[R], const XPtr<MT>& xp, int step, int lim) {
-    const uint32_t g0 = (uint32_t)step * kGroups;
+    const char* const sb = (const char*)mat.s;
+    const char* const zb = (const char*)mat.z;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const uint16_t* sp = mat.s + (rows[r].s + (uint64_t)g0);
-      const uint8_t* zp = mat.z + (rows[r].s + (uint64_t)g0);
-      a.z[r] = 0x08080808u;
+      const uint32_t at = rows[r].s + (uint32_t)step * kGroups;
       if (lim < kStep) {
 #pragma unroll
         for (int i = 0; i < (kGroups + 1) / 2; ++i) a.s[r][i] = 0;
 #pragma unroll
         for (int h = 0; h < kGroups; ++h) {
           if (G * h >= lim) break;
-          a.s[r][h / 2] |= (uint32_t)sp[h] << (16 * (h % 2));
+          a.s[r][h / 2] |= (uint32_t)*(const uint16_t*)(sb + 2 * (at + h)) << (16 * (h % 2));
         }
-        if (mat.z) {
-          a.z[r] = 0;
+      } else if constexpr (kGroups == 4) {
+        const u32x2 v = *(const u32x2_a1*)(sb + 2 * at);
+        a.s[r][0] = v[0]; a.s[r][1] = v[1];
+      } else if constexpr (kGroups == 2) {
+        a.s[r][0] = *(const u32_a1*)(sb + 2 * at);
+      } else {
+        a.s[r][0] = *(const uint16_t*)(sb + 2 * at);
+      }
+      a.z[r] = 0;
+      if (mat.z) {
+        if (lim < kStep) {
 #pragma unroll
           for (int h = 0; h < kGroups; ++h) {
             if (G * h >= lim) break;
-            a.z[r] |= (uint32_t)zp[h] << (8 * h);
+            a.z[r] |= (uint32_t)*(const uint8_t*)(zb + (at + h)) << (8 * h);
           }
-        }
-      } else {
-        if constexpr (kGroups == 4) {
-          const u32x2 v = *(const u32x2_a1*)sp;
-          a.s[r][0] = v[0]; a.s[r][1] = v[1];
-          if (mat.z) a.z[r] = *(const u32_a1*)zp;
-        } else if constexpr (kGroups == 2) {
-          a.s[r][0] = *(const u32_a1*)sp;
-          if (mat.z) a.z[r] = *(const u16_a1*)zp;
         } else {
-          a.s[r][0] = *sp;
-          if (mat.z) a.z[r] = *zp;
+          if constexpr (kGroups == 4) a.z[r] = *(const u32_a1*)(zb + at);
+          else if constexpr (kGroups == 2) a.z[r] = *(const u16_a1*)(zb + at);
+          else a.z[r] = *(const uint8_t*)(zb + at);
         }
       }
-      if constexpr (kGroups == 1) a.s[r][0] = a.s[r][0] << 16 | (a.z[r] & 0xffu);      // one word carries both
     }
     if constexpr (kGrouped) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) a.xs[m] = xp.scale[xp.at[m] + (uint32_t)step];
+      for (int m = 0; m < MT; ++m) a.xs[m] = *(const float*)((const char*)xp.scale + 4 * (xp.at[m] + (uint32_t)step));
+    }
+  }
+  // What was loaded, ready for use; one word carries a group's scale and zero point where a step has one group.
+  static __device__ __forceinline__ void finish_aux(Aux& a, const Mat& mat) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      a.z[r] = mat.z ? a.z[r] : 0x08080808u;
+      if constexpr (kGroups == 1) a.s[r][0] = a.s[r][0] << 16 | (a.z[r] & 0xffu);
     }
   }
 
@@ -481,7 +480,7 @@ struct Quant4 {
     u32x4 w[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) w[r] = gather(wt.w[r], ln);
-    const int row = 64 * t + 4 * (ln.lane & 15);          // quarter t's lane of this lane's weight row
+    const int row = 16 * (ln.lane & 15) + 4 * t;          // the lane with step t's of this lane's weight row
     uint32_t sw[R][(kGroups + 1) / 2], zw[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -502,17 +501,15 @@ struct Quant4 {
 #pragma unroll
       for (int f = 0; f < kWords; f += kBlock) {
         const int j = h * kWords + f;
-        typename X::V xv[kXR][MT][kBlock];
+        typename X::V xv[MT][kBlock];
 #pragma unroll
-        for (int v = 0; v < kXR; ++v)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < kBlock; ++i) {
-              xv[v][m][i] = x.get(ln, v, m, j + i);
-              if constexpr (k8) xv[v][m][i] = even_odd(xv[v][m][i][0], xv[v][m][i][1]);
-              else if constexpr (XK != X_SPLIT) xv[v][m][i] = paired(xv[v][m][i]);
-            }
+          for (int i = 0; i < kBlock; ++i) {
+            xv[m][i] = x.get(ln, m, j + i);
+            if constexpr (k8) xv[m][i] = even_odd(xv[m][i][0], xv[m][i][1]);
+            else if constexpr (XK != X_PACKED) xv[m][i] = paired(xv[m][i]);
+          }
         // both words of a load have been taken
         if ((!kPairs || kBlock == 2 || j % 2 == 1) && (!MAYBE || nx >= 0)) x.template load<false>(j, xp, nx, kStep);
         if constexpr (x_is_i8(XK)) {
@@ -528,39 +525,35 @@ struct Quant4 {
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
               if constexpr (kBlock == 1)
-                part[r][m] = __builtin_amdgcn_mfma_i32_16x16x32_i8(as_long(xv[0][m][0]), as_long(d[0]), part[r][m], 0, 0, 0);
+                part[r][m] = __builtin_amdgcn_mfma_i32_16x16x32_i8(as_long(xv[m][0]), as_long(d[0]), part[r][m], 0, 0, 0);
               else
-                part[r][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(as_i32x4(xv[0][m][0], xv[0][m][kBlock - 1]),
+                part[r][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(as_i32x4(xv[m][0], xv[m][kBlock - 1]),
                                                                    as_i32x4(d[0], d[kBlock - 1]), part[r][m], 0, 0, 0);
             }
           }
         } else if constexpr (x_is_e4m3(XK)) {
 #pragma unroll
           for (int m = 0; m < MT; ++m)
-            sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(as_long(xv[0][m][0]), 0x3838383838383838l, sum[m], 0, 0, 0);
+            sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(as_long(xv[m][0]), 0x3838383838383838l, sum[m], 0, 0, 0);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const long b = as_long(bytes8(w[r][j]));
 #pragma unroll
             for (int m = 0; m < MT; ++m)
-              part[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(as_long(xv[0][m][0]), b, part[r][m], 0, 0, 0);
+              part[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(as_long(xv[m][0]), b, part[r][m], 0, 0, 0);
           }
         } else {
           const u32x4 one = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
 #pragma unroll
-          for (int v = 0; v < kXR; ++v)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-              sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv[v][m][0]), __builtin_bit_cast(bf16x8, one),
-                                                               sum[m], 0, 0, 0);
+          for (int m = 0; m < MT; ++m)
+            sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv[m][0]), __builtin_bit_cast(bf16x8, one),
+                                                             sum[m], 0, 0, 0);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const bf16x8 b = frag16(w[r][j]);
 #pragma unroll
             for (int m = 0; m < MT; ++m)
-#pragma unroll
-              for (int v = 0; v < kXR; ++v)
-                part[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv[v][m][0]), b, part[r][m], 0, 0, 0);
+              part[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv[m][0]), b, part[r][m], 0, 0, 0);
           }
         }
         // a word at a time: all of a step at once would not fit in the registers
@@ -575,10 +568,10 @@ struct Quant4 {
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const float z = (float)((zw[r] >> (8 * h)) & 0xffu);
-            const float s = kGroups == 1 || h % 2 ? bf16_hi(sw[r][h / 2]) : bf16_lo(sw[r][h / 2]);
+            const float s = (kGroups == 1 || h % 2 ? bf16_hi(sw[r][h / 2]) : bf16_lo(sw[r][h / 2])) * (x_is_e4m3(XK) ? 512.0f : 1.0f);
             float v;
             if constexpr (x_is_i8(XK)) v = (float)part[r][m][i];
-            else if constexpr (x_is_e4m3(XK)) v = __builtin_fmaf(sum[m][i], z * -0x1p-9f, part[r][m][i]) * 512.0f;
+            else if constexpr (x_is_e4m3(XK)) v = __builtin_fmaf(sum[m][i], z * -0x1p-9f, part[r][m][i]);
             else v = __builtin_fmaf(sum[m][i], -128.0f - z, part[r][m][i]);
             acc[r][m][i] = __builtin_fmaf(v, kGrouped ? s * xs : s, acc[r][m][i]);
           }
@@ -599,12 +592,13 @@ __device__ __forceinline__ void run_steps(f32x4 (&acc)[Prod::kR][Prod::kMT], con
   typename Prod::Weights w[P];
   typename Prod::X x;
   typename Prod::Aux cur, nxt;
-  auto aux = [&](typename Prod::Aux& a, int i) { Prod::load_aux(a, mat, rows, xp, first + by * min(i + ln.quarter, n - 1), kStep); };
+  auto aux = [&](typename Prod::Aux& a, int i) { Prod::load_aux(a, mat, rows, xp, first + by * min(i + ln.piece(), n - 1), kStep); };
   aux(cur, 0);
   x.template load_all<false>(xp, first, kStep);
 #pragma unroll
   for (int p = 0; p < P; ++p)
     if (p < n) Prod::template load<false>(w[p], mat, rows, ln, first + by * p, kStep);
+  Prod::finish_aux(cur, mat);
   int i = 0;
   for (; i + 4 + P <= n; i += 4) {      // no branches in here: the compiler's waits count the loads in flight
     aux(nxt, i + 4);
@@ -612,7 +606,9 @@ __device__ __forceinline__ void run_steps(f32x4 (&acc)[Prod::kR][Prod::kMT], con
     for (int t = 0; t < 4; ++t)
       Prod::template consume<false, false>(w[t % P], x, cur, t, acc, mat, rows, xp, ln, kStep, first + by * (i + t + 1),
                                            first + by * (i + t + P));
+    __builtin_amdgcn_sched_barrier(0);
     cur = nxt;
+    Prod::finish_aux(cur, mat);
   }
   for (; i < n; i += 4) {
     if (i + 4 < n) aux(nxt, i + 4);
@@ -623,6 +619,7 @@ __device__ __forceinline__ void run_steps(f32x4 (&acc)[Prod::kR][Prod::kMT], con
                                     i + t + P < n ? first + by * (i + t + P) : -1);
     }
     cur = nxt;
+    Prod::finish_aux(cur, mat);
   }
 }
 // The same for the last `lim` < 128 k of the rows, which are those of `step`.
@@ -634,6 +631,7 @@ __device__ __forceinline__ void run_tail(f32x4 (&acc)[Prod::kR][Prod::kMT], cons
   typename Prod::X x;
   typename Prod::Aux aux;
   Prod::load_aux(aux, mat, rows, xp, step, lim);
+  Prod::finish_aux(aux, mat);
   x.template load_all<true>(xp, step, lim);
   Prod::template load<true>(w, mat, rows, ln, step, lim);
   Prod::template consume<true, true>(w, x, aux, 0, acc, mat, rows, xp, ln, lim, -1, -1);

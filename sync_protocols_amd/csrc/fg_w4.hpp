@@ -39,8 +39,8 @@ __device__ __forceinline__ void join_tile(const f32x4 (&acc)[R][MT], int m, floa
   __syncthreads();
 }
 
-template <int G, int XK, int MT, int R, int P, int W>
-__global__ __launch_bounds__(64 * W) void w4_linear_kernel(W4Args a) {
+template <int G, int XK, int MT, int R, int P, int W, int MIN_WAVES = (W > 8 ? W / 4 : 2)>
+__global__ __launch_bounds__(64 * W, MIN_WAVES) void w4_linear_kernel(W4Args a) {
   __shared__ float red[W * 16 * (16 * R + 1)];
   typedef Quant4<G, XK, MT, R, P> Prod;
   const Lanes ln;
@@ -51,15 +51,16 @@ __global__ __launch_bounds__(64 * W) void w4_linear_kernel(W4Args a) {
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int last = a.n - 1 - n0;
-    rows[r].set(mat, min(16 * r + ln.load_row(), last), min(16 * r + (ln.lane & 15), last), ln);
+    rows[r].set(mat, min(16 * r + ln.load_row(), last), ln);
   }
   XPtr<MT> xp;
   xp.base = a.x + t0 * a.ldx;
   xp.scale = a.xs + t0 * a.xs_stride;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    xp.row[m] = (uint32_t)min(16 * m + ln.load_row(), a.rows - 1 - t0) * (uint32_t)a.ldx + x_piece<G, XK>(ln);
-    xp.at[m] = (uint32_t)min(16 * m + (ln.lane & 15), a.rows - 1 - t0) * (uint32_t)a.xs_stride;
+    const uint32_t row = (uint32_t)min(16 * m + ln.load_row(), a.rows - 1 - t0);
+    xp.row[m] = row * (uint32_t)a.ldx + x_piece<G, XK>(ln);
+    xp.at[m] = row * (uint32_t)a.xs_stride;
   }
   f32x4 acc[R][MT];
   clear<Prod>(acc);
