@@ -451,6 +451,8 @@ enum { FG_SCORE_SOFTMAX = 0, FG_SCORE_SIGMOID = 1 };
 
 #define FG_NORM_MAX_N 65536
 #define FG_W4_MAX_ROWS 1048576
+#define FG_FEW_MAX_SIZE 16777216        /* n and k of fg_w4_linear, K and F of fg_moe_few */
+#define FG_FEW_MAX_ROW_BYTES 67108864   /* distance of two activation rows: less than this */
 #define FG_MOE_FEW_TOKENS 64
 #define FG_MOE_FEW_TOPK 16
 #define FG_MOE_FEW_EXPERTS 1024
@@ -487,12 +489,13 @@ fg_status fg_moe_route(const void* logits, int64_t ld, int32_t logits_type, int6
  *   x:       [rows][ldx] bf16, or FG_I8 / FG_E4M3 codes with fp32 x_scale xs, one
  *            per row (x_group 0: [rows]) or per 128 columns (x_group 128:
  *            [rows][k / 128], k % 128 == 0), as fg_add_rmsnorm writes them. Rows
- *            start on 16-byte (bf16) or 8-byte boundaries: ldx % 8 == 0
+ *            start on 16-byte (bf16) or 8-byte boundaries: ldx % 8 == 0, and
+ *            less than FG_FEW_MAX_ROW_BYTES apart
  *   w:       uint8 [n][k / 2], 16-byte aligned; element k of a row is the low
  *            (even k) or high nibble of byte k / 2
  *   w_scale: bf16 [n][k / group]; group 32, 64 or 128, k % group == 0
  *   w_zero:  uint8 [n][k / group] or NULL (8 everywhere)
- *   bias:    bf16 [n] or NULL;  out: bf16 [rows][ldo], any n
+ *   bias:    bf16 [n] or NULL;  out: bf16 [rows][ldo]; n any up to FG_FEW_MAX_SIZE
  *   rows:    any up to FG_W4_MAX_ROWS; made for 1 to 64 (more re-read the weights)
  * An infinity in x gives NaN in the whole row of out. */
 fg_status fg_w4_linear(const void* x, int64_t ldx, int32_t x_type, const float* x_scale, int32_t x_group, const void* w,
@@ -507,14 +510,16 @@ fg_status fg_moe_few_bytes(int32_t tokens, int32_t k, int32_t F, int64_t* bytes)
  *   y[t] = bf16( sum_j weights[t][j] * W2[e] (silu(W1[e][0:F] x[t]) * (W1[e][F:2F] x[t])) ),
  *   e = topk[t][j] - expert_base, over the picks with 0 <= e < n_local; a token
  *   with none gets zeros (other ranks' experts add their own terms).
- * The picked experts' weights are read once for up to 16 tokens an expert.
+ * The picked experts' weights are read once for up to 16 tokens an expert (from
+ * memory; more tokens find them in the caches as far as those reach).
  *   x, ldx, x_type, x_scale, x_group: activations [tokens][K], as fg_w4_linear
  *   w1, w2:  group 0: bf16 [n_local][2F][K] and [n_local][K][F], 16-byte aligned,
  *            scales and zeros NULL; group 32, 64, 128: 4-bit weights of the same
  *            rows in the layout of fg_w4_linear with their scales and zeros (or NULL)
  *   topk:    int32 [tokens][k], distinct per token (negative: no pick);  weights: fp32 [tokens][k]
  *   tokens <= FG_MOE_FEW_TOKENS, k <= FG_MOE_FEW_TOPK, n_local <= FG_MOE_FEW_EXPERTS,
- *   K and F multiples of 32 and of group
+ *   K and F multiples of 32 and of group, up to FG_FEW_MAX_SIZE; the F gate rows of
+ *            an expert take less than 4 GB
  *   workspace: fg_moe_few_bytes(tokens, k, F) bytes, 16-byte aligned, contents
  *            free; calls that may overlap need one each
  *   y:       bf16 [tokens][ldy] */

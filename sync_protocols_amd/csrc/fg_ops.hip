@@ -27,7 +27,8 @@ int pow2_at_least(int v) {
 bool rows_ok(const void* x, int64_t ldx, int32_t type, const float* scale, int32_t group, int32_t k) {
   if (!x || (type != FG_BF16 && type != FG_I8 && type != FG_E4M3)) return false;
   const int bytes = type == FG_BF16 ? 2 : 1;
-  if (ldx < k || ldx % 8 || !aligned(x, 8 * bytes)) return false;
+  // a lane's distance from a tile's first row, up to 64 rows on, is 32 bits
+  if (ldx < k || ldx % 8 || ldx * bytes >= FG_FEW_MAX_ROW_BYTES || !aligned(x, 8 * bytes)) return false;
   if (type == FG_BF16) return !scale && group == 0;
   return scale && aligned(scale, 4) && (group == 0 || (group == 128 && k % 128 == 0));
 }
@@ -76,17 +77,34 @@ void launch_w4_tile(const W4Args& a, hipStream_t stream) {
   hipLaunchKernelGGL((w4_linear_kernel<G, XK, MT, R, P, W>), grid, dim3(64 * W), 0, stream, a);
 }
 
-// The tile of 16 MT rows by 16 R columns. Up to 16 rows one column tile a
-// workgroup spreads the weights evenly over the compute units (5 x 8199 x 7200:
-// 18 us, with two 21 us); where that leaves most of them with one workgroup or
-// none, 16 waves share its steps. More rows take two column tiles, so that the
-// activations are read half as often (64 x 8192 x 8192: 22 us, with one 29 us).
+// The tile of 16 MT rows by 16 R columns. A larger one reads weights and
+// activations fewer times, but a workgroup takes a compute unit's time whether or
+// not the others have one: what counts is how many rounds of 256 workgroups there
+// are, each as long as a tile's cost (measured at k = 4096 and 8192, in units of the
+// smallest). Us for 8-bit rows, groups of 64, k = 8192, tiles (1,1) (1,2) (2,2) (4,2):
+//   12 x 4096: 7.6 9.0 - -;  12 x 8192: 10.9 10.0 - -;  28 x 8192: 16.1 16.1 12.6 -;
+//   60 x 4096: - - 12.7 17.0;  60 x 8192: - - 20.6 17.7.
+// The largest does not fit in the registers for groups of 32.
 template <int G, int XK>
 void launch_w4(const W4Args& a, hipStream_t stream) {
-  if (a.rows > 32) launch_w4_tile<G, XK, 4, 2, 2, 8>(a, stream);
-  else if (a.rows > 16) launch_w4_tile<G, XK, 2, 2, 1, 8>(a, stream);
-  else if (a.n <= 16 * kCUs) launch_w4_tile<G, XK, 1, 1, 1, 16>(a, stream);
-  else launch_w4_tile<G, XK, 1, 1, 2, 8>(a, stream);
+  auto rounds = [&](int mt, int r) {
+    const int64_t n = (int64_t)((a.n + 16 * r - 1) / (16 * r)) * ((a.rows + 16 * mt - 1) / (16 * mt));
+    return (n + kCUs - 1) / kCUs;
+  };
+  const float cost[4] = {1.0f * rounds(1, 1), 1.5f * rounds(1, 2), 2.2f * rounds(2, 2), 3.7f * rounds(4, 2)};
+  int best = 0;
+  for (int i = 1; i < (G == 32 ? 3 : 4); ++i)
+    if (cost[i] < cost[best]) best = i;
+  switch (best) {
+    case 0:       // one workgroup or none a compute unit: more waves where they have enough steps (1 x 2048 x 7168: 6.4 us, with 8 7.0)
+      if (rounds(1, 1) == 1 && a.k >= 48 * kStep) launch_w4_tile<G, XK, 1, 1, 2, 16>(a, stream);
+      else launch_w4_tile<G, XK, 1, 1, 2, 8>(a, stream);
+      break;
+    case 1: launch_w4_tile<G, XK, 1, 2, 2, 8>(a, stream); break;
+    case 2: launch_w4_tile<G, XK, 2, 2, 1, 8>(a, stream); break;
+    default:
+      if constexpr (G != 32) launch_w4_tile<G, XK, 4, 2, 1, 8>(a, stream);
+  }
 }
 
 template <int G>
@@ -98,8 +116,8 @@ void launch_w4(const W4Args& a, int type, bool grouped, hipStream_t stream) {
 
 // More than 16 rows an expert on average, were all picks here: two row tiles, so
 // that an expert's weights are still read once or twice; else one, whose fewer
-// registers leave room for more waves (64 tokens over 64 experts: 230 us, with two
-// row tiles 258 us).
+// registers leave room for more waves (64 tokens over 64 experts: 214 us, with two
+// row tiles 227 us).
 bool many_rows(const MoeArgs& a) { return a.tokens > 16 && a.tokens * a.k > 16 * a.n_local; }
 
 template <int G, int XK, int MT, int C, int P, int W>
@@ -109,10 +127,20 @@ void launch_moe_up_tile(const MoeArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((moe_up_kernel<G, XK, MT, C, P, W>), grid, dim3(64 * W), 0, stream, a);
 }
 
+// 4-bit weights: two column tiles share the loads of x (64 tokens over 64 experts:
+// 214 us, with one 240 us), where there are workgroups enough; for groups of 32 they
+// do not fit in the registers.
 template <int G, int XK>
 void launch_moe_up(const MoeArgs& a, hipStream_t stream) {
-  if constexpr (G == 0) many_rows(a) ? launch_moe_up_tile<G, XK, 2, 1, 2, 4>(a, stream) : launch_moe_up_tile<G, XK, 1, 1, 2, 4>(a, stream);
-  else many_rows(a) ? launch_moe_up_tile<G, XK, 2, 2, 2, 8>(a, stream) : launch_moe_up_tile<G, XK, 1, 2, 1, 4>(a, stream);
+  if constexpr (G == 0) {
+    many_rows(a) ? launch_moe_up_tile<G, XK, 2, 1, 2, 4>(a, stream) : launch_moe_up_tile<G, XK, 1, 1, 2, 4>(a, stream);
+  } else {
+    const int picks = a.tokens * a.k;
+    if (many_rows(a)) launch_moe_up_tile<G, XK, 2, 1, 1, 8>(a, stream);
+    else if (G == 32 || (picks < a.n_local ? picks : a.n_local) * (int64_t)(a.F / 32) < 2 * kCUs)
+      launch_moe_up_tile<G, XK, 1, 1, 2, 8>(a, stream);
+    else if constexpr (G != 32) launch_moe_up_tile<G, XK, 1, 2, 2, 4>(a, stream);
+  }
 }
 
 template <int G, int MT, int R, int P, int W>
@@ -121,13 +149,16 @@ void launch_moe_down_tile(const MoeArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((moe_down_kernel<G, MT, R, P, W>), dim3((a.K + 16 * R - 1) / (16 * R)), dim3(64 * W), lds, stream, a);
 }
 
-// Two column tiles halve the reads of h (64 tokens over 64 experts: 192 us, with
-// one 283 us), unless there are too few columns to give every second compute unit
-// a workgroup then.
+// Two column tiles halve the reads of h (64 tokens over 64 experts: 170 us, with
+// one 241 us), unless there are too few columns to give every second compute unit
+// a workgroup then. Entries of up to 16 picks where an expert may have more than 8
+// (one row tile there: 200 us).
 template <int G>
 void launch_moe_down(const MoeArgs& a, hipStream_t stream) {
-  if (many_rows(a)) launch_moe_down_tile<G, 4, 2, 1, 8>(a, stream);
-  else if (a.K < 32 * kCUs / 2) launch_moe_down_tile<G, 1, 1, 1, 8>(a, stream);
+  const bool few_columns = a.K < 32 * kCUs / 2;
+  if (a.tokens > 16) few_columns ? launch_moe_down_tile<G, 2, 1, 2, 8>(a, stream) : launch_moe_down_tile<G, 2, 2, 2, 8>(a, stream);
+  else if (few_columns) launch_moe_down_tile<G, 1, 1, 1, 8>(a, stream);
+  else if constexpr (G == 0) launch_moe_down_tile<G, 1, 2, 1, 16>(a, stream);
   else launch_moe_down_tile<G, 1, 2, 2, 8>(a, stream);
 }
 
@@ -197,7 +228,7 @@ fg_status fg_moe_route(const void* logits, int64_t ld, int32_t logits_type, int6
 fg_status fg_w4_linear(const void* x, int64_t ldx, int32_t x_type, const float* x_scale, int32_t x_group, const void* w,
                        const void* w_scale, const void* w_zero, int32_t group, const void* bias, void* out, int64_t ldo,
                        int64_t rows, int32_t n, int32_t k, hipStream_t stream) {
-  if (rows < 0 || rows > FG_W4_MAX_ROWS || n < 1 || k < 1 || !w4_ok(w, w_scale, group, k)) return FG_EINVAL;
+  if (rows < 0 || rows > FG_W4_MAX_ROWS || n < 1 || k < 1 || n > FG_FEW_MAX_SIZE || k > FG_FEW_MAX_SIZE || !w4_ok(w, w_scale, group, k)) return FG_EINVAL;
   if (rows == 0) return FG_OK;
   if (!rows_ok(x, ldx, x_type, x_scale, x_group, k) || !out || ldo < n || !aligned(out, 2) || !aligned(bias, 2)) return FG_EINVAL;
   W4Args a{};
@@ -224,8 +255,10 @@ fg_status fg_moe_few(const void* x, int64_t ldx, int32_t x_type, const float* x_
                      int32_t expert_base, int32_t n_local, int32_t K, int32_t F, void* workspace, int64_t workspace_bytes,
                      void* y, int64_t ldy, hipStream_t stream) {
   if (tokens < 0 || tokens > FG_MOE_FEW_TOKENS || k < 1 || k > FG_MOE_FEW_TOPK || n_local < 1 || n_local > FG_MOE_FEW_EXPERTS ||
-      expert_base < 0 || expert_base > 0x7fffffff - FG_MOE_FEW_EXPERTS || K < 1 || F < 1 || K % 32 || F % 32)
+      expert_base < 0 || expert_base > 0x7fffffff - FG_MOE_FEW_EXPERTS || K < 1 || F < 1 || K > FG_FEW_MAX_SIZE || F > FG_FEW_MAX_SIZE || K % 32 || F % 32)
     return FG_EINVAL;
+  // the distance from a gate row to its up row, in bytes, is 32 bits
+  if (((int64_t)F + 32) * K * (group ? 1 : 4) / 2 > 0xffffffff) return FG_EINVAL;
   if (group == 0) {
     if (!w1 || !w2 || w1_scale || w2_scale || w1_zero || w2_zero || !aligned(w1, 16) || !aligned(w2, 16)) return FG_EINVAL;
   } else if (!w4_ok(w1, w1_scale, group, K) || !w4_ok(w2, w2_scale, group, F)) {

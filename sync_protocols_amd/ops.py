@@ -25,6 +25,7 @@ BF16, I8, E4M3, F32 = 0, 1, 2, 3
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 NORM_MAX_N = 65536
 W4_MAX_ROWS = 1048576
+FEW_MAX_SIZE, FEW_MAX_ROW_BYTES = 16777216, 67108864
 MOE_FEW_TOKENS, MOE_FEW_TOPK, MOE_FEW_EXPERTS = 64, 16, 1024
 
 

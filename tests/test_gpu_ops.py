@@ -357,3 +357,135 @@ def test_layer_in_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want), i
+
+
+# ------------------------------------------------ tiles, grids and distances
+# Every tile of the products: rows and columns that pick it, with the types, groups and zero points.
+@pytest.mark.parametrize("rows,n", [(1, 4096), (16, 4096), (9, 8192), (31, 8192), (32, 6001), (64, 8192), (63, 8177), (50, 4111), (129, 4096), (3, 8199)])
+@pytest.mark.parametrize("group,kind,x_group,zero", [(128, "bf16", 0, True), (64, "i8", 0, False), (32, "e4m3", 128, True), (32, "bf16", 0, True),
+                                                     (128, "i8", 128, False), (64, "e4m3", 0, True), (64, "bf16", 0, False)])
+def test_w4_tiles(rows, n, group, kind, x_group, zero):
+    run_w4(rows, n, 384, group, zero, kind, x_group, bias=True)
+
+
+@pytest.mark.parametrize("k", [6144, 6272, 8064])
+def test_w4_long_rows(k):
+    """Steps in every remainder of four and of the waves, rows that share cache lines."""
+    run_w4(4, 100, k + 32, 32, True, "bf16", 0)
+    run_w4(16, 100, k + 64, 64, False, "i8", 0)
+    run_w4(40, 100, k, 128, True, "e4m3", 128)
+
+
+@pytest.mark.parametrize("zero", [0, 15])
+def test_w4_extreme_codes(zero):
+    """Every code against every 8-bit activation code, by exact values: no product or sum is out of its type's range."""
+    k, n = 256, 32
+    q = torch.full((n, k // 2), 0xFF, dtype=torch.uint8)
+    q[::2] = 0
+    s, z = torch.ones(n, k // 64).bfloat16(), torch.full((n, k // 64), zero, dtype=torch.uint8)
+    for kind, top in (("i8", -127), ("e4m3", 448)):
+        x = torch.full((17, k), top, dtype=torch.float32).to(torch.int8 if kind == "i8" else torch.float8_e4m3fn)
+        got = ops.w4_linear(dev(x), ops.W4Weight(*dev(q, s, z)), x_scale=torch.ones(17, device=DEV))
+        want = x.double() @ R.w4_values(q, s, z).t()
+        R.close(got, want, R.BF16_HALF * want.abs(), kind)
+
+
+def test_w4_rows_far_apart():
+    """Rows a little less than 64 MiB apart, 40 of them: distances beyond 31 bits."""
+    g = R.gen(8)
+    w = R.make_w4(g, (), 48, 256, 64, True)
+    x = torch.randn(40, 256, generator=g).bfloat16()
+    big = torch.empty(40 * ((1 << 25) - 8), dtype=BF, device=DEV).view(40, -1)
+    big[:, :256] = x.to(DEV)
+    want = ops.w4_linear(dev(x), ops.W4Weight(*dev(*w)))
+    assert torch.equal(ops.w4_linear(big[:, :256], ops.W4Weight(*dev(*w))), want)
+
+
+def test_norm_and_route_with_grids_of_two_dimensions():
+    rows = 5_000_003
+    x = torch.randn(rows, 8, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).bfloat16()
+    gamma = torch.ones(8, dtype=BF, device=DEV)
+    y = ops.add_rmsnorm(x, gamma).y
+    for at in (0, 4 << 20, (4 << 20) - 1, rows - 1):
+        check_norm(ops.NormResult(None, y[at:at + 1], None, None), x[at:at + 1].cpu(), gamma.cpu(), None, 1e-6, "bf16", 0)
+    h = x.float()
+    want = h * torch.rsqrt((h * h).mean(1, keepdim=True) + 1e-6)
+    assert ((y.float() - want).abs() <= (R.BF16_HALF + 2 * NORM_U) * want.abs()).all()
+    rows = 17_000_001
+    l = torch.randint(-9, 10, (rows, 4), generator=torch.Generator(device=DEV).manual_seed(2), device=DEV, dtype=torch.int8).to(BF)
+    topk, w = ops.moe_route(l, 1, score="sigmoid", renorm=True)
+    want = 4 * l.float() - torch.arange(4, device=DEV)                   # ties: lowest index
+    assert torch.equal(topk[:, 0].long(), want.argmax(1)) and (w == 1).all()
+
+
+@pytest.mark.parametrize("n", [64, 130, 512])
+def test_norm_many_short_rows(n):
+    """A wave a row, four rows a workgroup, the last one not full; and outputs larger than the caches."""
+    for rows in (1, 3, 1025, 40_001):
+        g = R.gen(rows)
+        x, res, gamma = torch.randn(rows, n, generator=g).bfloat16(), torch.randn(rows, n, generator=g).bfloat16(), torch.randn(n, generator=g).bfloat16()
+        check_norm(ops.add_rmsnorm(dev(x), dev(gamma), residual=dev(res), out="i8", keep_bf16=True), x, gamma, res, 1e-6, "i8", 0)
+
+
+def test_norm_infinite_group_leaves_the_others():
+    x = torch.randn(3, 384, generator=R.gen(3)).bfloat16()
+    gamma = torch.ones(384).bfloat16()
+    gamma[130] = math.inf                                                # its group alone has an infinite scale
+    got = ops.add_rmsnorm(dev(x), dev(gamma), out="e4m3", group=128)
+    assert got.scale[:, 1].isinf().all()
+    gamma[130] = 1
+    want = ops.add_rmsnorm(dev(x), dev(gamma), out="e4m3", group=128)
+    for c in (0, 2):
+        assert torch.equal(got.scale[:, c], want.scale[:, c])
+        assert torch.equal(got.q[:, 128 * c:128 * c + 128].float(), want.q[:, 128 * c:128 * c + 128].float())
+
+
+@pytest.mark.parametrize("experts", [16, 17, 32, 33, 129, 256, 512, 513])
+def test_route_lane_shapes(experts):
+    for dtype in (torch.float32, BF):
+        logits = (4 * torch.randn(19, experts, generator=R.gen(experts))).to(dtype)
+        logits[::3] = logits[::3].round()                                # equal ones
+        k = min(experts, 40)
+        check_route(ops.moe_route(dev(logits), k), logits, k, "softmax", True, 1.0)
+        check_route(ops.moe_route(wide(logits, 3, 1), k, score="sigmoid"), logits, k, "sigmoid", True, 1.0)
+
+
+# Entries of every size in the second product: 1 to 64 picks of an expert, first rows at odd and even places.
+@pytest.mark.parametrize("tokens", [8, 9, 16, 17, 64])
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+def test_moe_uneven_experts(tokens, group):
+    topk = torch.stack([torch.tensor([0, 1 + t % 3, 4 + t % 5]) for t in range(tokens)]).int()
+    topk[::4, 2] = -1
+    run_moe(tokens, 256, 384, 9, 0, 3, group, True, "bf16" if group % 64 else "i8", topk=topk)
+
+
+def test_moe_wide():
+    """Two column tiles in both products, 16 and more tokens."""
+    run_moe(16, 4096, 128, 3, 0, 2, 0)
+    run_moe(33, 4128, 96, 3, 0, 1, 32, True)
+    run_moe(2, 4224, 256, 3, 0, 2, 128, False, "e4m3", 128)
+    run_moe(20, 256, 4096, 8, 0, 2, 64, True, "i8")
+
+
+def test_moe_weights_of_zero_infinity_and_nan():
+    g = R.gen(11)
+    x = torch.randn(6, 64, generator=g).bfloat16()
+    w1, w2 = torch.randn(4, 64, 64, generator=g).bfloat16(), torch.randn(4, 64, 32, generator=g).bfloat16()
+    topk = torch.tensor([[0, 1], [1, 2], [2, 3], [3, 0], [0, 2], [1, 3]], dtype=torch.int32)
+    tw = torch.rand(6, 2, generator=g)
+    clean = ops.moe_few(*dev(x, w1, w2, topk, tw))
+    tw[1, 0] = 0
+    x[3, 5], tw[4, 1] = math.inf, math.nan
+    got = ops.moe_few(*dev(x, w1, w2, topk, tw))
+    for t in (0, 2, 5):
+        assert torch.equal(got[t], clean[t])
+    assert got[4].isnan().all() and not got[3].isfinite().any() and got[1].isfinite().all()
+
+
+@pytest.mark.parametrize("group", [0, 64])
+def test_moe_more_than_32_picks_repeat_bit_for_bit(group):
+    topk = torch.stack([torch.tensor([2, t % 2, 3 + t % 4]) for t in range(64)]).int()
+    got, args = run_moe(64, 320, 192, 8, 0, 3, group, topk=topk)
+    first = got.clone()
+    for _ in range(5):
+        assert torch.equal(first, ops.moe_few(*args))

@@ -145,3 +145,43 @@ def test_binding_refuses(call):
     with pytest.raises(fg.FgError) as e:
         call()
     assert e.value.code == fg.EINVAL
+
+
+@pytest.mark.parametrize("kw", [dict(n=(1 << 24) + 1, ldo=(1 << 24) + 1), dict(k=(1 << 24) + 128, ldx=(1 << 24) + 128), dict(ldx=1 << 25),
+                                dict(ldx=1 << 26, t=1, xs=P)])
+def test_w4_refuses_what_its_distances_do_not_reach(kw):
+    assert _w4(**kw) == fg.EINVAL
+
+
+@pytest.mark.parametrize("kw", [dict(K=(1 << 24) + 32, ldx=(1 << 24) + 32, ldy=(1 << 24) + 32), dict(F=(1 << 24) + 32, wsb=1 << 40), dict(ldx=1 << 25),
+                                dict(K=32768, ldx=32768, ldy=32768, F=65536, wsb=1 << 40),
+                                dict(K=65536, ldx=65536, ldy=65536, F=1 << 17, wsb=1 << 40, g=64, s1=P, s2=P),
+                                dict(F=1 << 20, e=1024, wsb=1 << 40)])
+def test_moe_refuses_what_its_distances_and_grid_do_not_reach(kw):
+    assert _moe(**kw) == fg.EINVAL
+
+
+def test_limits_of_sizes_match_the_header():
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "fg.h")).read()
+    defs = {k: int(v) for k, v in re.findall(r"^#define FG_(\w+) (\d+)", src, re.M)}
+    assert ops.FEW_MAX_SIZE == defs["FEW_MAX_SIZE"] and ops.FEW_MAX_ROW_BYTES == defs["FEW_MAX_ROW_BYTES"]
+
+
+@pytest.mark.parametrize("call", [
+    lambda: ops.add_rmsnorm(None, _bf(8)),
+    lambda: ops.add_rmsnorm([1.0], _bf(8)),
+    lambda: ops.moe_route(_bf(2, 8), "2"),
+    lambda: ops.moe_route(_bf(2, 8), 2.5),
+    lambda: ops.w4_linear(_bf(2, 256), W, out=3),
+    lambda: ops.moe_few(_bf(2, 64), _bf(4, 64, 64), _bf(4, 64, 32), torch.zeros(2, 2, dtype=torch.int32), None),
+])
+def test_binding_refuses_other_types(call):
+    with pytest.raises(TypeError):
+        call()
+
+
+def test_binding_refuses_a_base_beyond_int32():
+    with pytest.raises(fg.FgError):
+        ops.moe_few(_bf(2, 64), _bf(4, 64, 64), _bf(4, 64, 32), torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, 2), expert_base=1 << 40)
