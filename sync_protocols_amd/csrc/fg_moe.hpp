@@ -108,8 +108,10 @@ __device__ __forceinline__ void moe_up_pass(const MoeArgs& a, int e, int f0, con
 template <int G, int XK, int MT, int C, int P, int W, int MIN_WAVES = (W > 8 ? W / 4 : 2)>
 __global__ __launch_bounds__(64 * W, MIN_WAVES) void moe_up_kernel(MoeArgs a) {
   __shared__ uint32_t bits[FG_MOE_FEW_EXPERTS / 32];
+  __shared__ uint16_t expert[kMaxPicks];   // of a pick; kElsewhere: not here
   __shared__ uint16_t list[kMaxPicks];
   __shared__ float red[W * 16 * (32 * C + 1)];
+  constexpr uint32_t kElsewhere = 0xffffu;
   const int tid = threadIdx.x, lane = tid & 63;
   const int picks = a.tokens * a.k, ft = (a.F + 16 * C - 1) / (16 * C);
   const int nth = blockIdx.x / ft, f0 = (blockIdx.x % ft) * 16 * C;
@@ -117,27 +119,29 @@ __global__ __launch_bounds__(64 * W, MIN_WAVES) void moe_up_kernel(MoeArgs a) {
   __syncthreads();
   for (int p = tid; p < picks; p += 64 * W) {
     const uint32_t e = local_expert(a.topk[p], a.base);
-    if (e < (uint32_t)a.n_local) atomicOr(&bits[e >> 5], 1u << (e & 31));
+    const bool here = e < (uint32_t)a.n_local;
+    expert[p] = (uint16_t)(here ? e : kElsewhere);
+    if (here) atomicOr(&bits[e >> 5], 1u << (e & 31));
   }
   __syncthreads();
   // the nth set bit, in every wave
   const uint32_t word = lane < FG_MOE_FEW_EXPERTS / 32 ? bits[lane] : 0;
-  int upto = __popc(word);
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(upto, d);
-    if (lane >= d) upto += o;
+  int e = -1;
+  for (int w = 0, left = nth; w < (a.n_local + 31) / 32; ++w) {
+    uint32_t rest = (uint32_t)__builtin_amdgcn_readlane((int)word, w);
+    if (left >= __popc(rest)) {
+      left -= __popc(rest);
+      continue;
+    }
+    for (; left > 0; --left) rest &= rest - 1;
+    e = 32 * w + __ffs(rest) - 1;
+    break;
   }
-  const unsigned long long past = __ballot(upto > nth);
-  if (!past) return;                       // fewer experts are picked; the same in every wave
-  const int at = __ffsll(past) - 1;
-  uint32_t rest = __shfl(word, at);
-  for (int i = nth - (__shfl(upto, at) - __popc(rest)); i > 0; --i) rest &= rest - 1;
-  const int e = __builtin_amdgcn_readfirstlane(32 * at + __ffs(rest) - 1);
+  if (e < 0) return;                       // fewer experts are picked; the same in every wave
   // its picks in order, and how many belong to experts before it: its place among h's rows
   int cnt = 0, start = 0;
   for (int p0 = 0; p0 < picks; p0 += 64) {
-    const uint32_t l = p0 + lane < picks ? local_expert(a.topk[p0 + lane], a.base) : 0xffffffffu;
+    const uint32_t l = p0 + lane < picks ? expert[p0 + lane] : kElsewhere;
     const unsigned long long here = __ballot(l == (uint32_t)e);
     if (tid < 64 && l == (uint32_t)e) list[cnt + __popcll(here & ((1ull << lane) - 1))] = (uint16_t)(p0 + lane);
     cnt += __popcll(here);
@@ -169,15 +173,19 @@ struct DownPlan {
 
 template <int MT, int W>
 __device__ __forceinline__ void down_plan(const MoeArgs& a, DownPlan& pl) {
+  constexpr int kMine = (kMaxPicks + 64 * W - 1) / (64 * W);
   const int tid = threadIdx.x, lane = tid & 63;
   const int picks = a.tokens * a.k;
+  uint32_t mine[kMine];                            // experts of picks tid + 64 W i, n_local or more: not here
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) mine[i] = tid + 64 * W * i < picks ? local_expert(a.topk[tid + 64 * W * i], a.base) : 0xffffffffu;
   for (int i = tid; i < a.n_local; i += 64 * W) pl.mask[i] = 0;
   if (tid == 0) pl.again = 0;
   __syncthreads();
-  for (int p = tid; p < picks; p += 64 * W) {
-    const uint32_t e = local_expert(a.topk[p], a.base);
-    const unsigned long long bit = 1ull << (p / a.k);
-    if (e < (uint32_t)a.n_local && (atomicOr(&pl.mask[e], bit) & bit)) pl.again = 1;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const unsigned long long bit = 1ull << (((tid + 64 * W * i) / a.k) & 63);
+    if (mine[i] < (uint32_t)a.n_local && (atomicOr(&pl.mask[mine[i]], bit) & bit)) pl.again = 1;
   }
   __syncthreads();
   const bool again = pl.again;     // some token picked an expert twice: the masks do not count it, so count here
@@ -191,18 +199,10 @@ __device__ __forceinline__ void down_plan(const MoeArgs& a, DownPlan& pl) {
     for (int e0 = 0; e0 < a.n_local; e0 += 64) {
       const int e = e0 + lane;
       const int c = e >= a.n_local ? 0 : again ? same_before(e, picks) : __popcll(pl.mask[e]);
-      auto before = [&](int v) {   // sum over the lanes before this one
-        int s = v;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-          const int o = __shfl_up(s, d);
-          if (lane >= d) s += o;
-        }
-        return s - v;
-      };
-      const int cs = before(c), start = at + cs, tile = start & ~1;
+      const int c_upto = lanes_before_and_own(c);
+      const int start = at + c_upto - c, tile = start & ~1;
       const int n = c ? (start + c - tile + 8 * MT - 1) / (8 * MT) : 0;
-      const int ns = before(n), first = ent + ns;
+      const int n_upto = lanes_before_and_own(n), first = ent + n_upto - n;
       for (int i = 0; i < n; ++i) {
         const int s = max(start, tile + 8 * MT * i);
         pl.ent_e[first + i] = (uint16_t)e;
@@ -210,17 +210,17 @@ __device__ __forceinline__ void down_plan(const MoeArgs& a, DownPlan& pl) {
         pl.ent_c[first + i] = (uint8_t)(min(start + c, tile + 8 * MT * (i + 1)) - s);
       }
       if (e < a.n_local) pl.start[e] = (uint16_t)start;
-      at += __shfl(cs + c, 63);
-      ent += __shfl(ns + n, 63);
+      at += __builtin_amdgcn_readlane(c_upto, 63);
+      ent += __builtin_amdgcn_readlane(n_upto, 63);
     }
     if (lane == 0) pl.entries = ent;
   }
   __syncthreads();
-  for (int p = tid; p < picks; p += 64 * W) {
-    const uint32_t e = local_expert(a.topk[p], a.base);
-    if (e >= (uint32_t)a.n_local) continue;
-    const int t = p / a.k;
-    pl.token[pl.start[e] + (again ? same_before(e, p) : __popcll(pl.mask[e] & ((1ull << t) - 1)))] = (uint8_t)t;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    if (mine[i] >= (uint32_t)a.n_local) continue;
+    const int p = tid + 64 * W * i, t = p / a.k;
+    pl.token[pl.start[mine[i]] + (again ? same_before(mine[i], p) : __popcll(pl.mask[mine[i]] & ((1ull << t) - 1)))] = (uint8_t)t;
   }
   __syncthreads();
 }

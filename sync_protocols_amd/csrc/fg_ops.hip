@@ -157,7 +157,7 @@ template <int G>
 void launch_moe_down(const MoeArgs& a, hipStream_t stream) {
   const bool few_columns = a.K < 32 * kCUs / 2;
   if (a.tokens > 16) few_columns ? launch_moe_down_tile<G, 2, 1, 2, 8>(a, stream) : launch_moe_down_tile<G, 2, 2, 2, 8>(a, stream);
-  else if (few_columns) launch_moe_down_tile<G, 1, 1, 1, 8>(a, stream);
+  else if (few_columns) launch_moe_down_tile<G, 1, 1, 1, 16>(a, stream);
   else if constexpr (G == 0) launch_moe_down_tile<G, 1, 2, 1, 16>(a, stream);
   else launch_moe_down_tile<G, 1, 2, 2, 8>(a, stream);
 }

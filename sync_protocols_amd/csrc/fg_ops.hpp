@@ -89,6 +89,17 @@ __device__ __forceinline__ uint32_t lanes_min(uint32_t v) {
   return lanes_reduce<L>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
 }
 
+// Sum over this lane and the lanes before it.
+__device__ __forceinline__ int lanes_before_and_own(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);      // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);      // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);      // row_bcast:31 into rows 2 and 3
+  return v;
+}
+
 // ------------------------------------------------------------- activations
 // X_PACKED: bf16 in operand order (the expert layer's own intermediate, see
 // PackedRows); X_I8G, X_E4M3G: 8-bit rows
