@@ -138,8 +138,8 @@ void launch_moe_up(const MoeArgs& a, hipStream_t stream) {
     const int picks = a.tokens * a.k;
     if (many_rows(a)) launch_moe_up_tile<G, XK, 2, 1, 1, 8>(a, stream);
     else if (G == 32 || (picks < a.n_local ? picks : a.n_local) * (int64_t)(a.F / 32) < 2 * kCUs)
-      launch_moe_up_tile<G, XK, 1, 1, 2, 8>(a, stream);
-    else if constexpr (G != 32) launch_moe_up_tile<G, XK, 1, 2, 2, 4>(a, stream);
+      launch_moe_up_tile<G, XK, 1, 1, 1, 8>(a, stream);
+    else if constexpr (G != 32) launch_moe_up_tile<G, XK, 1, 2, 1, 4>(a, stream);
   }
 }
 

@@ -39,7 +39,7 @@ class ExpertLayer:
 
     def __init__(self, wo: ops.W4Weight, gamma: torch.Tensor, router: torch.Tensor, w1, w2, top_k: int, *, expert_base: int = 0,
                  score: str = "softmax", eps: float = 1e-6, norm_out: str = "e4m3"):
-        self.wo, self.gamma, self.router_t, self.w1, self.w2 = wo, gamma, router.t().contiguous(), w1, w2
+        self.wo, self.gamma, self.router, self.w1, self.w2 = wo, gamma, router, w1, w2
         self.top_k, self.expert_base, self.score, self.eps, self.norm_out = top_k, expert_base, score, eps, norm_out
         self.group = 128 if norm_out != "bf16" and gamma.numel() % 128 == 0 else 0
         first = w2.q if isinstance(w2, ops.W4Weight) else w2
@@ -53,7 +53,7 @@ class ExpertLayer:
         """a bf16 [tokens, heads], residual bf16 [tokens, hidden]."""
         o = ops.w4_linear(a, self.wo)
         n = ops.add_rmsnorm(o, self.gamma, residual=residual, eps=self.eps, out=self.norm_out, group=self.group, keep_bf16=True)
-        topk, weights = ops.moe_route(n.y @ self.router_t, self.top_k, score=self.score)
+        topk, weights = ops.moe_route(torch.nn.functional.linear(n.y, self.router), self.top_k, score=self.score)
         x = n.y if self.norm_out == "bf16" else n.q
         y = ops.moe_few(x, self.w1, self.w2, topk, weights, expert_base=self.expert_base, x_scale=n.scale, workspace=workspace)
         return StepResult(y, n.sum)
@@ -156,7 +156,7 @@ def main(argv=None) -> None:
     torch.cuda.synchronize()
     o = ops.w4_linear(captured.a, layer.wo)
     n = ops.add_rmsnorm(o, layer.gamma, residual=captured.residual, eps=layer.eps)
-    topk, weights = ops.moe_route(n.y @ layer.router_t, layer.top_k, score=layer.score)
+    topk, weights = ops.moe_route(torch.nn.functional.linear(n.y, layer.router), layer.top_k, score=layer.score)
     want = plain_step(layer, captured.a, captured.residual, topk, weights)
     off = (got.y.float() - want.y).norm() / want.y.norm()
     print(f"{c.tokens} tokens, {c.local} of {c.experts} experts of {c.hidden} x {c.width}: graph equals calls: {torch.equal(got.y, again.y)}, "

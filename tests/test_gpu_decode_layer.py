@@ -16,7 +16,7 @@ def _inputs(tokens, heads, hidden, seed):
 
 def _picks(layer, a, residual):
     n = ops.add_rmsnorm(ops.w4_linear(a, layer.wo), layer.gamma, residual=residual, eps=layer.eps)
-    return ops.moe_route(n.y @ layer.router_t, layer.top_k, score=layer.score)
+    return ops.moe_route(torch.nn.functional.linear(n.y, layer.router), layer.top_k, score=layer.score)
 
 
 # Relative to the norm of y. bf16 roundings (2^-8 / sqrt(3) each at most, in the mean): o, the experts' input and y, all
@@ -38,7 +38,7 @@ def test_shares_of_experts_add_up():
     part = torch.zeros_like(whole)
     for base in (0, 4, 8):
         w1, w2 = (ops.W4Weight(w.q[base:base + 4], w.scale[base:base + 4]) for w in (layer.w1, layer.w2))
-        share = D.ExpertLayer(layer.wo, layer.gamma, layer.router_t.t(), w1, w2, 3, expert_base=base)
+        share = D.ExpertLayer(layer.wo, layer.gamma, layer.router, w1, w2, 3, expert_base=base)
         part += share.step(a, residual).y.float()
     assert (part - whole).abs().max() <= 4 * 2.0 ** -8 * whole.abs().max()
 
