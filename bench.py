@@ -42,10 +42,14 @@ TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic.json")
 COPY_BYTES = 1 << 29          # plain device copy used to calibrate the HBM byte counters
 
 
+# the decoding operators' own sources: no part of the fused kernel
+OPERATOR_SOURCES = ("fg_moe.hpp", "fg_norm.hpp", "fg_ops.hip", "fg_ops.hpp", "fg_route.hpp", "fg_torch.cpp", "fg_w4.hpp")
+
+
 def kernel_source_hash():
-    """sha256 of the code of the HIP sources and the C header (comments and
-    white space removed): traffic counters recorded for other code do not
-    describe the kernel that runs; an edited comment does not change it."""
+    """sha256 of the code of the fused kernel's HIP sources and the C header
+    (comments and white space removed): traffic counters recorded for other code
+    do not describe the kernel that runs; an edited comment does not change it."""
     import hashlib
     import re
 
@@ -56,7 +60,7 @@ def kernel_source_hash():
 
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "sync_protocols_amd", "csrc")
-    for name in sorted(os.listdir(csrc)):
+    for name in sorted(set(os.listdir(csrc)) - set(OPERATOR_SOURCES)):
         with open(os.path.join(csrc, name), encoding="utf-8") as f:
             h.update(name.encode() + b"\0" + code(f.read()))
     with open(os.path.join(ROOT, "include", "fg.h"), encoding="utf-8") as f:
