@@ -61,8 +61,9 @@ __device__ __forceinline__ void moe_up_pass(const MoeArgs& a, int e, int f0, con
   xp.scale = a.xs;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const uint32_t token = list[min(s0 + 16 * m + ln.load_row(), cnt - 1)] / a.k;
-    xp.row[m] = token * (uint32_t)a.ldx + x_piece<G, XK>(ln);
+    const int slot = s0 + 16 * m + ln.load_row();
+    const uint32_t token = list[min(slot, cnt - 1)] / a.k;
+    xp.row[m] = !Prod::kMasked || slot < cnt ? token * (uint32_t)a.ldx + x_piece<G, XK>(ln) : kNoRow;
     xp.at[m] = token * (uint32_t)a.xs_stride;
   }
   f32x4 acc[2 * C][MT];
@@ -240,8 +241,10 @@ __device__ __forceinline__ void moe_down_pass(const MoeArgs& a, int e, int s, in
   xp.base = a.h;
   xp.plane = a.plane;
 #pragma unroll
-  for (int m = 0; m < MT; ++m)                   // past the entry: its last row; results of rows outside it are not used
-    xp.row[m] = (uint32_t)PackedRows::at(min(2 * tile + 16 * m + col, 2 * (s + c) - 1), 8 * ln.quarter, a.plane);
+  for (int m = 0; m < MT; ++m) {
+    const int row = 2 * tile + 16 * m + col;
+    xp.row[m] = row >= 2 * s && row < 2 * (s + c) ? (uint32_t)PackedRows::at(row, 8 * ln.quarter, a.plane) : kNoRow;
+  }
   f32x4 acc[R][MT];
   clear<Prod>(acc);
   run_steps<Prod>(acc, mat, rows, xp, ln, step, 1, min(end, full) - step);

@@ -59,7 +59,7 @@ __global__ __launch_bounds__(64 * W, MIN_WAVES) void w4_linear_kernel(W4Args a) 
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const uint32_t row = (uint32_t)min(16 * m + ln.load_row(), a.rows - 1 - t0);
-    xp.row[m] = row * (uint32_t)a.ldx + x_piece<G, XK>(ln);
+    xp.row[m] = 16 * m + ln.load_row() < a.rows - t0 ? row * (uint32_t)a.ldx + x_piece<G, XK>(ln) : kNoRow;
     xp.at[m] = row * (uint32_t)a.xs_stride;
   }
   f32x4 acc[R][MT];
