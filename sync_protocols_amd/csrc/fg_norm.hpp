@@ -19,7 +19,6 @@ struct NormArgs {
   int32_t n, group;             // group: 0 (row) or 128
   int32_t q_type;
   float eps;
-  int32_t past;                 // outputs are larger than the caches: store past them
 };
 
 // Eight elements at p, `left` of them valid.
@@ -33,12 +32,14 @@ __device__ __forceinline__ void load8(const uint16_t* p, int left, float (&f)[8]
     for (int i = 0; i < 8; ++i) f[i] = i < left ? bf16_f(p[i]) : 0.0f;
   }
 }
-__device__ __forceinline__ void store8(uint16_t* p, int left, int past, const float (&f)[8]) {
+// PAST: past the caches, for outputs larger than them.
+template <bool PAST>
+__device__ __forceinline__ void store8(uint16_t* p, int left, const float (&f)[8]) {
   if (left >= 8) {
     u32x4 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = f2_bf16(f[2 * i], f[2 * i + 1]);
-    if (past) __builtin_nontemporal_store(v, (u32x4_a2*)p);
+    if constexpr (PAST) __builtin_nontemporal_store(v, (u32x4_a2*)p);
     else *(u32x4_a2*)p = v;
   } else {
 #pragma unroll
@@ -76,6 +77,7 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* buf) {
 // Eight codes of one row from element e on. inv = Q / a keeps |v| within a
 // rounding of Q and the clamp takes that rounding off; a row (group) with a NaN or an
 // infinity has a scale that says so, and its codes mean nothing.
+template <bool PAST>
 __device__ __forceinline__ void quantise8(const NormArgs& a, int64_t row, int e, int left, float inv, const float (&y)[8]) {
   u32x2 v = {0u, 0u};
   if (a.q_type == FG_I8) {
@@ -99,7 +101,7 @@ __device__ __forceinline__ void quantise8(const NormArgs& a, int64_t row, int e,
   }
   uint8_t* p = a.q + row * a.ldq + e;
   if (left >= 8) {
-    if (a.past) __builtin_nontemporal_store(v, (u32x2_a1*)p);
+    if constexpr (PAST) __builtin_nontemporal_store(v, (u32x2_a1*)p);
     else *(u32x2_a1*)p = v;
   } else {
 #pragma unroll
@@ -118,7 +120,7 @@ struct NormShape {
   static constexpr int kRows = W == 1 ? 4 : 1;
   static constexpr int kThreads = 64 * W * kRows;
 };
-template <int W, int V>
+template <int W, int V, bool PAST>
 __global__ __launch_bounds__(NormShape<W>::kThreads) void add_rmsnorm_kernel(NormArgs a) {
   __shared__ float sbuf[W];
   __shared__ uint32_t mbuf[W];
@@ -155,12 +157,12 @@ __global__ __launch_bounds__(NormShape<W>::kThreads) void add_rmsnorm_kernel(Nor
     const int e = 8 * (t + 64 * W * i);
     const int left = a.n - e;
     if (left > 0) {
-      if (a.sum) store8(a.sum + row * a.lds + e, left, a.past, h[i]);
+      if (a.sum) store8<PAST>(a.sum + row * a.lds + e, left, h[i]);
       float g[8];
       load8(a.gamma + e, left, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * rstd * g[j];
-      if (a.y) store8(a.y + row * a.ldy + e, left, a.past, h[i]);
+      if (a.y) store8<PAST>(a.y + row * a.ldy + e, left, h[i]);
       if (!a.q) continue;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -176,7 +178,7 @@ __global__ __launch_bounds__(NormShape<W>::kThreads) void add_rmsnorm_kernel(Nor
     if (a.q && a.group && left > 0) {
       const float m = __uint_as_float(amax), top = a.q_type == FG_I8 ? 127.0f : 448.0f;
       if ((t & 15) == 0) a.scale[row * (a.n / 128) + e / 128] = m / top;
-      quantise8(a, row, e, left, m > 0.0f ? top / m : 0.0f, h[i]);
+      quantise8<PAST>(a, row, e, left, m > 0.0f ? top / m : 0.0f, h[i]);
     }
     if (a.group) amax = 0;
   }
@@ -187,7 +189,7 @@ __global__ __launch_bounds__(NormShape<W>::kThreads) void add_rmsnorm_kernel(Nor
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = 8 * (t + 64 * W * i);
-      if (a.n - e > 0) quantise8(a, row, e, a.n - e, inv, h[i]);
+      if (a.n - e > 0) quantise8<PAST>(a, row, e, a.n - e, inv, h[i]);
     }
   }
 }

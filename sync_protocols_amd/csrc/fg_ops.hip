@@ -44,14 +44,20 @@ dim3 wide_grid(int64_t n) {
   return n <= x ? dim3((unsigned)n) : dim3((unsigned)x, (unsigned)((n + x - 1) / x));
 }
 
-template <int W>
-void launch_norm(int V, const NormArgs& a, hipStream_t stream) {
+template <int W, int V>
+void launch_norm(bool past, const NormArgs& a, hipStream_t stream) {
   const dim3 grid = wide_grid((a.rows + NormShape<W>::kRows - 1) / NormShape<W>::kRows), block(NormShape<W>::kThreads);
+  if (past) hipLaunchKernelGGL((add_rmsnorm_kernel<W, V, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((add_rmsnorm_kernel<W, V, false>), grid, block, 0, stream, a);
+}
+
+template <int W>
+void launch_norm(int V, bool past, const NormArgs& a, hipStream_t stream) {
   switch (V) {
-    case 1: hipLaunchKernelGGL((add_rmsnorm_kernel<W, 1>), grid, block, 0, stream, a); break;
-    case 2: hipLaunchKernelGGL((add_rmsnorm_kernel<W, 2>), grid, block, 0, stream, a); break;
-    case 4: hipLaunchKernelGGL((add_rmsnorm_kernel<W, 4>), grid, block, 0, stream, a); break;
-    default: hipLaunchKernelGGL((add_rmsnorm_kernel<W, 8>), grid, block, 0, stream, a); break;
+    case 1: launch_norm<W, 1>(past, a, stream); break;
+    case 2: launch_norm<W, 2>(past, a, stream); break;
+    default:                       // more than two only where a row has all 16 waves
+      if constexpr (W == 16) V == 4 ? launch_norm<W, 4>(past, a, stream) : launch_norm<W, 8>(past, a, stream);
   }
 }
 
@@ -194,19 +200,19 @@ fg_status fg_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64
   a.n = n; a.group = q ? q_group : 0; a.q_type = q_type; a.eps = eps;
   // Few rows: as many threads a row as it takes, for the latency. Many: 16 elements
   // a thread, and stores past the caches once the outputs exceed them (8192 x 7168,
-  // residual, e4m3: 77 us; with 8 and 32 elements a thread 85 and 84 us; with
+  // residual, e4m3: 80 us; with 8 and 32 elements a thread 85 and 84 us; with
   // ordinary stores 82 us).
-  a.past = rows * n > ((int64_t)32 << 20) / 2;
+  const bool past = rows * n > ((int64_t)32 << 20) / 2;
   const int nv = (n + 7) / 8, want = rows < 1024 ? 1 : 2;
   int W = pow2_at_least((nv + 64 * want - 1) / (64 * want));
   if (W > 16) W = 16;
   const int V = pow2_at_least((nv + 64 * W - 1) / (64 * W));
   switch (W) {
-    case 1: launch_norm<1>(V, a, stream); break;
-    case 2: launch_norm<2>(V, a, stream); break;
-    case 4: launch_norm<4>(V, a, stream); break;
-    case 8: launch_norm<8>(V, a, stream); break;
-    default: launch_norm<16>(V, a, stream); break;
+    case 1: launch_norm<1>(V, past, a, stream); break;
+    case 2: launch_norm<2>(V, past, a, stream); break;
+    case 4: launch_norm<4>(V, past, a, stream); break;
+    case 8: launch_norm<8>(V, past, a, stream); break;
+    default: launch_norm<16>(V, past, a, stream); break;
   }
   HIPCHK_LAUNCH();
   return FG_OK;
