@@ -122,8 +122,8 @@ void launch_w4(const W4Args& a, int type, bool grouped, hipStream_t stream) {
 
 // More than 16 rows an expert on average, were all picks here: two row tiles, so
 // that an expert's weights are still read once or twice; else one, whose fewer
-// registers leave room for more waves (64 tokens over 64 experts: 214 us, with two
-// row tiles 227 us).
+// registers leave room for more waves (64 tokens over 64 experts: 214 us when this
+// was chosen, with two row tiles 227 us).
 bool many_rows(const MoeArgs& a) { return a.tokens > 16 && a.tokens * a.k > 16 * a.n_local; }
 
 template <int G, int XK, int MT, int C, int P, int W>
@@ -134,7 +134,7 @@ void launch_moe_up_tile(const MoeArgs& a, hipStream_t stream) {
 }
 
 // 4-bit weights: two column tiles share the loads of x (64 tokens over 64 experts:
-// 214 us, with one 240 us), where there are workgroups enough; for groups of 32 they
+// 206 us, with one 224 us), where there are workgroups enough; for groups of 32 they
 // do not fit in the registers.
 template <int G, int XK>
 void launch_moe_up(const MoeArgs& a, hipStream_t stream) {
@@ -155,10 +155,10 @@ void launch_moe_down_tile(const MoeArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((moe_down_kernel<G, MT, R, P, W>), dim3((a.K + 16 * R - 1) / (16 * R)), dim3(64 * W), lds, stream, a);
 }
 
-// Two column tiles halve the reads of h (64 tokens over 64 experts: 170 us, with
-// one 241 us), unless there are too few columns to give every second compute unit
+// Two column tiles halve the reads of h (64 tokens over 64 experts: 167 us, with
+// one 239 us), unless there are too few columns to give every second compute unit
 // a workgroup then. Entries of up to 16 picks where an expert may have more than 8
-// (one row tile there: 200 us).
+// (one row tile there: 198 us).
 template <int G>
 void launch_moe_down(const MoeArgs& a, hipStream_t stream) {
   const bool few_columns = a.K < 32 * kCUs / 2;
