@@ -134,17 +134,20 @@ void launch_moe_up_tile(const MoeArgs& a, hipStream_t stream) {
 }
 
 // 4-bit weights: two column tiles share the loads of x (64 tokens over 64 experts:
-// 206 us, with one 224 us), where there are workgroups enough; for groups of 32 they
-// do not fit in the registers.
+// 206 us, with one 224 us), where there are eight workgroups and more for each place
+// on the compute units (15 tokens over 64 experts of 4480 x 1472: 46 us, with one 40);
+// for groups of 32 they do not fit in the registers. Four waves: with eight, a
+// workgroup's start and end are a larger share of it (12 tokens over 8 of 64 experts
+// of 1792 x 1536: 7.6 us, with eight 8.9).
 template <int G, int XK>
 void launch_moe_up(const MoeArgs& a, hipStream_t stream) {
   if constexpr (G == 0) {
     many_rows(a) ? launch_moe_up_tile<G, XK, 2, 1, 2, 4>(a, stream) : launch_moe_up_tile<G, XK, 1, 1, 2, 4>(a, stream);
   } else {
     const int picks = a.tokens * a.k;
+    const int64_t pairs = (picks < a.n_local ? picks : a.n_local) * (int64_t)(a.F / 32);
     if (many_rows(a)) launch_moe_up_tile<G, XK, 2, 1, 1, 8>(a, stream);
-    else if (G == 32 || (picks < a.n_local ? picks : a.n_local) * (int64_t)(a.F / 32) < 2 * kCUs)
-      launch_moe_up_tile<G, XK, 1, 1, 1, 8>(a, stream);
+    else if (G == 32 || pairs < 16 * kCUs) launch_moe_up_tile<G, XK, 1, 1, 1, 4>(a, stream);
     else if constexpr (G != 32) launch_moe_up_tile<G, XK, 1, 2, 1, 4>(a, stream);
   }
 }
@@ -158,12 +161,13 @@ void launch_moe_down_tile(const MoeArgs& a, hipStream_t stream) {
 // Two column tiles halve the reads of h (64 tokens over 64 experts: 167 us, with
 // one 239 us), unless there are too few columns to give every second compute unit
 // a workgroup then. Entries of up to 16 picks where an expert may have more than 8
-// (one row tile there: 198 us).
+// (one row tile there: 198 us; 16 tokens that all pick 8 experts of 928 x 672: 11.4
+// us, with one row tile 12.2).
 template <int G>
 void launch_moe_down(const MoeArgs& a, hipStream_t stream) {
   const bool few_columns = a.K < 32 * kCUs / 2;
-  if (a.tokens > 16) few_columns ? launch_moe_down_tile<G, 2, 1, 2, 8>(a, stream) : launch_moe_down_tile<G, 2, 2, 2, 8>(a, stream);
-  else if (few_columns) launch_moe_down_tile<G, 1, 1, 1, 16>(a, stream);
+  if (few_columns) a.tokens > 8 ? launch_moe_down_tile<G, 2, 1, 1, 8>(a, stream) : launch_moe_down_tile<G, 1, 1, 1, 16>(a, stream);
+  else if (a.tokens > 16) launch_moe_down_tile<G, 2, 2, 2, 8>(a, stream);
   else if constexpr (G == 0) launch_moe_down_tile<G, 1, 2, 1, 16>(a, stream);
   else launch_moe_down_tile<G, 1, 2, 2, 8>(a, stream);
 }
