@@ -10,8 +10,18 @@ using namespace fg::ops;
 
 namespace {
 
-#define HIPCHK_LAUNCH() \
-  do { if (hipGetLastError() != hipSuccess) return FG_EHIP; } while (0)
+// Launches on one stream, with their own errors only (an error that an earlier call
+// of the program left behind is not theirs); none after one that failed.
+struct Launches {
+  hipStream_t stream;
+  hipError_t error = hipSuccess;
+  template <class Args>
+  void operator()(void (*kernel)(Args), dim3 grid, dim3 block, size_t lds, Args a) {
+    void* args[1] = {&a};
+    if (error == hipSuccess) error = hipLaunchKernel((const void*)kernel, grid, block, args, lds, stream);
+  }
+  fg_status status() const { return error == hipSuccess ? FG_OK : FG_EHIP; }
+};
 
 constexpr int kCUs = 256;          // compute units of the part
 
@@ -45,42 +55,42 @@ dim3 wide_grid(int64_t n) {
 }
 
 template <int W, int V>
-void launch_norm(bool past, const NormArgs& a, hipStream_t stream) {
+void launch_norm(bool past, const NormArgs& a, Launches& go) {
   const dim3 grid = wide_grid((a.rows + NormShape<W>::kRows - 1) / NormShape<W>::kRows), block(NormShape<W>::kThreads);
-  if (past) hipLaunchKernelGGL((add_rmsnorm_kernel<W, V, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((add_rmsnorm_kernel<W, V, false>), grid, block, 0, stream, a);
+  if (past) go(add_rmsnorm_kernel<W, V, true>, grid, block, 0, a);
+  else go(add_rmsnorm_kernel<W, V, false>, grid, block, 0, a);
 }
 
 template <int W>
-void launch_norm(int V, bool past, const NormArgs& a, hipStream_t stream) {
+void launch_norm(int V, bool past, const NormArgs& a, Launches& go) {
   switch (V) {
-    case 1: launch_norm<W, 1>(past, a, stream); break;
-    case 2: launch_norm<W, 2>(past, a, stream); break;
+    case 1: launch_norm<W, 1>(past, a, go); break;
+    case 2: launch_norm<W, 2>(past, a, go); break;
     default:                       // more than two only where a row has all 16 waves
-      if constexpr (W == 16) V == 4 ? launch_norm<W, 4>(past, a, stream) : launch_norm<W, 8>(past, a, stream);
+      if constexpr (W == 16) V == 4 ? launch_norm<W, 4>(past, a, go) : launch_norm<W, 8>(past, a, go);
   }
 }
 
 template <int L, int N, bool BF16>
-void launch_route_lanes(const RouteArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((moe_route_kernel<L, N, BF16>), wide_grid((a.rows * L + 255) / 256), dim3(256), 0, stream, a);
+void launch_route_lanes(const RouteArgs& a, Launches& go) {
+  go(moe_route_kernel<L, N, BF16>, wide_grid((a.rows * L + 255) / 256), dim3(256), 0, a);
 }
 
 template <bool BF16>
-void launch_route(const RouteArgs& a, hipStream_t stream) {
-  if (a.experts <= 16) launch_route_lanes<16, 1, BF16>(a, stream);
-  else if (a.experts <= 32) launch_route_lanes<16, 2, BF16>(a, stream);
-  else if (a.experts <= 64) launch_route_lanes<16, 4, BF16>(a, stream);
-  else if (a.experts <= 128) launch_route_lanes<16, 8, BF16>(a, stream);
-  else if (a.experts <= 256) launch_route_lanes<16, 16, BF16>(a, stream);
-  else if (a.experts <= 512) launch_route_lanes<64, 8, BF16>(a, stream);
-  else launch_route_lanes<64, 16, BF16>(a, stream);
+void launch_route(const RouteArgs& a, Launches& go) {
+  if (a.experts <= 16) launch_route_lanes<16, 1, BF16>(a, go);
+  else if (a.experts <= 32) launch_route_lanes<16, 2, BF16>(a, go);
+  else if (a.experts <= 64) launch_route_lanes<16, 4, BF16>(a, go);
+  else if (a.experts <= 128) launch_route_lanes<16, 8, BF16>(a, go);
+  else if (a.experts <= 256) launch_route_lanes<16, 16, BF16>(a, go);
+  else if (a.experts <= 512) launch_route_lanes<64, 8, BF16>(a, go);
+  else launch_route_lanes<64, 16, BF16>(a, go);
 }
 
 template <int G, int XK, int MT, int R, int P, int W>
-void launch_w4_tile(const W4Args& a, hipStream_t stream) {
+void launch_w4_tile(const W4Args& a, Launches& go) {
   const dim3 grid((a.n + 16 * R - 1) / (16 * R), (a.rows + 16 * MT - 1) / (16 * MT));
-  hipLaunchKernelGGL((w4_linear_kernel<G, XK, MT, R, P, W>), grid, dim3(64 * W), 0, stream, a);
+  go(w4_linear_kernel<G, XK, MT, R, P, W>, grid, dim3(64 * W), 0, a);
 }
 
 // The tile of 16 MT rows by 16 R columns. A larger one reads weights and
@@ -92,7 +102,7 @@ void launch_w4_tile(const W4Args& a, hipStream_t stream) {
 //   60 x 4096: - - 12.7 17.0;  60 x 8192: - - 20.6 17.7.
 // The largest does not fit in the registers for groups of 32.
 template <int G, int XK>
-void launch_w4(const W4Args& a, hipStream_t stream) {
+void launch_w4(const W4Args& a, Launches& go) {
   auto rounds = [&](int mt, int r) {
     const int64_t n = (int64_t)((a.n + 16 * r - 1) / (16 * r)) * ((a.rows + 16 * mt - 1) / (16 * mt));
     return (n + kCUs - 1) / kCUs;
@@ -103,21 +113,21 @@ void launch_w4(const W4Args& a, hipStream_t stream) {
     if (cost[i] < cost[best]) best = i;
   switch (best) {
     case 0:       // one workgroup or none a compute unit: more waves where they have enough steps (1 x 2048 x 7168: 6.4 us, with 8 7.0)
-      if (rounds(1, 1) == 1 && a.k >= 48 * kStep) launch_w4_tile<G, XK, 1, 1, 2, 16>(a, stream);
-      else launch_w4_tile<G, XK, 1, 1, 2, 8>(a, stream);
+      if (rounds(1, 1) == 1 && a.k >= 48 * kStep) launch_w4_tile<G, XK, 1, 1, 2, 16>(a, go);
+      else launch_w4_tile<G, XK, 1, 1, 2, 8>(a, go);
       break;
-    case 1: launch_w4_tile<G, XK, 1, 2, 2, 8>(a, stream); break;
-    case 2: launch_w4_tile<G, XK, 2, 2, 1, 8>(a, stream); break;
+    case 1: launch_w4_tile<G, XK, 1, 2, 2, 8>(a, go); break;
+    case 2: launch_w4_tile<G, XK, 2, 2, 1, 8>(a, go); break;
     default:
-      if constexpr (G != 32) launch_w4_tile<G, XK, 4, 2, 1, 8>(a, stream);
+      if constexpr (G != 32) launch_w4_tile<G, XK, 4, 2, 1, 8>(a, go);
   }
 }
 
 template <int G>
-void launch_w4(const W4Args& a, int type, bool grouped, hipStream_t stream) {
-  if (type == FG_BF16) launch_w4<G, X_BF16>(a, stream);
-  else if (type == FG_I8) grouped ? launch_w4<G, X_I8G>(a, stream) : launch_w4<G, X_I8>(a, stream);
-  else grouped ? launch_w4<G, X_E4M3G>(a, stream) : launch_w4<G, X_E4M3>(a, stream);
+void launch_w4(const W4Args& a, int type, bool grouped, Launches& go) {
+  if (type == FG_BF16) launch_w4<G, X_BF16>(a, go);
+  else if (type == FG_I8) grouped ? launch_w4<G, X_I8G>(a, go) : launch_w4<G, X_I8>(a, go);
+  else grouped ? launch_w4<G, X_E4M3G>(a, go) : launch_w4<G, X_E4M3>(a, go);
 }
 
 // More than 16 rows an expert on average, were all picks here: two row tiles, so
@@ -127,10 +137,10 @@ void launch_w4(const W4Args& a, int type, bool grouped, hipStream_t stream) {
 bool many_rows(const MoeArgs& a) { return a.tokens > 16 && a.tokens * a.k > 16 * a.n_local; }
 
 template <int G, int XK, int MT, int C, int P, int W>
-void launch_moe_up_tile(const MoeArgs& a, hipStream_t stream) {
+void launch_moe_up_tile(const MoeArgs& a, Launches& go) {
   const int picks = a.tokens * a.k, experts = picks < a.n_local ? picks : a.n_local;
   const dim3 grid(experts * ((a.F + 16 * C - 1) / (16 * C)));
-  hipLaunchKernelGGL((moe_up_kernel<G, XK, MT, C, P, W>), grid, dim3(64 * W), 0, stream, a);
+  go(moe_up_kernel<G, XK, MT, C, P, W>, grid, dim3(64 * W), 0, a);
 }
 
 // 4-bit weights: two column tiles share the loads of x (64 tokens over 64 experts:
@@ -140,22 +150,22 @@ void launch_moe_up_tile(const MoeArgs& a, hipStream_t stream) {
 // workgroup's start and end are a larger share of it (12 tokens over 8 of 64 experts
 // of 1792 x 1536: 7.6 us, with eight 8.9).
 template <int G, int XK>
-void launch_moe_up(const MoeArgs& a, hipStream_t stream) {
+void launch_moe_up(const MoeArgs& a, Launches& go) {
   if constexpr (G == 0) {
-    many_rows(a) ? launch_moe_up_tile<G, XK, 2, 1, 2, 4>(a, stream) : launch_moe_up_tile<G, XK, 1, 1, 2, 4>(a, stream);
+    many_rows(a) ? launch_moe_up_tile<G, XK, 2, 1, 2, 4>(a, go) : launch_moe_up_tile<G, XK, 1, 1, 2, 4>(a, go);
   } else {
     const int picks = a.tokens * a.k;
     const int64_t pairs = (picks < a.n_local ? picks : a.n_local) * (int64_t)(a.F / 32);
-    if (many_rows(a)) launch_moe_up_tile<G, XK, 2, 1, 1, 8>(a, stream);
-    else if (G == 32 || pairs < 16 * kCUs) launch_moe_up_tile<G, XK, 1, 1, 1, 4>(a, stream);
-    else if constexpr (G != 32) launch_moe_up_tile<G, XK, 1, 2, 1, 4>(a, stream);
+    if (many_rows(a)) launch_moe_up_tile<G, XK, 2, 1, 1, 8>(a, go);
+    else if (G == 32 || pairs < 16 * kCUs) launch_moe_up_tile<G, XK, 1, 1, 1, 4>(a, go);
+    else if constexpr (G != 32) launch_moe_up_tile<G, XK, 1, 2, 1, 4>(a, go);
   }
 }
 
 template <int G, int MT, int R, int P, int W>
-void launch_moe_down_tile(const MoeArgs& a, hipStream_t stream) {
+void launch_moe_down_tile(const MoeArgs& a, Launches& go) {
   const size_t lds = (size_t)W * a.tokens * 16 * R * sizeof(float);
-  hipLaunchKernelGGL((moe_down_kernel<G, MT, R, P, W>), dim3((a.K + 16 * R - 1) / (16 * R)), dim3(64 * W), lds, stream, a);
+  go(moe_down_kernel<G, MT, R, P, W>, dim3((a.K + 16 * R - 1) / (16 * R)), dim3(64 * W), lds, a);
 }
 
 // Two column tiles halve the reads of h (64 tokens over 64 experts: 167 us, with
@@ -164,23 +174,21 @@ void launch_moe_down_tile(const MoeArgs& a, hipStream_t stream) {
 // (one row tile there: 198 us; 16 tokens that all pick 8 experts of 928 x 672: 11.4
 // us, with one row tile 12.2).
 template <int G>
-void launch_moe_down(const MoeArgs& a, hipStream_t stream) {
+void launch_moe_down(const MoeArgs& a, Launches& go) {
   const bool few_columns = a.K < 32 * kCUs / 2;
-  if (few_columns) a.tokens > 8 ? launch_moe_down_tile<G, 2, 1, 1, 8>(a, stream) : launch_moe_down_tile<G, 1, 1, 1, 16>(a, stream);
-  else if (a.tokens > 16) launch_moe_down_tile<G, 2, 2, 2, 8>(a, stream);
-  else if constexpr (G == 0) launch_moe_down_tile<G, 1, 2, 1, 16>(a, stream);
-  else launch_moe_down_tile<G, 1, 2, 2, 8>(a, stream);
+  if (few_columns) a.tokens > 8 ? launch_moe_down_tile<G, 2, 1, 1, 8>(a, go) : launch_moe_down_tile<G, 1, 1, 1, 16>(a, go);
+  else if (a.tokens > 16) launch_moe_down_tile<G, 2, 2, 2, 8>(a, go);
+  else if constexpr (G == 0) launch_moe_down_tile<G, 1, 2, 1, 16>(a, go);
+  else launch_moe_down_tile<G, 1, 2, 2, 8>(a, go);
 }
 
 template <int G>
-fg_status launch_moe(const MoeArgs& a, int type, bool grouped, hipStream_t stream) {
-  if (type == FG_BF16) launch_moe_up<G, X_BF16>(a, stream);
-  else if (type == FG_I8) grouped ? launch_moe_up<G, X_I8G>(a, stream) : launch_moe_up<G, X_I8>(a, stream);
-  else grouped ? launch_moe_up<G, X_E4M3G>(a, stream) : launch_moe_up<G, X_E4M3>(a, stream);
-  HIPCHK_LAUNCH();
-  launch_moe_down<G>(a, stream);
-  HIPCHK_LAUNCH();
-  return FG_OK;
+fg_status launch_moe(const MoeArgs& a, int type, bool grouped, Launches& go) {
+  if (type == FG_BF16) launch_moe_up<G, X_BF16>(a, go);
+  else if (type == FG_I8) grouped ? launch_moe_up<G, X_I8G>(a, go) : launch_moe_up<G, X_I8>(a, go);
+  else grouped ? launch_moe_up<G, X_E4M3G>(a, go) : launch_moe_up<G, X_E4M3>(a, go);
+  launch_moe_down<G>(a, go);
+  return go.status();
 }
 
 }  // namespace
@@ -197,6 +205,7 @@ fg_status fg_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64
   if (!x || !gamma || ldx < n || (residual && ldr < n) || (sum && lds < n) || (y && ldy < n) || (q && ldq < n)) return FG_EINVAL;
   if (!aligned(x, 2) || !aligned(residual, 2) || !aligned(gamma, 2) || !aligned(sum, 2) || !aligned(y, 2) || !aligned(q_scale, 4))
     return FG_EINVAL;
+  Launches go{stream};
   NormArgs a{};
   a.x = (const uint16_t*)x; a.res = (const uint16_t*)residual; a.gamma = (const uint16_t*)gamma;
   a.sum = (uint16_t*)sum; a.y = (uint16_t*)y; a.q = (uint8_t*)q; a.scale = q_scale;
@@ -212,14 +221,13 @@ fg_status fg_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64
   if (W > 16) W = 16;
   const int V = pow2_at_least((nv + 64 * W - 1) / (64 * W));
   switch (W) {
-    case 1: launch_norm<1>(V, past, a, stream); break;
-    case 2: launch_norm<2>(V, past, a, stream); break;
-    case 4: launch_norm<4>(V, past, a, stream); break;
-    case 8: launch_norm<8>(V, past, a, stream); break;
-    default: launch_norm<16>(V, past, a, stream); break;
+    case 1: launch_norm<1>(V, past, a, go); break;
+    case 2: launch_norm<2>(V, past, a, go); break;
+    case 4: launch_norm<4>(V, past, a, go); break;
+    case 8: launch_norm<8>(V, past, a, go); break;
+    default: launch_norm<16>(V, past, a, go); break;
   }
-  HIPCHK_LAUNCH();
-  return FG_OK;
+  return go.status();
 }
 
 fg_status fg_moe_route(const void* logits, int64_t ld, int32_t logits_type, int64_t rows, int32_t experts, int32_t k,
@@ -229,10 +237,10 @@ fg_status fg_moe_route(const void* logits, int64_t ld, int32_t logits_type, int6
   if (rows == 0) return FG_OK;
   if (!logits || !topk || !weights || ld < experts) return FG_EINVAL;
   if (!aligned(logits, logits_type == FG_F32 ? 4 : 2) || !aligned(topk, 4) || !aligned(weights, 4)) return FG_EINVAL;
+  Launches go{stream};
   RouteArgs a{logits, topk, weights, ld, rows, experts, k, score, renorm, scale};
-  logits_type == FG_BF16 ? launch_route<true>(a, stream) : launch_route<false>(a, stream);
-  HIPCHK_LAUNCH();
-  return FG_OK;
+  logits_type == FG_BF16 ? launch_route<true>(a, go) : launch_route<false>(a, go);
+  return go.status();
 }
 
 fg_status fg_w4_linear(const void* x, int64_t ldx, int32_t x_type, const float* x_scale, int32_t x_group, const void* w,
@@ -241,16 +249,16 @@ fg_status fg_w4_linear(const void* x, int64_t ldx, int32_t x_type, const float* 
   if (rows < 0 || rows > FG_W4_MAX_ROWS || n < 1 || k < 1 || n > FG_FEW_MAX_SIZE || k > FG_FEW_MAX_SIZE || !w4_ok(w, w_scale, group, k)) return FG_EINVAL;
   if (rows == 0) return FG_OK;
   if (!rows_ok(x, ldx, x_type, x_scale, x_group, k) || !out || ldo < n || !aligned(out, 2) || !aligned(bias, 2)) return FG_EINVAL;
+  Launches go{stream};
   W4Args a{};
   a.x = (const char*)x; a.xs = x_scale; a.w = (const char*)w; a.s = (const uint16_t*)w_scale; a.z = (const uint8_t*)w_zero;
   a.bias = (const uint16_t*)bias; a.out = (uint16_t*)out;
   a.ldx = ldx * (x_type == FG_BF16 ? 2 : 1); a.xs_stride = x_group ? k / x_group : 1; a.ldo = ldo;
   a.rows = (int32_t)rows; a.n = n; a.k = k;
-  if (group == 32) launch_w4<32>(a, x_type, x_group != 0, stream);
-  else if (group == 64) launch_w4<64>(a, x_type, x_group != 0, stream);
-  else launch_w4<128>(a, x_type, x_group != 0, stream);
-  HIPCHK_LAUNCH();
-  return FG_OK;
+  if (group == 32) launch_w4<32>(a, x_type, x_group != 0, go);
+  else if (group == 64) launch_w4<64>(a, x_type, x_group != 0, go);
+  else launch_w4<128>(a, x_type, x_group != 0, go);
+  return go.status();
 }
 
 fg_status fg_moe_few_bytes(int32_t tokens, int32_t k, int32_t F, int64_t* bytes) {
@@ -280,6 +288,7 @@ fg_status fg_moe_few(const void* x, int64_t ldx, int32_t x_type, const float* x_
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < 4 * (int64_t)tokens * k * F) return FG_EINVAL;
   // a grid of fewer than 2^32 threads
   if ((int64_t)n_local * ((F + 15) / 16) > (1 << 23)) return FG_EINVAL;
+  Launches go{stream};
   MoeArgs a{};
   a.x = (const char*)x; a.xs = x_scale; a.topk = topk; a.weights = weights;
   a.w1 = (const char*)w1; a.s1 = (const uint16_t*)w1_scale; a.z1 = (const uint8_t*)w1_zero;
@@ -289,10 +298,10 @@ fg_status fg_moe_few(const void* x, int64_t ldx, int32_t x_type, const float* x_
   a.ldx = ldx * (x_type == FG_BF16 ? 2 : 1); a.xs_stride = x_group ? K / x_group : 1; a.ldy = ldy;
   a.tokens = tokens; a.k = k; a.base = expert_base; a.n_local = n_local; a.K = K; a.F = F;
   const bool grouped = x_group != 0;
-  if (group == 0) return launch_moe<0>(a, x_type, grouped, stream);
-  if (group == 32) return launch_moe<32>(a, x_type, grouped, stream);
-  if (group == 64) return launch_moe<64>(a, x_type, grouped, stream);
-  return launch_moe<128>(a, x_type, grouped, stream);
+  if (group == 0) return launch_moe<0>(a, x_type, grouped, go);
+  if (group == 32) return launch_moe<32>(a, x_type, grouped, go);
+  if (group == 64) return launch_moe<64>(a, x_type, grouped, go);
+  return launch_moe<128>(a, x_type, grouped, go);
 }
 
 }  // extern "C"
