@@ -90,7 +90,7 @@ void launch_route(const RouteArgs& a, Launches& go) {
 template <int G, int XK, int MT, int R, int P, int W>
 void launch_w4_tile(const W4Args& a, Launches& go) {
   const dim3 grid((a.n + 16 * R - 1) / (16 * R), (a.rows + 16 * MT - 1) / (16 * MT));
-  go(w4_linear_kernel<G, XK, MT, R, P, W>, grid, dim3(64 * W), 0, a);
+  go(w4_linear_kernel<G, XK, MT, R, P, W>, grid, dim3(64 * W), XK == X_LDS ? 2 * (size_t)a.k : 0, a);
 }
 
 // The tile of 16 MT rows by 16 R columns. A larger one reads weights and
@@ -101,31 +101,43 @@ void launch_w4_tile(const W4Args& a, Launches& go) {
 //   12 x 4096: 7.6 9.0 - -;  12 x 8192: 10.9 10.0 - -;  28 x 8192: 16.1 16.1 12.6 -;
 //   60 x 4096: - - 12.7 17.0;  60 x 8192: - - 20.6 17.7.
 // The largest does not fit in the registers for groups of 32.
+// One row takes one of the first two.
 template <int G, int XK>
 void launch_w4(const W4Args& a, Launches& go) {
+  constexpr int kTiles = XK == X_LDS ? 2 : G == 32 ? 3 : 4;
   auto rounds = [&](int mt, int r) {
     const int64_t n = (int64_t)((a.n + 16 * r - 1) / (16 * r)) * ((a.rows + 16 * mt - 1) / (16 * mt));
     return (n + kCUs - 1) / kCUs;
   };
   const float cost[4] = {1.0f * rounds(1, 1), 1.5f * rounds(1, 2), 2.2f * rounds(2, 2), 3.7f * rounds(4, 2)};
   int best = 0;
-  for (int i = 1; i < (G == 32 ? 3 : 4); ++i)
+  for (int i = 1; i < kTiles; ++i)
     if (cost[i] < cost[best]) best = i;
   switch (best) {
-    case 0:       // one workgroup or none a compute unit: more waves where they have enough steps (1 x 2048 x 7168: 6.4 us, with 8 7.0)
+    case 0:       // one workgroup or none a compute unit: more waves where they have enough steps (1 x 2048 x 7168: 5.6 us, with 8 5.9)
       if (rounds(1, 1) == 1 && a.k >= 48 * kStep) launch_w4_tile<G, XK, 1, 1, 2, 16>(a, go);
       else launch_w4_tile<G, XK, 1, 1, 2, 8>(a, go);
       break;
     case 1: launch_w4_tile<G, XK, 1, 2, 2, 8>(a, go); break;
-    case 2: launch_w4_tile<G, XK, 2, 2, 1, 8>(a, go); break;
+    case 2:
+      if constexpr (kTiles > 2) launch_w4_tile<G, XK, 2, 2, 1, 8>(a, go);
+      break;
     default:
-      if constexpr (G != 32) launch_w4_tile<G, XK, 4, 2, 1, 8>(a, go);
+      if constexpr (kTiles > 3) launch_w4_tile<G, XK, 4, 2, 1, 8>(a, go);
   }
 }
 
+// One bf16 row goes through LDS: 1 x 2048 x 7168 5.6 us, straight from L2 6.3; 8192 x
+// 8192 10.3 and 11.1; 4096 x 14336 9.0 and 10.6; with short rows there is no difference
+// (64 x 512: 3.6). From two rows on every row would be copied by every workgroup (8 x
+// 4096 x 4096: 6.8 us, from L2 5.5). Rows of 32 KB leave room for the sums of the waves
+// within 64 KB.
+constexpr int kLdsRow = 16384;
+
 template <int G>
 void launch_w4(const W4Args& a, int type, bool grouped, Launches& go) {
-  if (type == FG_BF16) launch_w4<G, X_BF16>(a, go);
+  if (type == FG_BF16 && a.rows == 1 && a.k <= kLdsRow) launch_w4<G, X_LDS>(a, go);
+  else if (type == FG_BF16) launch_w4<G, X_BF16>(a, go);
   else if (type == FG_I8) grouped ? launch_w4<G, X_I8G>(a, go) : launch_w4<G, X_I8>(a, go);
   else grouped ? launch_w4<G, X_E4M3G>(a, go) : launch_w4<G, X_E4M3>(a, go);
 }

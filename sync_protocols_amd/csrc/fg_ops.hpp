@@ -102,10 +102,10 @@ __device__ __forceinline__ int lanes_before_and_own(int v) {
 
 // ------------------------------------------------------------- activations
 // X_PACKED: bf16 in operand order (the expert layer's own intermediate, see
-// PackedRows); X_I8G, X_E4M3G: 8-bit rows
+// PackedRows); X_LDS: one bf16 row that the workgroup has copied to LDS; X_I8G, X_E4M3G: 8-bit rows
 // with one scale per 128 k, the others have one per row, which the caller
 // applies to the finished sums.
-enum { X_BF16 = FG_BF16, X_I8 = FG_I8, X_E4M3 = FG_E4M3, X_PACKED = 16, X_I8G = 17, X_E4M3G = 18 };
+enum { X_BF16 = FG_BF16, X_I8 = FG_I8, X_E4M3 = FG_E4M3, X_PACKED = 16, X_I8G = 17, X_E4M3G = 18, X_LDS = 19 };
 constexpr bool x_is_i8(int xk) { return xk == X_I8 || xk == X_I8G; }
 constexpr bool x_is_e4m3(int xk) { return xk == X_E4M3 || xk == X_E4M3G; }
 constexpr bool x_is_8bit(int xk) { return x_is_i8(xk) || x_is_e4m3(xk); }
@@ -207,6 +207,18 @@ struct PackedRows {
   }
 };
 
+// X_LDS: every row of the operand is that one, 128 k after 128 k in paired() order.
+// A read takes four pieces of 16 bytes whatever the lanes, so nothing is loaded 16
+// times from L2 and no lanes change places.
+__device__ __forceinline__ char* lds_row() {
+  extern __shared__ __attribute__((aligned(16))) char row[];
+  return row;
+}
+__device__ __forceinline__ void copy_row_to_lds(const char* x, int k, int threads) {
+  for (int c = threadIdx.x; c < k / 8; c += threads) ((u32x4*)lds_row())[c] = paired(((const u32x4*)x)[c]);
+  __syncthreads();
+}
+
 template <int XK, int MT, bool PAIRS, bool MASKED>
 struct XRows {
   static constexpr bool k8 = x_is_8bit(XK);
@@ -219,7 +231,9 @@ struct XRows {
     const int jj = TAIL && (PAIRS ? 64 * (j / 2) : 32 * j) >= lim ? 0 : j;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      if constexpr (XK == X_PACKED) {
+      if constexpr (XK == X_LDS) {
+        v[m][j] = *(const u32x4*)(lds_row() + 2 * kStep * step + 64 * jj + xp.row[m]);
+      } else if constexpr (XK == X_PACKED) {
         const auto r = rows_at(xp.base + (uint64_t)(16 * (uint32_t)step + 4 * jj) * xp.plane);
         v[m][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)xp.row[m], 0, 0));
       } else if constexpr (PAIRS) {
@@ -243,7 +257,7 @@ struct XRows {
     for (int j = 0; j < 4; j += PAIRS ? 2 : 1) load<TAIL>(j, xp, step, lim);
   }
   __device__ __forceinline__ V get(const Lanes& ln, int m, int j) const {
-    return XK == X_PACKED ? v[m][j] : from_lane(PAIRS ? ln.to_pairs : ln.to_operand, v[m][j]);
+    return XK == X_PACKED || XK == X_LDS ? v[m][j] : from_lane(PAIRS ? ln.to_pairs : ln.to_operand, v[m][j]);
   }
 };
 
@@ -534,7 +548,7 @@ struct Quant4 {
           for (int i = 0; i < kBlock; ++i) {
             xv[m][i] = x.get(ln, m, j + i);
             if constexpr (k8) xv[m][i] = even_odd(xv[m][i][0], xv[m][i][1]);
-            else if constexpr (XK != X_PACKED) xv[m][i] = paired(xv[m][i]);
+            else if constexpr (XK != X_PACKED && XK != X_LDS) xv[m][i] = paired(xv[m][i]);
           }
         // both words of a load have been taken
         if ((!kPairs || kBlock == 2 || j % 2 == 1) && (!MAYBE || nx >= 0)) x.template load<false>(j, xp, nx, kStep);
@@ -589,7 +603,7 @@ struct Quant4 {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < (XK == X_LDS ? 1 : 4); ++i) {
           const float xs = kGrouped ? row_scale(aux.xs[m], ln, t, i) : 1.0f;
 #pragma unroll
           for (int r = 0; r < R; ++r) {

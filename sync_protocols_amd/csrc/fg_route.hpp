@@ -59,10 +59,10 @@ __device__ __forceinline__ void load_logits(const char* p, int left, float (&x)[
 // L lanes per token; lane l of them holds logits l * N + 0..N-1. A pick is the
 // largest key of the lanes' largest and then the lowest index among those equal to
 // it; a bf16 logit's key leaves 16 bits free, so there the key itself ends in the
-// index, lowest largest, and one maximum finds both. 16 lanes with up to 16 logits each need the fewest
-// instructions, which bound it (8192 tokens, 256 experts, 8 picks: 4.5 us bf16, 5.8 us
-// fp32, of which a launch with its loads and one pick is 3.7; with 64 lanes of 4
-// logits 11.8 us); more experts take 64 lanes.
+// index, lowest largest, and one maximum finds both. 16 lanes with up to 16 logits
+// each need the fewest instructions, which bound it (8192 tokens, 256 experts, 8 picks:
+// 4.5 us bf16, 5.8 us fp32, of which a launch with its loads and one pick is 3.7; with
+// 64 lanes of 4 logits 11.8 us); more experts take 64 lanes.
 // Lane j % 16 keeps the j-th pick, so that scores are computed once, side by side.
 template <int L, int N, bool BF16>
 __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a) {

@@ -8,7 +8,7 @@
 // it: 64 rows x 8192 x 8192, groups of 64, int8 rows take 19 us (38 MB, 5.4 us at
 // the rate of streaming reads; loads alone 17, arithmetic alone 14), 5 x 8199 x 7200,
 // groups of 32 with zero points, 16.5 us (loads alone 14, arithmetic alone 12), one
-// row x 2048 x 7168 6 us, the latency of a few dependent steps.
+// row x 2048 x 7168 5.6 us, the latency of a few dependent steps.
 #pragma once
 
 #include "fg_ops.hpp"
@@ -64,9 +64,11 @@ __global__ __launch_bounds__(64 * W, MIN_WAVES) void w4_linear_kernel(W4Args a) 
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const uint32_t row = (uint32_t)min(16 * m + ln.load_row(), a.rows - 1 - t0);
-    xp.row[m] = 16 * m + ln.load_row() < a.rows - t0 ? row * (uint32_t)a.ldx + x_piece<G, XK>(ln) : kNoRow;
+    if constexpr (XK == X_LDS) xp.row[m] = 16 * ln.quarter;
+    else xp.row[m] = 16 * m + ln.load_row() < a.rows - t0 ? row * (uint32_t)a.ldx + x_piece<G, XK>(ln) : kNoRow;
     xp.at[m] = row * (uint32_t)a.xs_stride;
   }
+  if constexpr (XK == X_LDS) copy_row_to_lds(a.x, a.k, 64 * W);
   f32x4 acc[R][MT];
   clear<Prod>(acc);
   const int steps = a.k / kStep;

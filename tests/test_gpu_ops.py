@@ -489,3 +489,25 @@ def test_moe_more_than_32_picks_repeat_bit_for_bit(group):
     first = got.clone()
     for _ in range(5):
         assert torch.equal(first, ops.moe_few(*args))
+
+
+@pytest.mark.parametrize("k", [32, 96, 128, 480, 2048, 6176, 8192, 16384, 16416])
+@pytest.mark.parametrize("n", [1, 47, 4500])
+def test_w4_one_row(n, k):
+    """One bf16 row, in LDS up to 16384 elements; both tiles, ends of rows inside a step."""
+    for group in (32, 64, 128):
+        if k % group == 0:
+            run_w4(1, n, k, group, n % 2 == 1, "bf16", 0, bias=n == 47, pad=8 if k == 480 else 0)
+
+
+def test_w4_one_row_has_the_bits_it_has_among_others():
+    g = R.gen(11)
+    for n, k, group in ((48, 480, 32), (4500, 1088, 64), (80, 8192, 128)):
+        w = ops.W4Weight(*dev(*R.make_w4(g, (), n, k, group, True)))
+        x = torch.randn(5, k, generator=g).bfloat16()
+        x[4, k - 1] = math.inf
+        x = dev(x)
+        many = ops.w4_linear(x, w)
+        for t in range(4):
+            assert torch.equal(ops.w4_linear(x[t:t + 1], w), many[t:t + 1])
+        assert not ops.w4_linear(x[4:], w).isfinite().any()
