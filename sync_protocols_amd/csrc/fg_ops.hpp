@@ -29,6 +29,8 @@ namespace ops {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -113,8 +115,8 @@ constexpr bool x_grouped(int xk) { return xk == X_I8G || xk == X_E4M3G; }
 constexpr bool x_row_scaled(int xk) { return xk == X_I8 || xk == X_E4M3; }
 
 // 4-bit weights come out of a word as k pairs (0,4) (1,5) (2,6) (3,7) in 16 bits,
-// or as k (0,2,4,6) and (1,3,5,7) in 8 bits (see frag16, bytes8); activations are
-// brought into that order once for all the weight rows of a wave.
+// or as k (0,2,4,6) and (1,3,5,7) in 8 bits (see frag16, half16, bytes8); activations
+// are brought into that order once for all the weight rows of a wave.
 __device__ __forceinline__ u32x4 paired(u32x4 w) {
   u32x4 r;
   r[0] = __builtin_amdgcn_perm(w[2], w[0], 0x05040100u);
@@ -149,6 +151,17 @@ __device__ __forceinline__ bf16x8 widen8(u32x2 v) {
     }
   }
   return __builtin_bit_cast(bf16x8, r);
+}
+
+// Eight e4m3 activations as f16, exactly, in paired() order.
+__device__ __forceinline__ f16x8 half8(u32x2 v) {
+  const uint32_t a = __builtin_amdgcn_perm(v[1], v[0], 0x05010400u), b = __builtin_amdgcn_perm(v[1], v[0], 0x07030602u);
+  u32x4 r;
+  r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false));
+  r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true));
+  r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false));
+  r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true));
+  return __builtin_bit_cast(f16x8, r);
 }
 
 constexpr int kStep = 128;                      // k of a step of the products
@@ -391,9 +404,14 @@ struct Dense {
 //     against ones, shared by all weight rows of the wave. The subtraction costs
 //     about 5 bits of the fp32 sums, which leaves them 10 bits finer than the bf16
 //     result; an infinity in x gives NaN in its row of the result.
-//   e4m3: the byte q is the 8-bit float q * 2^-9 (0..7 are its subnormals, 8..15
-//     its first binade), so a nibble moved into a byte is a number already (3
-//     instructions per 8 weights); z by the sum of x as above.
+//   e4m3: x and q - z are f16 numbers. A nibble is made 1024 + q by one and-or
+//     (0x6400 | q), or 1024 + 16 q where it lies four bits higher, and one packed
+//     subtraction or multiply-add takes it to q - z: 9 instructions per 8 weights, 6
+//     per 8 activations. The 8-bit float matrix instruction would save 10 of them,
+//     but it drops what lies 13 bits and more below the largest of a lane's eight
+//     products, so that one large activation wipes out its neighbours; the 16-bit
+//     one keeps 23 bits and more of normal numbers (of f16 subnormals 13, so q 2^-24
+//     does not serve either).
 //   int8: the byte (q + 128 - z) ^ 128 is q - z in two's complement (no carry
 //     leaves a byte); int32 sums are exact and below 2^24.
 template <int G, int XK, int MT, int R, int P>
@@ -507,6 +525,20 @@ struct Quant4 {
     for (int i = 0; i < 4; ++i) r[i] = ((v >> (4 * i)) & 0x000f000fu) | 0x43004300u;
     return __builtin_bit_cast(bf16x8, r);
   }
+  // near: 1024 + z, far: -(64 + z), both twice
+  static __device__ __forceinline__ f16x8 half16(uint32_t v, f16x2 near, f16x2 far) {
+    const f16x2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const uint32_t u = v >> (4 * i);
+      const f16x2 a = __builtin_bit_cast(f16x2, (u & 0x000f000fu) | 0x64006400u);
+      const f16x2 b = __builtin_bit_cast(f16x2, (u & 0x00f000f0u) | 0x64006400u);
+      r[i] = __builtin_bit_cast(uint32_t, a - near);
+      r[i + 1] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(b, sixteenth, far));
+    }
+    return __builtin_bit_cast(f16x8, r);
+  }
   static __device__ __forceinline__ u32x2 bytes8(uint32_t v) { return u32x2{v & 0x0f0f0f0fu, (v >> 4) & 0x0f0f0f0fu}; }
   static __device__ __forceinline__ long as_long(u32x2 v) { return __builtin_bit_cast(long, v); }
   static __device__ __forceinline__ i32x4 as_i32x4(u32x2 a, u32x2 b) { return i32x4{(int)a[0], (int)a[1], (int)b[0], (int)b[1]}; }
@@ -538,6 +570,15 @@ struct Quant4 {
 #pragma unroll
         for (int r = 0; r < R; ++r) part[r][m] = Sum{0, 0, 0, 0};
       }
+      f16x2 near[R], far[R];
+      if constexpr (x_is_e4m3(XK)) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const _Float16 z = (_Float16)(uint16_t)((zw[r] >> (8 * h)) & 0xffu), a = z + (_Float16)1024.0f, b = -z - (_Float16)64.0f;
+          near[r] = f16x2{a, a};
+          far[r] = f16x2{b, b};
+        }
+      }
 #pragma unroll
       for (int f = 0; f < kWords; f += kBlock) {
         const int j = h * kWords + f;
@@ -547,8 +588,8 @@ struct Quant4 {
 #pragma unroll
           for (int i = 0; i < kBlock; ++i) {
             xv[m][i] = x.get(ln, m, j + i);
-            if constexpr (k8) xv[m][i] = even_odd(xv[m][i][0], xv[m][i][1]);
-            else if constexpr (XK != X_PACKED && XK != X_LDS) xv[m][i] = paired(xv[m][i]);
+            if constexpr (x_is_i8(XK)) xv[m][i] = even_odd(xv[m][i][0], xv[m][i][1]);
+            else if constexpr (!k8 && XK != X_PACKED && XK != X_LDS) xv[m][i] = paired(xv[m][i]);
           }
         // both words of a load have been taken
         if ((!kPairs || kBlock == 2 || j % 2 == 1) && (!MAYBE || nx >= 0)) x.template load<false>(j, xp, nx, kStep);
@@ -572,15 +613,14 @@ struct Quant4 {
             }
           }
         } else if constexpr (x_is_e4m3(XK)) {
+          f16x8 xo[MT];
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
-            sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(as_long(xv[m][0]), 0x3838383838383838l, sum[m], 0, 0, 0);
+          for (int m = 0; m < MT; ++m) xo[m] = half8(xv[m][0]);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            const long b = as_long(bytes8(w[r][j]));
+            const f16x8 b = half16(w[r][j], near[r], far[r]);
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-              part[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(as_long(xv[m][0]), b, part[r][m], 0, 0, 0);
+            for (int m = 0; m < MT; ++m) part[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xo[m], b, part[r][m], 0, 0, 0);
           }
         } else {
           const u32x4 one = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
@@ -608,10 +648,9 @@ struct Quant4 {
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const float z = (float)((zw[r] >> (8 * h)) & 0xffu);
-            const float s = (kGroups == 1 || h % 2 ? bf16_hi(sw[r][h / 2]) : bf16_lo(sw[r][h / 2])) * (x_is_e4m3(XK) ? 512.0f : 1.0f);
+            const float s = kGroups == 1 || h % 2 ? bf16_hi(sw[r][h / 2]) : bf16_lo(sw[r][h / 2]);
             float v;
-            if constexpr (x_is_i8(XK)) v = (float)part[r][m][i];
-            else if constexpr (x_is_e4m3(XK)) v = __builtin_fmaf(sum[m][i], z * -0x1p-9f, part[r][m][i]);
+            if constexpr (k8) v = (float)part[r][m][i];
             else v = __builtin_fmaf(sum[m][i], -128.0f - z, part[r][m][i]);
             acc[r][m][i] = __builtin_fmaf(v, kGrouped ? s * xs : s, acc[r][m][i]);
           }
