@@ -9,6 +9,7 @@
 
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/StreamGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -92,30 +93,27 @@ bool vector_of(const Tensor& t, int64_t n) { return t.dim() == 1 && t.size(0) ==
 
 void* ptr(const Tensor* t) { return t ? t->data_ptr() : nullptr; }
 
-// Tensors of one call: all on one GPU, kept for record_stream.
+// One call: its stream, and its tensors, all on one GPU.
+//
+// On another stream than the current one, what the call allocates comes from that
+// stream's memory: a block that the current stream has freed may still be read there
+// by kernels that have not run, and nothing orders the other stream after them. The
+// allocator is told that the caller's tensors are used on the other stream, and that
+// new outputs, which the caller goes on with, may be used on the current one.
 struct Call {
   const Tensor* used[16];
   int n = 0;
   c10::Device device;
+  std::optional<c10::Stream> other;
+  hipStream_t handle = nullptr;
   explicit Call(const Tensor& t) : device(t.device()) {}
-  void on_gpu() const {
+  // The stream of the launch: the device's current one, or `s`.
+  void on(PyObject* s) {
     if (!device.is_cuda()) refuse("tensors must be on the GPU");
-  }
-  void use(const Tensor* t) {
-    if (!t) return;
-    if (t->device() != device) refuse("tensors are on different devices");
-    used[n++] = t;
-  }
-  // The output `given`, checked, or a new one.
-  Tensor out(const Tensor* given, at::IntArrayRef shape, ScalarType type, const char* what) const {
-    if (!given) return at::detail::empty_cuda(shape, type, device, std::nullopt);
-    if (!is_type(*given, type) || !is_shape(*given, shape) || given->device() != device) refuse(what);
-    return *given;
-  }
-  // The stream of the launch: the device's current one, or `stream`; then the
-  // allocator is told that the tensors are used there.
-  hipStream_t stream(PyObject* s) const {
-    if (s == Py_None) return c10::hip::getCurrentHIPStream(device.index()).stream();
+    if (s == Py_None) {
+      handle = c10::hip::getCurrentHIPStream(device.index()).stream();
+      return;
+    }
     int64_t part[3];
     const char* name[3] = {"stream_id", "device_index", "device_type"};
     for (int i = 0; i < 3; ++i) {
@@ -126,14 +124,41 @@ struct Call {
       if (part[i] == -1 && PyErr_Occurred()) throw Refused();
     }
     if (part[1] != device.index()) refuse("stream and tensors are on different devices");
-    const c10::Stream st = c10::Stream::unpack3(part[0], (c10::DeviceIndex)part[1], (c10::DeviceType)part[2]);
-    for (int i = 0; i < n; ++i) used[i]->record_stream(st);
     PyObject* v = PyObject_GetAttrString(s, "cuda_stream");
     if (!v) throw Refused();
-    void* handle = PyLong_AsVoidPtr(v);
+    handle = (hipStream_t)PyLong_AsVoidPtr(v);
     Py_DECREF(v);
     if (PyErr_Occurred()) throw Refused();
-    return (hipStream_t)handle;
+    const c10::Stream st = c10::Stream::unpack3(part[0], (c10::DeviceIndex)part[1], (c10::DeviceType)part[2]);
+    if (st != current()) other = st;
+  }
+  c10::Stream current() const { return c10::impl::VirtualGuardImpl(device.type()).getStream(device); }
+  void use(const Tensor* t) {
+    if (!t) return;
+    if (t->device() != device) refuse("tensors are on different devices");
+    used[n++] = t;
+  }
+  // Memory of the launching stream.
+  Tensor memory(at::IntArrayRef shape, ScalarType type) const {
+    const c10::OptionalStreamGuard guard(other);
+    return at::detail::empty_cuda(shape, type, device, std::nullopt);
+  }
+  void check(const Tensor* given, at::IntArrayRef shape, ScalarType type, const char* what) const {
+    if (given && (!is_type(*given, type) || !is_shape(*given, shape) || given->device() != device)) refuse(what);
+  }
+  // The output `given`, which has been checked, or a new one.
+  Tensor out(const Tensor* given, at::IntArrayRef shape, ScalarType type) {
+    if (given) {
+      use(given);
+      return *given;
+    }
+    const Tensor t = memory(shape, type);
+    if (other) t.record_stream(current());
+    return t;
+  }
+  void record() const {
+    if (!other) return;
+    for (int i = 0; i < n; ++i) used[i]->record_stream(*other);
   }
 };
 
@@ -144,6 +169,7 @@ struct WithoutGil {
 
 template <class F>
 void launch(const Call& c, const char* name, F f) {
+  c.record();
   fg_status code;
   {
     const WithoutGil released;
@@ -214,30 +240,29 @@ PyObject* add_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const bool has_sum = res || sum_in, has_y = !bits8 || truth(a[6]) || y_in;
     const ScalarType qt = i8 ? at::kChar : at::kFloat8_e4m3fn;
     // what is given is checked before anything is allocated
-    if (sum_in) { c.out(sum_in, x.sizes(), at::kBFloat16, "sum must be bf16 like x"); ROWS2D(*sum_in, "sum"); }
-    if (y_in) { c.out(y_in, x.sizes(), at::kBFloat16, "y must be bf16 like x"); ROWS2D(*y_in, "y"); }
-    if (q_in) { c.out(q_in, x.sizes(), qt, "q must be of the type that out names and like x"); ROWS2D(*q_in, "q"); }
+    if (sum_in) { c.check(sum_in, x.sizes(), at::kBFloat16, "sum must be bf16 like x"); ROWS2D(*sum_in, "sum"); }
+    if (y_in) { c.check(y_in, x.sizes(), at::kBFloat16, "y must be bf16 like x"); ROWS2D(*y_in, "y"); }
+    if (q_in) { c.check(q_in, x.sizes(), qt, "q must be of the type that out names and like x"); ROWS2D(*q_in, "q"); }
     const int64_t sshape[2] = {rows, group ? n / group : 1};
     if (scale_in) {
-      c.out(scale_in, sshape, at::kFloat, "scale must be float32 [rows, 1 or n / 128]");
+      c.check(scale_in, sshape, at::kFloat, "scale must be float32 [rows, 1 or n / 128]");
       if (!scale_in->is_contiguous()) refuse("scale must be contiguous");
     }
-    c.on_gpu();
+    const float eps = (float)number(a[3]);
+    c.on(a[11]);
     c.use(&x); c.use(&gamma); c.use(res);
     Tensor sum, y, q, scale;
-    if (has_sum) { sum = c.out(sum_in, x.sizes(), at::kBFloat16, "sum"); c.use(&sum); }
-    if (has_y) { y = c.out(y_in, x.sizes(), at::kBFloat16, "y"); c.use(&y); }
+    if (has_sum) sum = c.out(sum_in, x.sizes(), at::kBFloat16);
+    if (has_y) y = c.out(y_in, x.sizes(), at::kBFloat16);
     if (bits8) {
-      q = c.out(q_in, x.sizes(), qt, "q"); c.use(&q);
-      scale = c.out(scale_in, sshape, at::kFloat, "scale"); c.use(&scale);
+      q = c.out(q_in, x.sizes(), qt);
+      scale = c.out(scale_in, sshape, at::kFloat);
     }
-    const float eps = (float)number(a[3]);
-    const hipStream_t stream = c.stream(a[11]);
     launch(c, "fg_add_rmsnorm", [&] {
       return fg_add_rmsnorm(x.data_ptr(), ld(x), ptr(res), res ? ld(*res) : 0, gamma.data_ptr(), eps, has_sum ? sum.data_ptr() : nullptr,
                             has_sum ? ld(sum) : 0, has_y ? y.data_ptr() : nullptr, has_y ? ld(y) : 0, bits8 ? q.data_ptr() : nullptr,
                             bits8 ? ld(q) : 0, i8 ? FG_I8 : FG_E4M3, (int32_t)group, bits8 ? (float*)scale.data_ptr() : nullptr, rows,
-                            (int32_t)n, stream);
+                            (int32_t)n, c.handle);
     });
     return tuple({wrap(sum, has_sum), wrap(y, has_y), wrap(q, bits8), wrap(scale, bits8)});
   });
@@ -259,19 +284,18 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     if (experts > FG_MOE_FEW_EXPERTS) refuse("moe_route takes up to 1024 experts");
     Call c(l);
     const int64_t shape[2] = {rows, k};
-    if (topk_in) c.out(topk_in, shape, at::kInt, "topk must be int32 [rows, k]");
-    if (w_in) c.out(w_in, shape, at::kFloat, "weights must be float32 [rows, k]");
+    c.check(topk_in, shape, at::kInt, "topk must be int32 [rows, k]");
+    c.check(w_in, shape, at::kFloat, "weights must be float32 [rows, k]");
     if ((topk_in && !topk_in->is_contiguous()) || (w_in && !w_in->is_contiguous())) refuse("topk and weights must be contiguous");
-    c.on_gpu();
-    const Tensor topk = c.out(topk_in, shape, at::kInt, "topk"), w = c.out(w_in, shape, at::kFloat, "weights");
-    c.use(&l); c.use(&topk); c.use(&w);
     const bool renorm = truth(a[3]);
     const float scale = (float)number(a[4]);
-    const hipStream_t stream = c.stream(a[7]);
+    c.on(a[7]);
+    c.use(&l);
+    const Tensor topk = c.out(topk_in, shape, at::kInt), w = c.out(w_in, shape, at::kFloat);
     launch(c, "fg_moe_route", [&] {
       return fg_moe_route(l.data_ptr(), ld(l), is_type(l, at::kFloat) ? FG_F32 : FG_BF16, rows, (int32_t)experts, (int32_t)k,
                           softmax ? FG_SCORE_SOFTMAX : FG_SCORE_SIGMOID, renorm ? 1 : 0, scale, (int32_t*)topk.data_ptr(),
-                          (float*)w.data_ptr(), stream);
+                          (float*)w.data_ptr(), c.handle);
     });
     return tuple({wrap(topk), wrap(w)});
   });
@@ -335,15 +359,13 @@ PyObject* w4_linear(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     if (bias && (!is_type(*bias, at::kBFloat16) || !vector_of(*bias, n))) refuse("bias must be bf16 [n]");
     Call c(x);
     const int64_t rows = x.size(0), shape[2] = {rows, n};
-    if (out_in) { c.out(out_in, shape, at::kBFloat16, "out must be bf16 [rows, n]"); ROWS2D(*out_in, "out"); }
-    c.on_gpu();
+    if (out_in) { c.check(out_in, shape, at::kBFloat16, "out must be bf16 [rows, n]"); ROWS2D(*out_in, "out"); }
+    c.on(a[7]);
     c.use(&x); c.use(xs); c.use(w.q); c.use(w.scale); c.use(w.zero); c.use(bias);
-    const Tensor out = c.out(out_in, shape, at::kBFloat16, "out");
-    c.use(&out);
-    const hipStream_t stream = c.stream(a[7]);
+    const Tensor out = c.out(out_in, shape, at::kBFloat16);
     launch(c, "fg_w4_linear", [&] {
       return fg_w4_linear(x.data_ptr(), ld(x), act.type, (const float*)ptr(xs), act.group, w.q->data_ptr(), w.scale->data_ptr(),
-                          ptr(w.zero), group, ptr(bias), out.data_ptr(), ld(out), rows, (int32_t)n, (int32_t)k, stream);
+                          ptr(w.zero), group, ptr(bias), out.data_ptr(), ld(out), rows, (int32_t)n, (int32_t)k, c.handle);
     });
     return wrap(out);
   });
@@ -384,22 +406,19 @@ PyObject* moe_few(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int32_t base = int32_of(a[10], "expert_base must be an int32");
     Call c(x);
     const int64_t shape[2] = {tokens, K};
-    if (out_in) { c.out(out_in, shape, at::kBFloat16, "out must be bf16 [tokens, K]"); ROWS2D(*out_in, "out"); }
+    if (out_in) { c.check(out_in, shape, at::kBFloat16, "out must be bf16 [tokens, K]"); ROWS2D(*out_in, "out"); }
     if (ws_in && !ws_in->is_contiguous()) refuse("workspace must be contiguous");
-    c.on_gpu();
+    c.on(a[13]);
     c.use(&x); c.use(xs); c.use(w1.q); c.use(w1.scale); c.use(w1.zero); c.use(w2.q); c.use(w2.scale); c.use(w2.zero);
     c.use(&topk); c.use(&weights); c.use(ws_in);
-    const Tensor out = c.out(out_in, shape, at::kBFloat16, "out");
+    const Tensor out = c.out(out_in, shape, at::kBFloat16);
     const int64_t need[1] = {4 * tokens * k * F};
-    const Tensor ws = ws_in ? *ws_in : c.out(nullptr, need, at::kByte, "workspace");
-    c.use(&out);
-    if (!ws_in) c.use(&ws);
-    const hipStream_t stream = c.stream(a[13]);
+    const Tensor ws = ws_in ? *ws_in : c.memory(need, at::kByte);
     launch(c, "fg_moe_few", [&] {
       return fg_moe_few(x.data_ptr(), ld(x), act.type, (const float*)ptr(xs), act.group, w1.q->data_ptr(), ptr(w1.scale), ptr(w1.zero),
                         w2.q->data_ptr(), ptr(w2.scale), ptr(w2.zero), group, (const int32_t*)topk.data_ptr(),
                         (const float*)weights.data_ptr(), (int32_t)tokens, (int32_t)k, base, (int32_t)n_local, (int32_t)K, (int32_t)F,
-                        ws.data_ptr(), (int64_t)ws.nbytes(), out.data_ptr(), ld(out), stream);
+                        ws.data_ptr(), (int64_t)ws.nbytes(), out.data_ptr(), ld(out), c.handle);
     });
     return wrap(out);
   });

@@ -8,6 +8,11 @@ fg.FgError (code fg.EINVAL) for arguments it does not take. Outputs are allocate
 unless given. All of them may be captured into a graph; nothing is kept between
 calls. The formulas and limits stand at the entry points in include/fg.h.
 
+With `stream`, the caller orders that stream after whatever makes the inputs (and
+last used given outputs), and the use of the outputs after that stream. What a call
+allocates comes from that stream's memory, so it needs no further order; tensors of
+either stream may be dropped right after the call.
+
 The work of a call is done by the extension fg_torch (csrc/fg_torch.cpp)."""
 from __future__ import annotations
 

@@ -35,3 +35,68 @@ def test_w4_small_elements_beside_a_large_one(rows, group, x_group):
     want = x.double() @ R.w4_values(packed, s, z).t()
     tol = (2 * group + 8) * R.U * 15 * x.double().abs().sum(1, keepdim=True)
     R.close(got, want, tol + R.BF16_HALF * (want.abs() + tol), "out")
+
+
+# ------------------------------------------------------------------ streams
+def _fresh(nbytes):
+    """The address of a block of that size that the current stream has just freed."""
+    t = torch.empty(nbytes, dtype=torch.uint8, device=DEV)
+    at = t.data_ptr()
+    del t
+    return at
+
+
+def test_outputs_on_another_stream_are_not_memory_that_this_one_freed():
+    s = torch.cuda.Stream()
+    g = R.gen(21)
+    x, gamma = torch.randn(2048, 4096, generator=g).bfloat16(), torch.ones(4096).bfloat16()
+    logits = torch.randn(1 << 17, 64, generator=g)
+    w = ops.W4Weight(*dev(*R.make_w4(g, (), 65536, 128, 64, False)))
+    x, gamma, logits = dev(x, gamma, logits)
+    rows = torch.randn(64, 128, generator=g).bfloat16().to(DEV)
+    torch.cuda.synchronize()
+    at = _fresh(2048 * 4096 * 2)
+    r = ops.add_rmsnorm(x, gamma, stream=s)
+    assert r.y.data_ptr() != at and _fresh(2048 * 4096 * 2) == at
+    at = _fresh(2048 * 4096)
+    r8 = ops.add_rmsnorm(x, gamma, out="i8", stream=s)
+    assert r8.q.data_ptr() != at
+    at = _fresh((1 << 17) * 32)
+    topk, weights = ops.moe_route(logits, 8, stream=s)
+    assert topk.data_ptr() != at and weights.data_ptr() != at
+    at = _fresh(64 * 65536 * 2)
+    out = ops.w4_linear(rows, w, stream=s)
+    assert out.data_ptr() != at
+    s.synchronize()
+    assert torch.equal(r.y, ops.add_rmsnorm(x, gamma).y) and torch.equal(out, ops.w4_linear(rows, w))
+
+
+def test_outputs_of_another_stream_stay_while_this_one_uses_them():
+    s = torch.cuda.Stream()
+    x, gamma = torch.randn(2048, 2048, generator=R.gen(22)).bfloat16().to(DEV), torch.ones(2048, dtype=BF, device=DEV)
+    want = ops.add_rmsnorm(x, gamma).y
+    torch.cuda.synchronize()
+    r = ops.add_rmsnorm(x, gamma, stream=s)
+    at = r.y.data_ptr()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda._sleep(20_000_000)
+    copy = r.y.clone()
+    del r                                                     # this stream has yet to read it
+    with torch.cuda.stream(s):
+        other = torch.zeros(2048, 2048, dtype=BF, device=DEV)
+    assert other.data_ptr() != at
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want)
+
+
+def test_expert_layers_of_two_streams_at_once():
+    """Their workspaces are the calls' own: the first one's is freed on return, while its kernels have yet to run."""
+    s = torch.cuda.Stream()
+    args = [run_moe(24, 512, 384, 12, 0, 5, 64, seed=i)[1] for i in range(2)]
+    want = [ops.moe_few(*a) for a in args]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        torch.cuda._sleep(1_000_000)
+        a, b = ops.moe_few(*args[0]), ops.moe_few(*args[1], stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
