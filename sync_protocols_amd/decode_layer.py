@@ -61,13 +61,15 @@ class ExpertLayer:
 
 class CapturedStep:
     """A step of a fixed number of tokens as one graph launch: fill `a` and
-    `residual`, call replay(), read `result`."""
+    `residual`, call replay(), read `result`. The graph holds the addresses of the
+    layer's weights as they were, so those tensors are kept with it."""
 
     def __init__(self, layer: ExpertLayer, tokens: int, heads: int):
         hidden, device = layer.gamma.numel(), layer.gamma.device
         self.a = torch.zeros(tokens, heads, dtype=torch.bfloat16, device=device)
         self.residual = torch.zeros(tokens, hidden, dtype=torch.bfloat16, device=device)
         self.workspace = layer.workspace(tokens)
+        self.weights = (layer.wo, layer.gamma, layer.router, layer.w1, layer.w2)
         side = torch.cuda.Stream(device)
         side.wait_stream(torch.cuda.current_stream(device))
         with torch.cuda.stream(side):          # the library product's own setup happens here, outside the graph

@@ -100,3 +100,19 @@ def test_expert_layers_of_two_streams_at_once():
         a, b = ops.moe_few(*args[0]), ops.moe_few(*args[1], stream=s)
         torch.cuda.synchronize()
         assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+
+
+def test_captured_step_outlives_its_layer():
+    from sync_protocols_amd import decode_layer as D
+    g = R.gen(31)
+    a, residual = torch.randn(5, 256, generator=g).bfloat16().to(DEV), torch.randn(5, 384, generator=g).bfloat16().to(DEV)
+    want = D.random_layer(384, 192, 256, 8, 8, 2, group=32, device=DEV, seed=7).step(a, residual)
+    captured = D.CapturedStep(D.random_layer(384, 192, 256, 8, 8, 2, group=32, device=DEV, seed=7), 5, 256)
+    captured.a.copy_(a)
+    captured.residual.copy_(residual)
+    for _ in range(3):
+        junk = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for n in (1 << 12, 1 << 16, 1 << 18, 1 << 20) for _ in range(8)]
+        got = captured.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got.y, want.y) and torch.equal(got.residual, want.residual)
+        del junk
