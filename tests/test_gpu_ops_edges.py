@@ -116,3 +116,52 @@ def test_captured_step_outlives_its_layer():
         torch.cuda.synchronize()
         assert torch.equal(got.y, want.y) and torch.equal(got.residual, want.residual)
         del junk
+
+
+# ------------------------------------------- tiles of the expert layer's large cases
+def check_moe_large(tokens, K, F, local, k, group, zero, kind, x_group, seed):
+    """As run_moe, an expert at a time and with the 64-bit form on the GPU."""
+    g = R.gen(seed)
+    x, xs, xv = R.make_rows(g, tokens, K, kind, x_group)
+    topk = torch.stack([torch.randperm(local, generator=g)[:k] for _ in range(tokens)]).int()
+    weights = torch.rand(tokens, k, generator=g)
+    if group:
+        p1, p2 = (dev(*R.make_w4(g, (local,), a, b, group, zero)) for a, b in ((2 * F, K), (K, F)))
+        w1, w2 = ops.W4Weight(*p1), ops.W4Weight(*p2)
+        of = lambda p, e: R.w4_values(*(None if v is None else v[e].cpu() for v in p)).to(DEV)
+        error = lambda v, p, e, w: R.w4_error(v, p[1][e], group)
+    else:
+        w1, w2 = p1, p2 = [(torch.randn(local, a, b, generator=g) / math.sqrt(b)).bfloat16().to(DEV) for a, b in ((2 * F, K), (K, F))]
+        of = lambda p, e: p[e].double()
+        error = lambda v, p, e, w: R.dense_error(v, w)
+    got = ops.moe_few(dev(x), w1, w2, dev(topk), dev(weights), x_scale=dev(xs))
+    topk, weights, xv = topk.to(DEV), weights.to(DEV), xv.to(DEV)
+    y, tol = torch.zeros(tokens, K, dtype=torch.float64, device=DEV), torch.zeros(tokens, K, dtype=torch.float64, device=DEV)
+    for e in range(local):
+        t, j = torch.nonzero(topk == e, as_tuple=True)
+        if not t.numel():
+            continue
+        a, b = of(p1, e), of(p2, e)
+        gu, d, c = xv[t] @ a.t(), error(xv[t], p1, e, a), weights[t, j].double()[:, None]
+        (gate, up), (dg, du) = gu.chunk(2, 1), d.chunk(2, 1)
+        silu = gate * torch.sigmoid(gate)
+        h = c * silu * up
+        dh = c.abs() * (1.1 * dg * (up.abs() + du) + silu.abs() * du) + (2.0 ** -16 + (8 + 2 * gate.abs()) * R.U) * h.abs()      # as in R.moe
+        y.index_add_(0, t, h @ b.t())
+        tol.index_add_(0, t, dh @ b.abs().t() + error(h, p2, e, b))
+    R.close(got, y.cpu(), (tol + R.BF16_HALF * (y.abs() + tol) + 2.0 ** -133).cpu(), "y")
+
+
+@pytest.mark.parametrize("group", [64, 128])
+@pytest.mark.parametrize("kind,x_group", [("bf16", 0), ("i8", 0), ("i8", 128), ("e4m3", 0), ("e4m3", 128)])
+@pytest.mark.parametrize("tokens,k", [(16, 4), (40, 3)])
+def test_moe_two_column_tiles_of_the_first_product(tokens, k, group, kind, x_group):
+    """64 experts of width 2048: 4096 pairs of column tiles."""
+    check_moe_large(tokens, 640, 2048, 64, k, group, group == 64, kind, x_group, tokens + group)
+
+
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("tokens,F,local,k", [(64, 256, 8, 2), (64, 128, 64, 8), (63, 384, 5, 5)])
+def test_moe_many_tokens_and_columns_of_the_second_product(tokens, F, local, k, group):
+    """Two column tiles over 64 tokens: 64 KB of sums beside the plan."""
+    check_moe_large(tokens, 4096, F, local, k, group, True, "bf16", 0, tokens + F)
