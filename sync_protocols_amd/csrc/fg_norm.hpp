@@ -76,16 +76,26 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* buf) {
   return v;
 }
 
-// Eight codes of one row from element e on. inv = Q / a keeps |v| within a
+// Q / a would leave fp32 for a below 2^-118, and make zeros NaN: numbers that small
+// are taken by 2^100 first, exactly.
+struct Inverse {
+  float up, inv;
+  __device__ __forceinline__ Inverse(float m, float top) {
+    up = m < 0x1p-100f ? 0x1p100f : 1.0f;
+    inv = m > 0.0f ? top / (m * up) : 0.0f;
+  }
+};
+
+// Eight codes of one row from element e on. Q / a keeps |v| within a
 // rounding of Q and the clamp takes that rounding off; a row (group) with a NaN or an
 // infinity has a scale that says so, and its codes mean nothing.
 template <bool PAST>
-__device__ __forceinline__ void quantise8(const NormArgs& a, int64_t row, int e, int left, float inv, const float (&y)[8]) {
+__device__ __forceinline__ void quantise8(const NormArgs& a, int64_t row, int e, int left, Inverse by, const float (&y)[8]) {
   u32x2 v = {0u, 0u};
   if (a.q_type == FG_I8) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float f = __builtin_rintf(y[j] * inv);
+      const float f = __builtin_rintf(y[j] * by.up * by.inv);
       v[j / 4] |= ((uint32_t)(int)fminf(fmaxf(f, -127.0f), 127.0f) & 0xffu) << (8 * (j % 4));
     }
   } else {
@@ -94,7 +104,7 @@ __device__ __forceinline__ void quantise8(const NormArgs& a, int64_t row, int e,
       float f[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        f[k] = y[j + k] * inv;
+        f[k] = y[j + k] * by.up * by.inv;
         f[k] = f[k] > 448.0f ? 448.0f : f[k] < -448.0f ? -448.0f : f[k];
       }
       int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
@@ -180,18 +190,18 @@ __global__ __launch_bounds__(NormShape<W>::kThreads) void add_rmsnorm_kernel(Nor
     if (a.q && a.group && left > 0) {
       const float m = __uint_as_float(amax), top = a.q_type == FG_I8 ? 127.0f : 448.0f;
       if ((t & 15) == 0) a.scale[row * (a.n / 128) + e / 128] = m / top;
-      quantise8<PAST>(a, row, e, left, m > 0.0f ? top / m : 0.0f, h[i]);
+      quantise8<PAST>(a, row, e, left, Inverse(m, top), h[i]);
     }
     if (a.group) amax = 0;
   }
   if (a.q && !a.group) {
     const float m = __uint_as_float(row_max<W>(amax, mbuf)), top = a.q_type == FG_I8 ? 127.0f : 448.0f;
     if (t == 0) a.scale[row] = m / top;
-    const float inv = m > 0.0f ? top / m : 0.0f;
+    const Inverse by(m, top);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = 8 * (t + 64 * W * i);
-      if (a.n - e > 0) quantise8<PAST>(a, row, e, a.n - e, inv, h[i]);
+      if (a.n - e > 0) quantise8<PAST>(a, row, e, a.n - e, by, h[i]);
     }
   }
 }

@@ -165,3 +165,25 @@ def test_moe_two_column_tiles_of_the_first_product(tokens, k, group, kind, x_gro
 def test_moe_many_tokens_and_columns_of_the_second_product(tokens, F, local, k, group):
     """Two column tiles over 64 tokens: 64 KB of sums beside the plan."""
     check_moe_large(tokens, 4096, F, local, k, group, True, "bf16", 0, tokens + F)
+
+
+# --------------------------------------------------------------------- norm
+@pytest.mark.parametrize("out", ["i8", "e4m3"])
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("n", [256, 2048, 20096])
+@pytest.mark.parametrize("top", [2.0 ** -118, 2.0 ** -121, 2.0 ** -126, 2.0 ** -133, 2.0 ** -143])
+def test_norm_tiny_rows(n, out, group, top):
+    """Zeros and numbers whose maximum, about 2^10 x, is too small for its reciprocal; the last are below what gamma leaves of them."""
+    g = R.gen(n)
+    down = 100 if top < 2.0 ** -123 else 0   # bf16's smallest numbers are 2^-133: the rest by gamma
+    x = (torch.randn(4, n, generator=g).double().clamp(-2, 2) * top * 2.0 ** (down - 10)).bfloat16()
+    x[:, ::3] = 0
+    x[1, n // 2:] = 0
+    gamma = torch.full((n,), 2.0 ** -down).bfloat16()
+    got = ops.add_rmsnorm(dev(x), dev(gamma), eps=2.0 ** -20, out=out, group=group, keep_bf16=True)
+    assert got.scale.isfinite().all() and got.q.float().isfinite().all()
+    assert (got.q[:, ::3].float() == 0).all() and (got.q[1, n // 2:].float() == 0).all()
+    check_norm(got, x, gamma, None, 2.0 ** -20, out, group)
+    if top == 2.0 ** -118:                   # scales that fp32 holds in full: codes that use their range
+        v = R.groups_of(got.q.float(), group).abs().amax(-1)
+        assert ((v == 0) == (got.scale == 0)).all() and (v[got.scale > 0] >= 0.99 * R.TOP[out]).all()
