@@ -494,7 +494,8 @@ fg_status fg_moe_route(const void* logits, int64_t ld, int32_t logits_type, int6
  *   w:       uint8 [n][k / 2], 16-byte aligned; element k of a row is the low
  *            (even k) or high nibble of byte k / 2
  *   w_scale: bf16 [n][k / group]; group 32, 64 or 128, k % group == 0
- *   w_zero:  uint8 [n][k / group] or NULL (8 everywhere)
+ *   w_zero:  uint8 [n][k / group] or NULL (8 everywhere); with FG_I8 rows 0..128,
+ *            one above makes its column NaN
  *   bias:    bf16 [n] or NULL;  out: bf16 [rows][ldo]; n any up to FG_FEW_MAX_SIZE
  *   rows:    any up to FG_W4_MAX_ROWS; made for 1 to 64 (more re-read the weights)
  * An infinity in x gives NaN in the whole row of out. */

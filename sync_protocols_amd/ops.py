@@ -43,7 +43,8 @@ class NormResult(NamedTuple):
 
 class W4Weight(NamedTuple):
     """4-bit weights [.., n, k]: `q` uint8 [.., n, k // 2], the low nibble first;
-    `scale` bf16 [.., n, k // group]; `zero` uint8 like scale, or None (8)."""
+    `scale` bf16 [.., n, k // group]; `zero` uint8 like scale, or None (8). With int8
+    activations a zero point above 128 makes its row's results NaN."""
     q: torch.Tensor
     scale: torch.Tensor
     zero: Optional[torch.Tensor] = None

@@ -187,3 +187,35 @@ def test_norm_tiny_rows(n, out, group, top):
     if top == 2.0 ** -118:                   # scales that fp32 holds in full: codes that use their range
         v = R.groups_of(got.q.float(), group).abs().amax(-1)
         assert ((v == 0) == (got.scale == 0)).all() and (v[got.scale > 0] >= 0.99 * R.TOP[out]).all()
+
+
+# ------------------------------------------------------------- zero points
+@pytest.mark.parametrize("zero", [16, 127, 128, 129, 200, 255])
+@pytest.mark.parametrize("kind", ["bf16", "i8", "e4m3"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("rows", [1, 3, 33])
+def test_w4_every_zero_point(rows, group, kind, zero):
+    """Zero points a byte holds, 16 and more among them; the tolerance is that of sums of up to 255 |x| s instead of 15.
+    int8 rows take them up to 128: a column with a larger one is NaN, the others are what they are without it."""
+    k, n = 384, 40
+    g = R.gen(zero + rows)
+    q, s, z = R.make_w4(g, (), n, k, group, True)
+    z[::2] = zero                                                     # and ordinary ones beside them
+    x, xs, xv = R.make_rows(g, rows, k, kind, 0)
+    got = ops.w4_linear(dev(x), ops.W4Weight(*dev(q, s, z)), x_scale=dev(xs))
+    want = xv @ R.w4_values(q, s, z).t()
+    if kind == "i8" and zero > 128:
+        want[:, ::2] = math.nan
+    tol = 255 / 15 * R.w4_error(xv, s, group)
+    R.close(got, want, tol + R.BF16_HALF * (want.abs() + tol), "out")
+
+
+def test_w4_int8_zero_points_are_exact():
+    """Whole numbers below 2^24 throughout: only the result's rounding is left."""
+    k, n = 128, 129
+    q = torch.full((n, k // 2), 0xF0, dtype=torch.uint8)
+    z = torch.arange(129, dtype=torch.uint8)[:, None].expand(n, 2).contiguous()      # all that int8 rows take
+    x = torch.tensor([[127] * k, [-127] * k, [127, -127] * (k // 2), [-127, 126] * (k // 2)], dtype=torch.int8)
+    w = ops.W4Weight(*dev(q, torch.ones(n, 2).bfloat16(), z))
+    got = ops.w4_linear(dev(x), w, x_scale=torch.ones(4, device=DEV))
+    assert torch.equal(got.cpu(), (x.double() @ R.w4_values(q, torch.ones(n, 2).bfloat16(), z).t()).bfloat16())
