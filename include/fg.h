@@ -478,7 +478,8 @@ fg_status fg_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64
  * index (NaN counts as -infinity), and their gate weights
  *   p = softmax over all experts, or sigmoid;  weight = p * scale, with renorm
  *   != 0 divided by the sum of the token's k picks (0 where that sum is 0).
- * The outputs are what a TOPK route, fg_combine and fg_moe_few take.
+ * The outputs are what a TOPK route, fg_combine and fg_moe_few take; they share no
+ * memory with the logits or each other.
  *   logits:  fp32 or bf16 (logits_type) [rows][ld], experts <= FG_MOE_FEW_EXPERTS
  *   topk:    int32 [rows][k], k <= min(experts, 64);  weights: fp32 [rows][k] */
 fg_status fg_moe_route(const void* logits, int64_t ld, int32_t logits_type, int64_t rows, int32_t experts, int32_t k,
@@ -496,7 +497,8 @@ fg_status fg_moe_route(const void* logits, int64_t ld, int32_t logits_type, int6
  *   w_scale: bf16 [n][k / group]; group 32, 64 or 128, k % group == 0
  *   w_zero:  uint8 [n][k / group] or NULL (8 everywhere); with FG_I8 rows 0..128,
  *            one above makes its column NaN
- *   bias:    bf16 [n] or NULL;  out: bf16 [rows][ldo]; n any up to FG_FEW_MAX_SIZE
+ *   bias:    bf16 [n] or NULL;  out: bf16 [rows][ldo], sharing no memory with the
+ *            inputs (rows may interleave with theirs); n any up to FG_FEW_MAX_SIZE
  *   rows:    any up to FG_W4_MAX_ROWS; made for 1 to 64 (more re-read the weights)
  * An infinity in x gives NaN in the whole row of out. */
 fg_status fg_w4_linear(const void* x, int64_t ldx, int32_t x_type, const float* x_scale, int32_t x_group, const void* w,
@@ -523,7 +525,8 @@ fg_status fg_moe_few_bytes(int32_t tokens, int32_t k, int32_t F, int64_t* bytes)
  *            an expert take less than 4 GB
  *   workspace: fg_moe_few_bytes(tokens, k, F) bytes, 16-byte aligned, contents
  *            free; calls that may overlap need one each
- *   y:       bf16 [tokens][ldy] */
+ *   y:       bf16 [tokens][ldy]; it may be x. Neither it nor the workspace shares
+ *            memory with anything else */
 fg_status fg_moe_few(const void* x, int64_t ldx, int32_t x_type, const float* x_scale, int32_t x_group, const void* w1,
                      const void* w1_scale, const void* w1_zero, const void* w2, const void* w2_scale, const void* w2_zero,
                      int32_t group, const int32_t* topk, const float* weights, int32_t tokens, int32_t k,

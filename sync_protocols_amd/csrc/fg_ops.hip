@@ -27,6 +27,34 @@ constexpr int kCUs = 256;          // compute units of the part
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+// Rows of `bytes` bytes, `pitch` apart (one row: any pitch).
+struct Rows {
+  const void* p;
+  int64_t rows, bytes, pitch;
+  uintptr_t begin() const { return (uintptr_t)p; }
+  uintptr_t end() const { return begin() + (rows - 1) * pitch + bytes; }
+};
+Rows whole(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
+
+// Do they share a byte? Rows that interleave, as columns of one buffer do, need not.
+bool overlap(const Rows& a, const Rows& b) {
+  if (!a.p || !b.p || a.end() <= b.begin() || b.end() <= a.begin()) return false;
+  if (a.rows > b.rows) return overlap(b, a);
+  if (a.pitch == b.pitch && a.rows > 1) {
+    const int64_t d = (int64_t)(b.begin() - a.begin()) % a.pitch, shift = d < 0 ? d + a.pitch : d;
+    if (shift >= a.bytes && shift + b.bytes <= a.pitch) return false;
+  }
+  for (int64_t i = 0; i < a.rows; ++i) {         // the last row of b that starts before the end of a's
+    const uintptr_t from = a.begin() + i * a.pitch, to = from + a.bytes;
+    if (to <= b.begin()) continue;
+    const int64_t j = b.rows == 1 ? 0 : (int64_t)((to - 1 - b.begin()) / b.pitch);
+    if (b.begin() + (j < b.rows ? j : b.rows - 1) * b.pitch + b.bytes > from) return true;
+  }
+  return false;
+}
+template <class... Others>
+bool overlaps(const Rows& a, const Others&... others) { return (overlap(a, others) || ...); }
+
 int pow2_at_least(int v) {
   int p = 1;
   while (p < v) p *= 2;
@@ -249,6 +277,9 @@ fg_status fg_moe_route(const void* logits, int64_t ld, int32_t logits_type, int6
   if (rows == 0) return FG_OK;
   if (!logits || !topk || !weights || ld < experts) return FG_EINVAL;
   if (!aligned(logits, logits_type == FG_F32 ? 4 : 2) || !aligned(topk, 4) || !aligned(weights, 4)) return FG_EINVAL;
+  const int64_t element = logits_type == FG_F32 ? 4 : 2;
+  const Rows in{logits, rows, element * experts, element * ld}, picks = whole(topk, 4 * rows * k), gates = whole(weights, 4 * rows * k);
+  if (overlaps(picks, in, gates) || overlaps(gates, in)) return FG_EINVAL;
   Launches go{stream};
   RouteArgs a{logits, topk, weights, ld, rows, experts, k, score, renorm, scale};
   logits_type == FG_BF16 ? launch_route<true>(a, go) : launch_route<false>(a, go);
@@ -261,6 +292,12 @@ fg_status fg_w4_linear(const void* x, int64_t ldx, int32_t x_type, const float* 
   if (rows < 0 || rows > FG_W4_MAX_ROWS || n < 1 || k < 1 || n > FG_FEW_MAX_SIZE || k > FG_FEW_MAX_SIZE || !w4_ok(w, w_scale, group, k)) return FG_EINVAL;
   if (rows == 0) return FG_OK;
   if (!rows_ok(x, ldx, x_type, x_scale, x_group, k) || !out || ldo < n || !aligned(out, 2) || !aligned(bias, 2)) return FG_EINVAL;
+  const int64_t element = x_type == FG_BF16 ? 2 : 1, groups = k / group;
+  // workgroups write their columns while others still read
+  if (overlaps(Rows{out, rows, 2 * (int64_t)n, 2 * ldo}, Rows{x, rows, element * k, element * ldx},
+               whole(x_scale, 4 * rows * (x_group ? k / x_group : 1)), whole(w, (int64_t)n * k / 2), whole(w_scale, 2 * n * groups),
+               whole(w_zero, n * groups), whole(bias, 2 * (int64_t)n)))
+    return FG_EINVAL;
   Launches go{stream};
   W4Args a{};
   a.x = (const char*)x; a.xs = x_scale; a.w = (const char*)w; a.s = (const uint16_t*)w_scale; a.z = (const uint8_t*)w_zero;
@@ -298,6 +335,17 @@ fg_status fg_moe_few(const void* x, int64_t ldx, int32_t x_type, const float* x_
   if (!rows_ok(x, ldx, x_type, x_scale, x_group, K) || !topk || !weights || !y || ldy < K) return FG_EINVAL;
   if (!aligned(topk, 4) || !aligned(weights, 4) || !aligned(y, 2)) return FG_EINVAL;
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < 4 * (int64_t)tokens * k * F) return FG_EINVAL;
+  {
+    // the first kernel reads all but w2 and writes the workspace, the second reads w2, topk and the workspace and writes y
+    const int64_t element = x_type == FG_BF16 ? 2 : 1, elements = (int64_t)n_local * K * F, per = group ? group : 1, picks = 4 * (int64_t)tokens * k;
+    const int64_t bytes = group ? elements / 2 : 2 * elements;
+    const Rows h = whole(workspace, picks * F), sum{y, tokens, 2 * (int64_t)K, 2 * ldy}, ids = whole(topk, picks);
+    const Rows b = whole(w2, bytes), sb = whole(w2_scale, 2 * elements / per), zb = whole(w2_zero, elements / per);
+    if (overlaps(h, ids, sum, b, sb, zb, Rows{x, tokens, element * K, element * ldx}, whole(x_scale, 4 * (int64_t)tokens * (x_group ? K / x_group : 1)),
+                 whole(weights, picks), whole(w1, 2 * bytes), whole(w1_scale, 4 * elements / per), whole(w1_zero, 2 * elements / per)) ||
+        overlaps(sum, ids, b, sb, zb))
+      return FG_EINVAL;
+  }
   // a grid of fewer than 2^32 threads
   if ((int64_t)n_local * ((F + 15) / 16) > (1 << 23)) return FG_EINVAL;
   Launches go{stream};

@@ -219,3 +219,38 @@ def test_w4_int8_zero_points_are_exact():
     w = ops.W4Weight(*dev(q, torch.ones(n, 2).bfloat16(), z))
     got = ops.w4_linear(dev(x), w, x_scale=torch.ones(4, device=DEV))
     assert torch.equal(got.cpu(), (x.double() @ R.w4_values(q, torch.ones(n, 2).bfloat16(), z).t()).bfloat16())
+
+
+# ------------------------------------------------------------ shared memory
+def test_outputs_beside_their_inputs_in_one_buffer():
+    """Rows that interleave without sharing a byte are taken; moe_few may write over its own x."""
+    g = R.gen(41)
+    w = ops.W4Weight(*dev(*R.make_w4(g, (), 64, 128, 64, True)))
+    x = torch.randn(20, 128, generator=g).bfloat16().to(DEV)
+    want = ops.w4_linear(x, w)
+    for first, gap in ((0, 0), (0, 8), (64, 0), (72, 8)):             # x before out in each row, or after it
+        big = torch.zeros(20, 128 + 64 + gap + 8, dtype=BF, device=DEV)
+        xv = big[:, first:first + 128]
+        out = big[:, 128 + gap:192 + gap] if first == 0 else big[:, :64]
+        xv.copy_(x)
+        assert torch.equal(ops.w4_linear(xv, w, out=out), want) and torch.equal(xv, x)
+    logits = torch.randn(9, 24, generator=g).to(DEV)
+    topk, weights = ops.moe_route(logits, 4)
+    big = torch.empty(3 * 9 * 24, device=DEV)
+    big[:216] = logits.flatten()
+    got = ops.moe_route(big[:216].view(9, 24), 4, topk=big[216:252].view(torch.int32).view(9, 4), weights=big[252:288].view(9, 4))
+    assert torch.equal(got[0], topk) and torch.equal(got[1], weights)
+    want, args = run_moe(6, 128, 64, 4, 0, 2)
+    x = args[0]
+    assert torch.equal(ops.moe_few(*args, out=x), want)
+
+
+@pytest.mark.parametrize("shift", [0, 8, 127])
+def test_w4_refuses_to_write_over_its_own_input(shift):
+    from sync_protocols_amd import fg
+    w = ops.W4Weight(*dev(*R.make_w4(R.gen(1), (), 128, 128, 64, False)))
+    big = torch.randn(8, 256, device=DEV).bfloat16()
+    before = big.clone()
+    with pytest.raises(fg.FgError):
+        ops.w4_linear(big[:, :128], w, out=big[:, shift:shift + 128])
+    assert torch.equal(big, before)

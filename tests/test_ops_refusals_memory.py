@@ -1,0 +1,35 @@
+"""Refusals of outputs that lie on inputs, and of sizes no grid holds, without a GPU: nothing is launched."""
+import pytest
+
+from sync_protocols_amd import fg
+from test_ops_refusals import P, _moe, _route, _w4
+
+FAR = P + (1 << 30)      # the outputs, away from everything that lies at P
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=P), dict(out=P, n=256, ldo=256), dict(out=P + 2, n=1, ldo=1), dict(x=FAR + 112), dict(x=FAR + 48, rows=1), dict(w=FAR),
+    dict(w=FAR - 32 * 128 + 16), dict(s=FAR + 62), dict(s=FAR - 62), dict(z=FAR + 127), dict(b=FAR + 2), dict(t=1, xs=FAR + 4),
+    dict(t=1, xs=FAR + 120, xg=128), dict(x=FAR - 512 * 3 + 16, ldx=768, rows=2), dict(x=FAR, ldx=64, k=64, g=32, n=32, ldo=40, rows=20)])
+def test_w4_refuses_out_on_an_input(kw):
+    a = dict(out=FAR)
+    a.update(kw)
+    assert _w4(**a) == fg.EINVAL
+
+
+@pytest.mark.parametrize("kw", [dict(topk=P), dict(w=P), dict(topk=P + 63 * 4), dict(w=P + 4 * 64 + 4), dict(topk=FAR, w=FAR + 4), dict(l=FAR + 32, w=P)])
+def test_route_refuses_outputs_on_its_logits_or_each_other(kw):
+    a = dict(topk=FAR, w=FAR + 4096)
+    a.update(kw)
+    assert _route(**a) == fg.EINVAL
+
+
+@pytest.mark.parametrize("kw", [
+    dict(ws=P), dict(y=P + (1 << 24), ws=P + (1 << 24)), dict(y=FAR + 16 + 4 * 2 * 2 * 64 - 2, ws=FAR + 16), dict(topk=FAR + 8), dict(topk=FAR - 12), dict(w2=FAR),
+    dict(w=FAR + (1 << 20) + 4), dict(x=FAR + (1 << 20) + 16), dict(w1=FAR + (1 << 20)), dict(g=32, s1=FAR + (1 << 20), s2=P), dict(g=32, s1=P, s2=FAR),
+    dict(g=32, s1=P, s2=P, z2=FAR + 7), dict(g=32, s1=P, s2=P, z1=FAR + (1 << 20)), dict(t=1, xs=FAR + (1 << 20))])
+def test_moe_refuses_outputs_on_what_it_still_reads(kw):
+    """y may lie on x: the first kernel has read it."""
+    a = dict(y=FAR, ws=FAR + (1 << 20))
+    a.update(kw)
+    assert _moe(**a) == fg.EINVAL
