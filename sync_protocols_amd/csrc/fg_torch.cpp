@@ -7,6 +7,7 @@
 // (out of memory) pass through as they are.
 #include <Python.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/StreamGuard.h>
@@ -136,7 +137,13 @@ struct Call {
   void use(const Tensor* t) {
     if (!t) return;
     if (t->device() != device) refuse("tensors are on different devices");
+    no_gradient(*t);
     used[n++] = t;
+  }
+  // The results have no gradient function, so a tensor that needs one is no input (nor an output buffer).
+  static void no_gradient(const Tensor& t) {
+    if (t.requires_grad() && at::GradMode::is_enabled())
+      refuse("the decoding operators have no backward pass: call them under torch.no_grad() or detach their inputs");
   }
   // Memory of the launching stream.
   Tensor memory(at::IntArrayRef shape, ScalarType type) const {
@@ -144,12 +151,16 @@ struct Call {
     return at::detail::empty_cuda(shape, type, device, std::nullopt);
   }
   void check(const Tensor* given, at::IntArrayRef shape, ScalarType type, const char* what) const {
-    if (given && (!is_type(*given, type) || !is_shape(*given, shape) || given->device() != device)) refuse(what);
+    if (!given) return;
+    if (!is_type(*given, type) || !is_shape(*given, shape) || given->device() != device) refuse(what);
+    no_gradient(*given);
   }
-  // The output `given`, which has been checked, or a new one.
+  // The output `given`, which has been checked, or a new one. Autograd, which may have
+  // saved a given one, is told that it is written.
   Tensor out(const Tensor* given, at::IntArrayRef shape, ScalarType type) {
     if (given) {
       use(given);
+      if (!given->is_inference()) given->unsafeGetTensorImpl()->bump_version();
       return *given;
     }
     const Tensor t = memory(shape, type);
@@ -249,8 +260,8 @@ PyObject* add_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
       if (!scale_in->is_contiguous()) refuse("scale must be contiguous");
     }
     const float eps = (float)number(a[3]);
-    c.on(a[11]);
     c.use(&x); c.use(&gamma); c.use(res);
+    c.on(a[11]);
     Tensor sum, y, q, scale;
     if (has_sum) sum = c.out(sum_in, x.sizes(), at::kBFloat16);
     if (has_y) y = c.out(y_in, x.sizes(), at::kBFloat16);
@@ -289,8 +300,8 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     if ((topk_in && !topk_in->is_contiguous()) || (w_in && !w_in->is_contiguous())) refuse("topk and weights must be contiguous");
     const bool renorm = truth(a[3]);
     const float scale = (float)number(a[4]);
-    c.on(a[7]);
     c.use(&l);
+    c.on(a[7]);
     const Tensor topk = c.out(topk_in, shape, at::kInt), w = c.out(w_in, shape, at::kFloat);
     launch(c, "fg_moe_route", [&] {
       return fg_moe_route(l.data_ptr(), ld(l), is_type(l, at::kFloat) ? FG_F32 : FG_BF16, rows, (int32_t)experts, (int32_t)k,
@@ -360,8 +371,8 @@ PyObject* w4_linear(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     Call c(x);
     const int64_t rows = x.size(0), shape[2] = {rows, n};
     if (out_in) { c.check(out_in, shape, at::kBFloat16, "out must be bf16 [rows, n]"); ROWS2D(*out_in, "out"); }
-    c.on(a[7]);
     c.use(&x); c.use(xs); c.use(w.q); c.use(w.scale); c.use(w.zero); c.use(bias);
+    c.on(a[7]);
     const Tensor out = c.out(out_in, shape, at::kBFloat16);
     launch(c, "fg_w4_linear", [&] {
       return fg_w4_linear(x.data_ptr(), ld(x), act.type, (const float*)ptr(xs), act.group, w.q->data_ptr(), w.scale->data_ptr(),
@@ -408,9 +419,9 @@ PyObject* moe_few(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int64_t shape[2] = {tokens, K};
     if (out_in) { c.check(out_in, shape, at::kBFloat16, "out must be bf16 [tokens, K]"); ROWS2D(*out_in, "out"); }
     if (ws_in && !ws_in->is_contiguous()) refuse("workspace must be contiguous");
-    c.on(a[13]);
     c.use(&x); c.use(xs); c.use(w1.q); c.use(w1.scale); c.use(w1.zero); c.use(w2.q); c.use(w2.scale); c.use(w2.zero);
     c.use(&topk); c.use(&weights); c.use(ws_in);
+    c.on(a[13]);
     const Tensor out = c.out(out_in, shape, at::kBFloat16);
     const int64_t need[1] = {4 * tokens * k * F};
     const Tensor ws = ws_in ? *ws_in : c.memory(need, at::kByte);

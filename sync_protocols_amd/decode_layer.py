@@ -35,7 +35,8 @@ class ExpertLayer:
     """Weights of the half layer. `wo` [hidden, heads] 4-bit; gamma bf16 [hidden];
     router bf16 [experts, hidden]; w1 [n_local, 2 width, hidden] and w2 [n_local,
     hidden, width], both 4-bit or both bf16. `norm_out` is the type of the experts'
-    input: "e4m3" and "i8" (scales per 128 columns where hidden allows) or "bf16"."""
+    input: "e4m3" and "i8" (scales per 128 columns where hidden allows) or "bf16".
+    Parameters serve as weights under torch.no_grad(): a step has no backward pass."""
 
     def __init__(self, wo: ops.W4Weight, gamma: torch.Tensor, router: torch.Tensor, w1, w2, top_k: int, *, expert_base: int = 0,
                  score: str = "softmax", eps: float = 1e-6, norm_out: str = "e4m3"):

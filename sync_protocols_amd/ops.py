@@ -8,6 +8,9 @@ fg.FgError (code fg.EINVAL) for arguments it does not take. Outputs are allocate
 unless given. All of them may be captured into a graph; nothing is kept between
 calls. The formulas and limits stand at the entry points in include/fg.h.
 
+There is no backward pass: tensors that require gradients are refused unless
+gradients are off (torch.no_grad()). Given buffers count as written in place.
+
 With `stream`, the caller orders that stream after whatever makes the inputs (and
 last used given outputs), and the use of the outputs after that stream. What a call
 allocates comes from that stream's memory, so it needs no further order; tensors of

@@ -254,3 +254,26 @@ def test_w4_refuses_to_write_over_its_own_input(shift):
     with pytest.raises(fg.FgError):
         ops.w4_linear(big[:, :128], w, out=big[:, shift:shift + 128])
     assert torch.equal(big, before)
+
+
+# ------------------------------------------------------------------ autograd
+def test_given_outputs_count_as_written():
+    """What autograd has saved and a call then overwrites is noticed; without gradients parameters are taken."""
+    g = R.gen(51)
+    x, gamma = torch.randn(4, 128, generator=g).bfloat16().to(DEV), torch.nn.Parameter(torch.ones(128, dtype=BF, device=DEV))
+    w = ops.W4Weight(*dev(*R.make_w4(g, (), 128, 128, 64, True)))
+    buffers = dict(sum=torch.empty_like(x), y=torch.empty_like(x), q=torch.empty_like(x, dtype=torch.int8), scale=torch.empty(4, 1, device=DEV))
+    before = {k: t._version for k, t in buffers.items()}
+    with torch.no_grad():
+        ops.add_rmsnorm(x, gamma, residual=x, out="i8", **buffers)
+    assert all(t._version > before[k] for k, t in buffers.items())
+    leaf = torch.randn(4, 128, device=DEV, requires_grad=True)
+    held = torch.randn(4, 128, device=DEV).bfloat16()
+    loss = (leaf * held).sum()
+    ops.w4_linear(x, w, out=held)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        out = torch.empty(4, 128, dtype=BF, device=DEV)
+    ops.w4_linear(x, w, out=out)                                      # has no version to raise
+    assert torch.equal(out, held)

@@ -1,7 +1,8 @@
-"""Refusals of outputs that lie on inputs, and of sizes no grid holds, without a GPU: nothing is launched."""
+"""Refusals of outputs that lie on inputs, of gradients, and of sizes no grid holds, without a GPU: nothing is launched."""
 import pytest
+import torch
 
-from sync_protocols_amd import fg
+from sync_protocols_amd import fg, ops
 from test_ops_refusals import P, _moe, _route, _w4
 
 FAR = P + (1 << 30)      # the outputs, away from everything that lies at P
@@ -33,3 +34,42 @@ def test_moe_refuses_outputs_on_what_it_still_reads(kw):
     a = dict(y=FAR, ws=FAR + (1 << 20))
     a.update(kw)
     assert _moe(**a) == fg.EINVAL
+
+
+# ------------------------------------------------------------------ autograd
+
+def _grad(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16, requires_grad=True)
+
+
+def _bf(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+W = ops.W4Weight(torch.zeros(32, 128, dtype=torch.uint8), _bf(32, 2))
+PICKS = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, 2)
+CALLS = [
+    lambda: ops.add_rmsnorm(_grad(2, 8), _bf(8)),
+    lambda: ops.add_rmsnorm(_bf(2, 8), _grad(8)),
+    lambda: ops.add_rmsnorm(_bf(2, 8), _bf(8), residual=_grad(2, 8)),
+    lambda: ops.add_rmsnorm(_bf(2, 8), _bf(8), y=_grad(2, 8)),
+    lambda: ops.add_rmsnorm(_grad(2, 8) * 2, _bf(8)),
+    lambda: ops.moe_route(_grad(2, 8), 2),
+    lambda: ops.w4_linear(_grad(2, 256), W),
+    lambda: ops.w4_linear(_bf(2, 256), ops.W4Weight(W.q, _grad(32, 2))),
+    lambda: ops.w4_linear(_bf(2, 256), W, bias=_grad(32)),
+    lambda: ops.w4_linear(_bf(2, 256), W, out=_grad(2, 32)),
+    lambda: ops.moe_few(_grad(2, 64), _bf(4, 64, 64), _bf(4, 64, 32), *PICKS),
+    lambda: ops.moe_few(_bf(2, 64), _grad(4, 64, 64), _bf(4, 64, 32), *PICKS),
+    lambda: ops.moe_few(_bf(2, 64), _bf(4, 64, 64), _bf(4, 64, 32), PICKS[0], PICKS[1].clone().requires_grad_()),
+]
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_tensors_that_require_gradients_are_refused(call):
+    """There is no backward pass: a result cut off from its inputs would be a silent loss."""
+    with pytest.raises(fg.FgError, match="no backward pass") as e:
+        call()
+    assert e.value.code == fg.EINVAL
+    with torch.no_grad(), pytest.raises(fg.FgError, match="on the GPU"):      # the next refusal, of these CPU tensors
+        call()
