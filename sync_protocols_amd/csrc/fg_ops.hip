@@ -346,8 +346,6 @@ fg_status fg_moe_few(const void* x, int64_t ldx, int32_t x_type, const float* x_
         overlaps(sum, ids, b, sb, zb))
       return FG_EINVAL;
   }
-  // a grid of fewer than 2^32 threads
-  if ((int64_t)n_local * ((F + 15) / 16) > (1 << 23)) return FG_EINVAL;
   Launches go{stream};
   MoeArgs a{};
   a.x = (const char*)x; a.xs = x_scale; a.topk = topk; a.weights = weights;
@@ -357,6 +355,9 @@ fg_status fg_moe_few(const void* x, int64_t ldx, int32_t x_type, const float* x_
   a.y = (uint16_t*)y;
   a.ldx = ldx * (x_type == FG_BF16 ? 2 : 1); a.xs_stride = x_group ? K / x_group : 1; a.ldy = ldy;
   a.tokens = tokens; a.k = k; a.base = expert_base; a.n_local = n_local; a.K = K; a.F = F;
+  // a grid of fewer than 2^32 threads: the first product's workgroups have 256, those of 4-bit weights and many rows 512
+  const int64_t workgroups = (int64_t)n_local * ((F + 15) / 16);
+  if (workgroups > 1 << 23 || (workgroups == 1 << 23 && group && many_rows(a))) return FG_EINVAL;
   const bool grouped = x_group != 0;
   if (group == 0) return launch_moe<0>(a, x_type, grouped, go);
   if (group == 32) return launch_moe<32>(a, x_type, grouped, go);

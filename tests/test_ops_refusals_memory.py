@@ -73,3 +73,11 @@ def test_tensors_that_require_gradients_are_refused(call):
     assert e.value.code == fg.EINVAL
     with torch.no_grad(), pytest.raises(fg.FgError, match="on the GPU"):      # the next refusal, of these CPU tensors
         call()
+
+
+# --------------------------------------------------------------------- grids
+def test_moe_refuses_the_first_grid_of_eight_waves_that_does_not_fit():
+    """2^23 workgroups of 512 threads are 2^32 threads: 8 experts of 2^24 columns, more than 16 tokens each."""
+    far = 1 << 45
+    many = dict(tokens=64, k=4, e=8, K=32, ldx=32, F=1 << 24, g=32, s1=P, s2=P, ldy=32, wsb=1 << 45, ws=far, y=far - 65536)
+    assert _moe(**many) == fg.EINVAL
