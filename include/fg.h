@@ -475,9 +475,10 @@ fg_status fg_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64
                          int32_t q_group, float* q_scale, int64_t rows, int32_t n, hipStream_t stream);
 
 /* Router: each token's k largest logits, largest first, equal ones by lowest
- * index (NaN counts as -infinity), and their gate weights
+ * index (NaN after -infinity and weighted like it), and their gate weights
  *   p = softmax over all experts, or sigmoid;  weight = p * scale, with renorm
  *   != 0 divided by the sum of the token's k picks (0 where that sum is 0).
+ * +infinity among a token's logits makes its softmax weights NaN.
  * The outputs are what a TOPK route, fg_combine and fg_moe_few take; they share no
  * memory with the logits or each other.
  *   logits:  fp32 or bf16 (logits_type) [rows][ld], experts <= FG_MOE_FEW_EXPERTS

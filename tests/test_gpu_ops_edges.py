@@ -277,3 +277,23 @@ def test_given_outputs_count_as_written():
         out = torch.empty(4, 128, dtype=BF, device=DEV)
     ops.w4_linear(x, w, out=out)                                      # has no version to raise
     assert torch.equal(out, held)
+
+
+# --------------------------------------------------------------------- route
+@pytest.mark.parametrize("experts", [2, 7, 64, 300])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_nan_comes_after_minus_infinity(experts, dtype, score):
+    logits = torch.full((6, experts), -math.inf)
+    logits[0, 0] = math.nan                                              # of [NaN, -inf, ..] the second is first
+    logits[1, ::2] = math.nan
+    logits[2, -1] = 1.0
+    logits[2, 0] = math.nan
+    logits[3, :-1] = math.nan
+    logits[4] = math.nan
+    logits[5, 1] = math.inf                                              # softmax: NaN weights
+    logits = logits.to(dtype)
+    k = min(experts, 6)
+    for renorm in (True, False):
+        check_route(ops.moe_route(dev(logits), k, score=score, renorm=renorm), logits, k, score, renorm, 1.0)
+    assert ops.moe_route(dev(logits), k)[0][0, 0] == 1
