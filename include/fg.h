@@ -501,7 +501,8 @@ fg_status fg_moe_route(const void* logits, int64_t ld, int32_t logits_type, int6
  *   bias:    bf16 [n] or NULL;  out: bf16 [rows][ldo], sharing no memory with the
  *            inputs (rows may interleave with theirs); n any up to FG_FEW_MAX_SIZE
  *   rows:    any up to FG_W4_MAX_ROWS; made for 1 to 64 (more re-read the weights)
- * An infinity in x gives NaN in the whole row of out. */
+ * An infinity in bf16 x gives NaN in the whole row of out (the product and the sum of
+ * x are both infinite); magnitudes from 2^113 on may, as sums of 143 |x| are formed. */
 fg_status fg_w4_linear(const void* x, int64_t ldx, int32_t x_type, const float* x_scale, int32_t x_group, const void* w,
                        const void* w_scale, const void* w_zero, int32_t group, const void* bias, void* out, int64_t ldo,
                        int64_t rows, int32_t n, int32_t k, hipStream_t stream);
@@ -519,7 +520,8 @@ fg_status fg_moe_few_bytes(int32_t tokens, int32_t k, int32_t F, int64_t* bytes)
  *   x, ldx, x_type, x_scale, x_group: activations [tokens][K], as fg_w4_linear
  *   w1, w2:  group 0: bf16 [n_local][2F][K] and [n_local][K][F], 16-byte aligned,
  *            scales and zeros NULL; group 32, 64, 128: 4-bit weights of the same
- *            rows in the layout of fg_w4_linear with their scales and zeros (or NULL)
+ *            rows in the layout of fg_w4_linear with their scales and zeros (or NULL);
+ *            what that says of infinities holds for x and the intermediate values
  *   topk:    int32 [tokens][k], distinct per token (negative: no pick);  weights: fp32 [tokens][k]
  *   tokens <= FG_MOE_FEW_TOKENS, k <= FG_MOE_FEW_TOPK, n_local <= FG_MOE_FEW_EXPERTS,
  *   K and F multiples of 32 and of group, up to FG_FEW_MAX_SIZE; the F gate rows of

@@ -297,3 +297,25 @@ def test_route_nan_comes_after_minus_infinity(experts, dtype, score):
     for renorm in (True, False):
         check_route(ops.moe_route(dev(logits), k, score=score, renorm=renorm), logits, k, score, renorm, 1.0)
     assert ops.moe_route(dev(logits), k)[0][0, 0] == 1
+
+
+# ---------------------------------------------------------- infinities and NaN
+@pytest.mark.parametrize("group", [0, 32, 128])
+def test_moe_an_infinity_in_x_stays_in_its_token(group):
+    """With bf16 rows of 4-bit weights it gives NaN: its product and its sum are both infinite."""
+    tokens = 20
+    g = R.gen(61)
+    x = torch.randn(tokens, 128, generator=g).bfloat16()
+    topk = torch.stack([torch.randperm(6, generator=g)[:2] for _ in range(tokens)]).int()
+    tw = torch.rand(tokens, 2, generator=g)
+    if group:
+        w1, w2 = (ops.W4Weight(*dev(*R.make_w4(g, (6,), a, b, group, True))) for a, b in ((256, 128), (128, 128)))
+    else:
+        w1, w2 = (torch.randn(6, a, b, generator=g).bfloat16().to(DEV) for a, b in ((256, 128), (128, 128)))
+    clean = ops.moe_few(dev(x), w1, w2, *dev(topk, tw))
+    x[4, 7], x[11, 100] = math.inf, math.nan
+    got = ops.moe_few(dev(x), w1, w2, *dev(topk, tw))
+    rest = torch.ones(tokens, dtype=torch.bool, device=DEV)
+    rest[4] = rest[11] = False
+    assert torch.equal(got[rest], clean[rest]) and got[11].isnan().all()
+    assert got[4].isnan().all() if group else not got[4].isfinite().any()
