@@ -319,3 +319,18 @@ def test_moe_an_infinity_in_x_stays_in_its_token(group):
     rest[4] = rest[11] = False
     assert torch.equal(got[rest], clean[rest]) and got[11].isnan().all()
     assert got[4].isnan().all() if group else not got[4].isfinite().any()
+
+
+# ---------------------------------------------------------------- largest sizes
+@pytest.mark.parametrize("group", [32, 64])
+def test_w4_most_rows(group):
+    """FG_W4_MAX_ROWS rows: up to 65536 workgroups in the grid's second dimension."""
+    rows, n, k = ops.W4_MAX_ROWS, 16, 64
+    g = R.gen(71)
+    q, s, z = R.make_w4(g, (), n, k, group, True)
+    x = torch.randn(rows, k, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV).bfloat16()
+    got = ops.w4_linear(x, ops.W4Weight(*dev(q, s, z)))
+    w, s = R.w4_values(q, s, z).to(DEV), s.to(DEV)
+    for part, rest in zip(x.split(1 << 17), got.split(1 << 17)):
+        want, tol = part.double() @ w.t(), R.w4_error(part.double(), s, group)
+        assert ((rest.double() - want).abs() <= tol + R.BF16_HALF * (want.abs() + tol) + 2.0 ** -133).all()
