@@ -463,7 +463,8 @@ enum { FG_SCORE_SOFTMAX = 0, FG_SCORE_SIGMOID = 1 };
  *   over each 128 columns (q_group 128), Q = 127 (FG_I8) or 448 (FG_E4M3):
  *   q_scale = a / Q, q = rne(y * (Q / a)), all codes 0 where a = 0.
  * A NaN or infinity in a row reaches its y and its q_scale (NaN); codes under
- * such a scale mean nothing.
+ * such a scale mean nothing. A row whose sum of h^2 leaves fp32 (|h| from 2^64 on)
+ * gives zeros, with eps 0 one whose sum is 0 in fp32 infinities or NaN.
  *   x, residual, sum, y: bf16 [rows][ld]; residual, sum and y may be NULL; sum
  *            and y may be x or residual themselves (same ld)
  *   gamma:   bf16 [n]
