@@ -98,7 +98,7 @@ __device__ __forceinline__ void moe_up_pass(const MoeArgs& a, int e, int f0, con
         g *= s;
         u *= s;
       }
-      const float h = g / (1.0f + __expf(-g)) * u * a.weights[p];
+      const float h = g / (1.0f + expf(-g)) * u * a.weights[p];
       const uint16_t hi = f_bf16(h);
       char* to = a.h + PackedRows::at(2 * (start + slot), G == 0 ? f0 + col : paired_place(f0 + col), a.plane);
       *(uint16_t*)to = hi;
