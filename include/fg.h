@@ -437,7 +437,7 @@ fg_status fg_gather_gemm_noalloc(const fg_config* cfg, int hip_device, const voi
  * and may be captured into a graph. Pointers are device pointers owned by the
  * caller; `ld*` is the distance of two rows in elements. Sums, means, softmax
  * statistics and scales are fp32; results are rounded once, to nearest even,
- * and do not depend on timing. Rows of 0: FG_OK, nothing is launched.
+ * and do not depend on timing (fg_moe_few holds its intermediate to 2^-16). Rows of 0: FG_OK, nothing is launched.
  * Errors of every entry: FG_EINVAL (shapes, types, NULLs, alignment), FG_EHIP
  * (the launch failed). */
 
@@ -503,7 +503,8 @@ fg_status fg_moe_route(const void* logits, int64_t ld, int32_t logits_type, int6
  *            inputs (rows may interleave with theirs); n any up to FG_FEW_MAX_SIZE
  *   rows:    any up to FG_W4_MAX_ROWS; made for 1 to 64 (more re-read the weights)
  * An infinity in bf16 x gives NaN in the whole row of out (the product and the sum of
- * x are both infinite); magnitudes from 2^113 on may, as sums of 143 |x| are formed. */
+ * x are both infinite); magnitudes from 2^113 on may, as sums of 143 |x| are formed.
+ * For bf16 x a group's sum is the difference of larger ones, about 5 of fp32's bits. */
 fg_status fg_w4_linear(const void* x, int64_t ldx, int32_t x_type, const float* x_scale, int32_t x_group, const void* w,
                        const void* w_scale, const void* w_zero, int32_t group, const void* bias, void* out, int64_t ldo,
                        int64_t rows, int32_t n, int32_t k, hipStream_t stream);
@@ -512,7 +513,8 @@ fg_status fg_w4_linear(const void* x, int64_t ldx, int32_t x_type, const float* 
 fg_status fg_moe_few_bytes(int32_t tokens, int32_t k, int32_t F, int64_t* bytes);
 
 /* A whole expert layer for few tokens: gate and up products, SiLU, down product
- * and the weighted sum over each token's picks, in two kernels:
+ * and the weighted sum over each token's picks, in two kernels. Between them
+ * weights[t][j] silu(..) * .. is held as two bf16 numbers, within 2^-16 of its value:
  *   y[t] = bf16( sum_j weights[t][j] * W2[e] (silu(W1[e][0:F] x[t]) * (W1[e][F:2F] x[t])) ),
  *   e = topk[t][j] - expert_base, over the picks with 0 <= e < n_local; a token
  *   with none gets zeros (other ranks' experts add their own terms).
