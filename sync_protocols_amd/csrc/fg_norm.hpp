@@ -76,7 +76,7 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* buf) {
   return v;
 }
 
-// Q / a would leave fp32 for a below 2^-118, and make zeros NaN: numbers that small
+// Q / a would leave fp32 for a below 2^-119, and make zeros NaN: numbers that small
 // are taken by 2^100 first, exactly.
 struct Inverse {
   float up, inv;

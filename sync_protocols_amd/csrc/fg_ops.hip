@@ -125,9 +125,13 @@ void launch_w4_tile(const W4Args& a, Launches& go) {
 // activations fewer times, but a workgroup takes a compute unit's time whether or
 // not the others have one: what counts is how many rounds of 256 workgroups there
 // are, each as long as a tile's cost (measured at k = 4096 and 8192, in units of the
-// smallest). Us for 8-bit rows, groups of 64, k = 8192, tiles (1,1) (1,2) (2,2) (4,2):
-//   12 x 4096: 7.6 9.0 - -;  12 x 8192: 10.9 10.0 - -;  28 x 8192: 16.1 16.1 12.6 -;
-//   60 x 4096: - - 12.7 17.0;  60 x 8192: - - 20.6 17.7.
+// smallest). Us for groups of 64, k = 8192, tiles (1,1) (1,2) (2,2) (4,2):
+//               int8 rows            e4m3 rows
+//   12 x 4096    7.7  9.7 12.0 16.0   8.3 11.0 13.6 17.7
+//   12 x 8192   11.9 10.4 12.2 16.3  12.5 11.8 14.4 18.4
+//   28 x 8192   18.4 16.2 12.2 16.3  19.8 18.2 14.5 18.4
+//   60 x 4096   17.3 14.9 11.9 16.4  18.8 17.2 13.9 18.6
+//   60 x 8192   32.7 27.6 20.3 17.4  35.0 31.4 23.1 19.6
 // The largest does not fit in the registers for groups of 32.
 // One row takes one of the first two.
 template <int G, int XK>
@@ -157,8 +161,11 @@ void launch_w4(const W4Args& a, Launches& go) {
 
 // One bf16 row goes through LDS: 1 x 2048 x 7168 5.6 us, straight from L2 6.3; 8192 x
 // 8192 10.3 and 11.1; 4096 x 14336 9.0 and 10.6; with short rows there is no difference
-// (64 x 512: 3.6). From two rows on every row would be copied by every workgroup (8 x
-// 4096 x 4096: 6.8 us, from L2 5.5). Rows of 32 KB leave room for the sums of the waves
+// (64 x 512: 3.6). More rows would all be copied by every workgroup. Through LDS and
+// from L2, at 4096 x 4096, 2048 x 7168 and 8192 x 4096: two rows 5.5 5.5, 6.1 6.4, 7.4
+// 7.3 (4096 x 14336 10.0 11.2); three 5.8 5.6, 6.3 6.5, 7.7 7.4; four 6.0 5.5, 6.8 6.6,
+// 7.9 7.4; eight 7.3 5.7, -, 9.0 7.3: two rows gain with long k alone, four lose. 8-bit
+// rows have no such form. Rows of 32 KB leave room for the sums of the waves
 // within 64 KB.
 constexpr int kLdsRow = 16384;
 
@@ -172,8 +179,11 @@ void launch_w4(const W4Args& a, int type, bool grouped, Launches& go) {
 
 // More than 16 rows an expert on average, were all picks here: two row tiles, so
 // that an expert's weights are still read once or twice; else one, whose fewer
-// registers leave room for more waves (64 tokens over 64 experts: 214 us when this
-// was chosen, with two row tiles 227 us).
+// registers leave room for more waves. Us a layer with one and two row tiles, bf16
+// weights, then 4-bit ones in groups of 128 with e4m3 rows and of 32 with int8 rows:
+// 64 tokens over 64 experts of 7168 x 2048, 8 rows each: 4-bit e4m3 396 and 509; 8
+// experts of that size, 32 rows each: 268 227, 126 131, int8 in groups of 64 129 128;
+// 33 rows: 317 273, 144 154, 180 174; 64 rows: 410 322, 195 186, 242 209.
 bool many_rows(const MoeArgs& a) { return a.tokens > 16 && a.tokens * a.k > 16 * a.n_local; }
 
 template <int G, int XK, int MT, int C, int P, int W>
@@ -183,11 +193,12 @@ void launch_moe_up_tile(const MoeArgs& a, Launches& go) {
   go(moe_up_kernel<G, XK, MT, C, P, W>, grid, dim3(64 * W), 0, a);
 }
 
-// 4-bit weights: two column tiles share the loads of x (64 tokens over 64 experts:
-// 206 us, with one 224 us), where there are eight workgroups and more for each place
-// on the compute units (15 tokens over 64 experts of 4480 x 1472: 46 us, with one 40);
-// for groups of 32 they do not fit in the registers. Four waves: with eight, a
-// workgroup's start and end are a larger share of it (12 tokens over 8 of 64 experts
+// 4-bit weights: two column tiles share the loads of x (a layer of 64 tokens over 64
+// experts of 7168 x 2048, with two and with one: bf16 rows 394 and 410 us, int8 375 and
+// 380, e4m3 390 and 392), where there are eight workgroups and more for each place on
+// the compute units (15 tokens over 64 experts of 4480 x 1472: int8 89.4 and 88.6, e4m3
+// 93.6 and 91.5); for groups of 32 they do not fit in the registers. Four waves: with
+// eight, a workgroup's start and end are a larger share of it (12 tokens over 8 of 64 experts
 // of 1792 x 1536: 7.6 us, with eight 8.9).
 template <int G, int XK>
 void launch_moe_up(const MoeArgs& a, Launches& go) {

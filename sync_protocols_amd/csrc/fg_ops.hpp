@@ -6,7 +6,7 @@
 // sum_k x[t][k] W[n][k]. For the few rows of a decoding step every weight is
 // read once and used T times, so the memory rate bounds it, and the arithmetic
 // only has to stay out of the way: a wave multiplies 16 weight rows with 16
-// token rows by v_mfma_f32_16x16x32_bf16 even when T = 1 (the matrix unit is
+// token rows by a 16x16 matrix instruction (bf16, f16 or int8) even when T = 1 (the matrix unit is
 // idle otherwise; products over 16 tokens cost it 16 clocks per 512 weights,
 // while HBM delivers that many 4-bit weights to one SIMD in about 110).
 // Tokens are the "A" operand and weights the "B" operand: lane l then holds, in
@@ -193,8 +193,8 @@ __device__ __forceinline__ u32x2 from_lane(int index, u32x2 v) { return u32x2{fr
 // Activations of a tile: base + row[m] is the row that this lane loads from (16 m +
 // l / 4) and its piece of it. Where the tile has no such row, which a decoding step's
 // few rows leave most lanes to, it is kNoRow and buffer loads return zeros without
-// asking for memory (MASKED: 64 tokens over 64 4-bit experts 213 -> 206 us in the
-// first product), or one that exists (16-bit weights, whose first product it made
+// asking for memory (MASKED; 64 tokens over 64 4-bit experts take 398 us a layer with
+// it, 399 without), or one that exists (16-bit weights, whose first product it made
 // slower, 79 -> 81 us). The base is uniform and the rest of an address 32 bits, as for
 // the weights. Scales per 128 k: those of the row start at scale + at[m].
 constexpr uint32_t kNoRow = 0xfffff000u;
