@@ -438,8 +438,8 @@ fg_status fg_gather_gemm_noalloc(const fg_config* cfg, int hip_device, const voi
  * caller; `ld*` is the distance of two rows in elements. Sums, means, softmax
  * statistics and scales are fp32; results are rounded once, to nearest even,
  * and do not depend on timing (fg_moe_few holds its intermediate to 2^-16). Rows of 0: FG_OK, nothing is launched.
- * Errors of every entry: FG_EINVAL (shapes, types, NULLs, alignment), FG_EHIP
- * (the launch failed). */
+ * Errors of every entry: FG_EINVAL (shapes, types, NULLs, alignment, outputs on
+ * memory that is still read), FG_EHIP (the launch failed). */
 
 enum {                     /* element types */
   FG_BF16 = 0,

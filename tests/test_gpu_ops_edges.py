@@ -334,3 +334,47 @@ def test_w4_most_rows(group):
     for part, rest in zip(x.split(1 << 17), got.split(1 << 17)):
         want, tol = part.double() @ w.t(), R.w4_error(part.double(), s, group)
         assert ((rest.double() - want).abs() <= tol + R.BF16_HALF * (want.abs() + tol) + 2.0 ** -133).all()
+
+
+# ---------------------------------------------------------------- e4m3 rows
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("x_group", [0, 128])
+def test_w4_e4m3_nan_stays_in_its_row(group, x_group):
+    g = R.gen(81)
+    w = ops.W4Weight(*dev(*R.make_w4(g, (), 48, 384, group, True)))
+    x, xs, _ = R.make_rows(g, 20, 384, "e4m3", x_group)
+    clean = ops.w4_linear(dev(x), w, x_scale=dev(xs))
+    x.view(torch.uint8)[3, 100], x.view(torch.uint8)[18, 383] = 0x7F, 0xFF
+    got = ops.w4_linear(dev(x), w, x_scale=dev(xs))
+    rest = torch.ones(20, dtype=torch.bool, device=DEV)
+    rest[3] = rest[18] = False
+    assert got[~rest].isnan().all() and torch.equal(got[rest], clean[rest])
+
+
+@pytest.mark.parametrize("tokens", [1, 20, 64])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("x_group", [0, 128])
+def test_moe_small_elements_beside_a_large_one(tokens, group, x_group):
+    """As the product's test of that name, through both products; the first one's tolerance is taken through the formula."""
+    K, F = 256, 128
+    g = R.gen(group + tokens)
+    x = torch.full((tokens, K), 2.0 ** -5)
+    q = torch.full((1, 2 * F, K), 1, dtype=torch.uint8)
+    for t in range(tokens):
+        x[t, 17 + t % 3], x[t, 140 + t % 3] = 448.0, -448.0
+    q[..., 17:20] = q[..., 140:143] = 15
+    w1 = q[..., 0::2] | q[..., 1::2] << 4, torch.full((1, 2 * F, K // group), 2.0 ** -6).bfloat16(), torch.full((1, 2 * F, K // group), 15, dtype=torch.uint8)
+    w1[1][:, :F] *= -1                                                # gates of about +1.7, up values of -1.7
+    w2 = R.make_w4(g, (1,), K, F, group, True)
+    x = x.to(torch.float8_e4m3fn)
+    xs = torch.ones((tokens, K // 128) if x_group else tokens)
+    got = ops.moe_few(dev(x), ops.W4Weight(*dev(*w1)), ops.W4Weight(*dev(*w2)), torch.zeros(tokens, 1, dtype=torch.int32, device=DEV),
+                      torch.ones(tokens, 1, device=DEV), x_scale=dev(xs))
+    a, b = R.w4_values(*(v[0] for v in w1)), R.w4_values(*(v[0] for v in w2))
+    gate, up = (x.double() @ a.t()).chunk(2, 1)
+    d = (2 * group + 8) * R.U * 15 * x.double().abs().sum(1, keepdim=True) * 2.0 ** -6
+    silu = gate * torch.sigmoid(gate)
+    h = silu * up
+    dh = 1.1 * d * (up.abs() + d) + silu.abs() * d + (2.0 ** -16 + (8 + 2 * gate.abs()) * R.U) * h.abs()
+    y, tol = h @ b.t(), dh @ b.abs().t() + R.w4_error(h, w2[1][0], group)
+    R.close(got, y, tol + R.BF16_HALF * (y.abs() + tol) + 2.0 ** -133, "y")
