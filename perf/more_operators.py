@@ -26,7 +26,7 @@ def listed():
         dict(name="append_64x8x128_e4m3", op="append", rows=64, pad=3, heads=8, dim=128, both=True, e4m3=True, page=16),
         # latent rows of a prompt: 8 shards of 1024 tokens
         dict(name="append_8192_latent", op="append", rows=8192, pad=0, heads=1, dim=576, both=False, e4m3=False, page=64),
-        # three short requests of a small model, one of them a padded row
+        # four short requests of a small model, one of them a padded row
         dict(name="paged_4x300_12of4x64", op="paged", batch=4, longest=300, ragged=True, heads=12, kv=4, dim=64, page=16, window=0, e4m3=False),
         # one long document: the work has to be split over the cache's length
         dict(name="paged_1x131072_64of8x128", op="paged", batch=1, longest=131072, ragged=False, heads=64, kv=8, dim=128, page=64, window=0, e4m3=False),
@@ -123,6 +123,12 @@ def _rows8(x):
     return (x.float() * torch.where(a > 0, 448.0 / a, 0.0)).to(E4M3), (a / 448.0).squeeze(-1)
 
 
+def _cache8(x):
+    """A cache as 8-bit rows; scales [pages, heads, page]."""
+    q, s = _rows8(x)
+    return q, s.transpose(1, 2).contiguous()
+
+
 def _normal(g, *shape, scale=1.0):
     return torch.randn(*shape, generator=g, device=DEV, dtype=BF16).mul_(scale)
 
@@ -166,7 +172,7 @@ def prepare(case, seed):
             # rows as a projection leaves them: slices of a wider row
             c[name] = _normal(g, r, h * d + 64)[:, :h * d].unflatten(1, (h, d))
             old = _normal(g, *shape)
-            c[name + "c"], c[name + "s"] = _rows8(old) if c["e4m3"] else (old, None)
+            c[name + "c"], c[name + "s"] = _cache8(old) if c["e4m3"] else (old, None)
     elif c["op"] == "paged":
         n, page, kv, d = c["batch"], c["page"], c["kv"], c["dim"]
         c["host"] = _shuffled(g, _lengths(c))
@@ -176,7 +182,7 @@ def prepare(case, seed):
             x = _normal(g, pages, page, kv, d)
             if name == "v":
                 x += _normal(g, kv, d)  # values of a head have a mean of their own
-            c[name + "c"], c[name + "s"] = _rows8(x) if c["e4m3"] else (x, None)
+            c[name + "c"], c[name + "s"] = _cache8(x) if c["e4m3"] else (x, None)
         c["q"] = _normal(g, n, c["heads"], d, scale=1.5)
         c["lens"] = torch.tensor(c["host"], dtype=torch.int32, device=DEV)
     else:
@@ -237,11 +243,12 @@ def _plain_pages(c):
 
 def _plain_append(c):
     out, n = {}, c["rows"] - c["pad"]
+    page, place = c["slots"][:n] // c["page"], c["slots"][:n] % c["page"]
     for name in ("k", "v") if c["both"] else ("k",):
         x, cache, s = c[name].float(), c[name + "c"], c[name + "s"]
         if c["e4m3"]:
             x, scale = _rows8(x)
-            s.flatten(0, 1)[c["slots"][:n]] = scale[:n]
+            s[page, :, place] = scale[:n]
             out[name + "s"] = s
             cache.view(torch.uint8).flatten(0, 1)[c["slots"][:n]] = x.view(torch.uint8)[:n]
         else:
@@ -266,7 +273,7 @@ def _plain_paged(c):
             continue
         first = max(0, n - c["window"]) if c["window"] else 0
         k, v = (t[_pages_of(c, b)].flatten(0, 1)[first:n].float() if s is None else
-                (t[_pages_of(c, b)].float() * s[_pages_of(c, b)].unsqueeze(-1)).flatten(0, 1)[first:n] for t, s in ((c["kc"], c["ks"]), (c["vc"], c["vs"])))
+                (t[_pages_of(c, b)].float() * s[_pages_of(c, b)].transpose(1, 2).unsqueeze(-1)).flatten(0, 1)[first:n] for t, s in ((c["kc"], c["ks"]), (c["vc"], c["vs"])))
         q = c["q"][b].float().unflatten(0, (kv, -1))
         p = _softmax(torch.matmul(q, k.permute(1, 2, 0)) / math.sqrt(d))
         out[b] = torch.matmul(p, v.transpose(0, 1)).flatten(0, 1)
@@ -364,7 +371,7 @@ def _exact_pages(c):
     """The step request by request, on the host."""
     page, lens, add = c["page"], c["lens"].tolist(), c["add"].tolist()
     table, ring, (head, tail) = c["table"].tolist(), c["ring"].tolist(), c["ends"].tolist()
-    asked, taken, given, left = 0, 0, 0, 0
+    asked, taken, given, wanted, left = 0, 0, 0, 0, 0
     out, starts, slots, positions = [], [0], [], []
     for b, (n, a) in enumerate(zip(lens, add)):
         if a < 0:
@@ -377,7 +384,9 @@ def _exact_pages(c):
             ok = wants <= c["width"]
             if ok:
                 asked += wants - has
-                ok = (wants == has or asked <= tail - head) and given + a <= c["tokens"]
+                ok = wants == has or asked <= tail - head
+                wanted += a if ok else 0
+                ok = ok and wanted <= c["tokens"]
             if ok:
                 for i in range(has, wants):
                     table[b][i] = ring[(head + taken) % len(ring)]
@@ -399,11 +408,6 @@ def _exact_pages(c):
             "positions": whole(positions, i32), "table": whole(table, i32), "ring": whole(ring, i32)}
 
 
-def _exact_cache(c, name):
-    t = c[name + "c"].double()
-    return t if c[name + "s"] is None else t * c[name + "s"].double()[..., None]
-
-
 def _weights64(scores):
     return torch.softmax(scores, -1)
 
@@ -420,7 +424,8 @@ def exact(case, seed):
             if c["e4m3"]:
                 s = x.abs().max(-1).values / 448
                 out[name + "s"] = c[name + "s"].double()
-                out[name + "s"].flatten(0, 1).index_copy_(0, c["slots"][:n], s)
+                for i, t in enumerate(c["slots"][:n].tolist()):
+                    out[name + "s"][t // c["page"], :, t % c["page"]] = s[i]
                 x = (x / torch.where(s > 0, s, 1)[..., None]).to(E4M3).double()
             out[name] = flat.index_copy(0, c["slots"][:n], x).reshape(c[name + "c"].shape)
         return out
@@ -432,7 +437,7 @@ def exact(case, seed):
                 continue
             page, place = c["table"][b].long()[at // c["page"]], at % c["page"]
             for j in range(c["kv"]):
-                k, v = (c[x + "c"][page, place, j].double() * (1 if c[x + "s"] is None else c[x + "s"][page, place, j].double()[:, None]) for x in "kv")
+                k, v = (c[x + "c"][page, place, j].double() * (1 if c[x + "s"] is None else c[x + "s"][page, j, place].double()[:, None]) for x in "kv")
                 for i in range(j * c["heads"] // c["kv"], (j + 1) * c["heads"] // c["kv"]):
                     out[b, i] = torch.mv(v.t(), _weights64(torch.mv(k, c["q"][b, i].double()) * c["dim"] ** -0.5))
         return out
