@@ -42,8 +42,9 @@ TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic.json")
 COPY_BYTES = 1 << 29          # plain device copy used to calibrate the HBM byte counters
 
 
-# the decoding operators' own sources: no part of the fused kernel
-OPERATOR_SOURCES = ("fg_moe.hpp", "fg_norm.hpp", "fg_ops.hip", "fg_ops.hpp", "fg_route.hpp", "fg_torch.cpp", "fg_w4.hpp")
+# the operators' own sources: no part of the fused kernel
+OPERATOR_SOURCES = ("fg_cache.hip", "fg_entry.hpp", "fg_latent.hip", "fg_latent.hpp", "fg_moe.hpp", "fg_norm.hpp", "fg_ops.hip", "fg_ops.hpp",
+                    "fg_paged.hpp", "fg_pages.hpp", "fg_prompt.hpp", "fg_route.hpp", "fg_split.hpp", "fg_torch.cpp", "fg_w4.hpp")
 
 
 def kernel_source_hash():

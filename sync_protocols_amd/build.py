@@ -6,16 +6,19 @@ import os
 import subprocess
 import sys
 import sysconfig
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIB_DIR, "libfg.so")
-SOURCES = [os.path.join(CSRC, "fg.hip"), os.path.join(CSRC, "fg_ops.hip")]
+SOURCES = [os.path.join(CSRC, n) for n in ("fg.hip", "fg_ops.hip", "fg_cache.hip", "fg_latent.hip")]
 HEADERS = [os.path.join(CSRC, n) for n in ("fg_sync.hpp", "fg_gemm.hpp", "fg_plan.hpp", "fg_kernels.hpp", "fg_combine.hpp",
-                                               "fg_ops.hpp", "fg_norm.hpp", "fg_route.hpp", "fg_w4.hpp", "fg_moe.hpp")] + [
-    os.path.join(ROOT, "include", "fg.h")]
+                                               "fg_entry.hpp", "fg_ops.hpp", "fg_norm.hpp", "fg_route.hpp", "fg_w4.hpp", "fg_moe.hpp",
+                                               "fg_split.hpp", "fg_pages.hpp", "fg_paged.hpp", "fg_latent.hpp", "fg_prompt.hpp")] + [
+    os.path.join(ROOT, "include", n) for n in ("fg.h", "fg_attention.h")]
 EXTENSION = os.path.join(LIB_DIR, "fg_torch.so")
 EXTENSION_SOURCE = os.path.join(CSRC, "fg_torch.cpp")
 
@@ -40,20 +43,28 @@ def _extension_command(out: str) -> list[str]:
             "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip", f"-L{rocm}/lib", "-lamdhip64", "-Wl,-rpath,$ORIGIN", "-o", out]
 
 
+def _run(what: str, cmd: list[str], verbose: bool) -> None:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError(f"the compiler failed building {what}")
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source into libfg.so, then fg_torch.so; always recompiles."""
+    """Compile every HIP source into libfg.so, the sources side by side, then fg_torch.so; always recompiles."""
     os.makedirs(LIB_DIR, exist_ok=True)
-    for what, out, command in (("libfg.so", LIB, lambda tmp: [HIPCC, *FLAGS, *SOURCES, "-o", tmp]),
-                               ("fg_torch.so", EXTENSION, _extension_command)):
-        tmp = out + ".tmp"
-        cmd = command(tmp)
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            sys.stderr.write(r.stdout + r.stderr)
-            raise RuntimeError(f"the compiler failed building {what}")
-        os.replace(tmp, out)
+    flags = [f for f in FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory(dir=LIB_DIR) as objects:
+        made = [os.path.join(objects, os.path.basename(s) + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(len(SOURCES)) as pool:
+            for done in [pool.submit(_run, os.path.basename(s), [HIPCC, *flags, "-c", s, "-o", o], verbose) for s, o in zip(SOURCES, made)]:
+                done.result()
+        _run("libfg.so", [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *made, "-o", LIB + ".tmp"], verbose)
+    os.replace(LIB + ".tmp", LIB)
+    _run("fg_torch.so", _extension_command(EXTENSION + ".tmp"), verbose)
+    os.replace(EXTENSION + ".tmp", EXTENSION)
     return LIB
 
 

@@ -1,0 +1,177 @@
+// Entry points of latent attention (include/fg_attention.h): the absorbed form of one
+// new token over a paged cache, and the expanded form of prompts.
+#include "fg_attention.h"
+#include "fg_entry.hpp"
+#include "fg_latent.hpp"
+#include "fg_prompt.hpp"
+
+using namespace fg::ops;
+
+namespace {
+
+constexpr int64_t kMax = 0x7fffffff;
+
+bool multiple(int64_t v, int64_t of) { return v >= 0 && v % of == 0; }
+Rows rows3(const void* p, int64_t element, int64_t n, int64_t ns, int64_t heads, int64_t hs, int64_t dim) {
+  return {p, n, element * ((heads - 1) * hs + dim), element * ns};
+}
+
+bool sizes_ok(int32_t heads, int32_t rank, int32_t rope, int32_t nope, float scale) {
+  return heads >= 1 && heads <= FG_ATTN_MAX_HEADS && (rank == 256 || rank == 512) && (rope == 32 || rope == 64) && (nope == 64 || nope == 128) &&
+         scale > 0.0f && scale < __builtin_inff();
+}
+
+// 16-head tiles of a workgroup, and the workgroups that this makes of all heads.
+int head_tiles(int32_t heads) { return heads <= 16 ? 1 : heads <= 32 ? 2 : heads <= 64 ? 4 : 8; }
+int64_t head_parts(int32_t heads) { return (heads + 16 * head_tiles(heads) - 1) / (16 * head_tiles(heads)); }
+// One workgroup a compute unit, which its LDS fills.
+int latent_target(int32_t heads) {
+  const int64_t t = kCUs / head_parts(heads);
+  return (int)(t < 1 ? 1 : t);
+}
+constexpr int kLatentLeast = 2;
+
+template <int R, int P, int HT, int S>
+void launch_latent(const LatentArgs& a, dim3 grid, Launches& go) {
+  go(latent_kernel<R, P, HT, S>, grid, dim3(64 * HT * S), LatentShape<R, P, HT, S>::LDS, a);
+}
+template <int R, int P>
+void launch_latent(const LatentArgs& a, dim3 grid, Launches& go) {
+  switch (head_tiles(a.heads)) {
+    case 1: launch_latent<R, P, 1, 4>(a, grid, go); break;
+    case 2: launch_latent<R, P, 2, 2>(a, grid, go); break;
+    case 4: launch_latent<R, P, 4, 1>(a, grid, go); break;
+    default: launch_latent<R, P, 8, 1>(a, grid, go);
+  }
+}
+
+template <int M, int P>
+void launch_prompt(const PromptArgs& a, int waves, Launches& go) {
+  const unsigned grid = 8 * (unsigned)(((int64_t)a.items * a.heads + 7) / 8);
+  const size_t lds = 2 * PromptShape<M, P>::STAGE;
+  if (waves == 8) go(prompt_kernel<M, P, 8>, dim3(grid), dim3(512), lds, a);
+  else go(prompt_kernel<M, P, 4>, dim3(grid), dim3(256), lds, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+fg_status fg_latent_attention_bytes(int32_t batch, int32_t heads, int32_t rank, int64_t* bytes) {
+  if (!bytes || batch < 0 || batch > FG_ATTN_MAX_BATCH || heads < 1 || heads > FG_ATTN_MAX_HEADS || (rank != 256 && rank != 512)) return FG_EINVAL;
+  const int64_t items = batch + latent_target(heads), rows = (int64_t)batch * heads;
+  // absorbed queries, weighted means (two numbers each); sums of the pieces; pieces of every request
+  *bytes = 6 * rows * rank + items * heads * (4 * rank + 8) + 8 * (int64_t)batch;
+  return FG_OK;
+}
+
+fg_status fg_latent_attention(const void* q, int64_t q_b, int64_t q_h, const void* w, const void* cache, int64_t page_stride,
+                              int64_t row_stride, const fg_pages_t* pages, int32_t heads, int32_t rank, int32_t rope, int32_t nope,
+                              float scale, void* workspace, int64_t workspace_bytes, void* out, int64_t out_b, int64_t out_h,
+                              float* lse, int64_t lse_b, hipStream_t stream) {
+  int64_t need = 0;
+  if (!pages || !sizes_ok(heads, rank, rope, nope, scale) || fg_latent_attention_bytes(pages->batch, heads, rank, &need) != FG_OK) return FG_EINVAL;
+  if (pages->n_pages < 1 || pages->page < 16 || pages->page % 16 || pages->width < 1 || pages->ldt < pages->width ||
+      (int64_t)pages->width * pages->page > kMax)
+    return FG_EINVAL;
+  const int64_t batch = pages->batch, parts = head_parts(heads);
+  if (batch * ((int64_t)pages->width * pages->page / kLatentTile + 2) > kMax) return FG_EINVAL;
+  if (batch == 0) return FG_OK;
+  if (!q || !w || !cache || !pages->table || !pages->lens || !out || !workspace || workspace_bytes < need) return FG_EINVAL;
+  if (!aligned(q, 16) || !aligned(w, 16) || !aligned(cache, 16) || !aligned(out, 2) || !aligned(lse, 4) || !aligned(workspace, 16) ||
+      !aligned(pages->table, 4) || !aligned(pages->lens, 4))
+    return FG_EINVAL;
+  if (!multiple(q_b, 8) || !multiple(q_h, 8) || !multiple(page_stride, 8) || !multiple(row_stride, 8) || 32 * row_stride > kMax || out_b < 0 || out_h < 0 ||
+      (lse && lse_b < heads && batch > 1))
+    return FG_EINVAL;
+  if (!distinct({{batch, out_b}, {heads, out_h}, {nope, 1}})) return FG_EINVAL;
+  const Rows ws = whole(workspace, need), o = rows3(out, 2, batch, out_b, heads, out_h, nope), qr = rows3(q, 2, batch, q_b, heads, q_h, nope + rope);
+  const Rows cr = whole(cache, 2 * ((int64_t)(pages->n_pages - 1) * page_stride + (int64_t)(pages->page - 1) * row_stride + rank + rope));
+  const Rows wr = whole(w, 4 * (int64_t)heads * nope * rank), le = whole(pages->lens, 4 * batch);
+  const Rows t{pages->table, batch, 4 * (int64_t)pages->width, 4 * pages->ldt}, ls{lse, batch, 4 * (int64_t)heads, 4 * lse_b};
+  if (overlaps(o, qr, wr, cr, t, le, ws, ls) || overlaps(ls, qr, wr, cr, t, le, ws) || overlaps(ws, qr, wr, cr, t, le)) return FG_EINVAL;
+  const int64_t items = batch + latent_target(heads), rows = batch * heads;
+  char* at = (char*)workspace;
+  char* const absorbed = at;
+  at += 2 * rows * rank;
+  char* const mean = at;
+  at += 4 * rows * rank;
+  LatentArgs a{};
+  a.part = (float*)at;
+  at += 4 * items * heads * rank;
+  a.ml = (float*)at;
+  at += 8 * items * heads;
+  a.split = SplitArgs{pages->lens, pages->table, pages->ldt, pages->batch, pages->width, pages->n_pages, pages->page, 0, latent_target(heads), kLatentLeast,
+                      (int32_t*)at};
+  a.a = absorbed;
+  a.q = (const char*)q + 2 * nope;
+  a.cache = (const char*)cache;
+  a.out = (uint16_t*)mean; a.lse = lse;
+  a.q_b = 2 * q_b; a.q_h = 2 * q_h; a.c_page = 2 * page_stride; a.c_tok = (int32_t)(2 * row_stride); a.lse_b = lse_b;
+  a.heads = heads; a.c = scale * kLog2E;
+  Launches go{stream};
+  const unsigned tiles = (unsigned)((batch + 15) / 16);
+  const HeadsArgs absorb{(const char*)q, (const char*)w, (uint16_t*)absorbed, 2 * q_b, 2 * q_h, 4 * (int64_t)nope * rank, (int64_t)heads * rank, rank,
+                         (int32_t)batch, heads, nope, rank};
+  go(heads_product_kernel<true>, dim3((unsigned)rank / 128, (unsigned)heads, tiles), dim3(64), 0, absorb);
+  const dim3 grid((unsigned)items, (unsigned)parts);
+  if (rank == 512) rope == 64 ? launch_latent<512, 64>(a, grid, go) : launch_latent<512, 32>(a, grid, go);
+  else rope == 64 ? launch_latent<256, 64>(a, grid, go) : launch_latent<256, 32>(a, grid, go);
+  if ((int64_t)pages->width * pages->page > (int64_t)kLatentLeast * kLatentTile) {
+    const JoinArgs j{a.split.pieces, a.part, a.ml, a.out, lse, 2 * (int64_t)heads * rank, 2 * rank, lse_b, heads};
+    const dim3 jg((unsigned)heads, (unsigned)batch), jb(64 * kJoinWaves);
+    rank == 512 ? go(join_kernel<512, true>, jg, jb, 0, j) : go(join_kernel<256, true>, jg, jb, 0, j);
+  }
+  const HeadsArgs up{mean, (const char*)w + 2 * (int64_t)nope * rank, (uint16_t*)out, 4 * (int64_t)heads * rank, 4 * rank, 4 * (int64_t)nope * rank,
+                     out_b, out_h, (int32_t)batch, heads, rank, nope};
+  go(heads_product_kernel<false>, dim3((unsigned)nope / 16, (unsigned)heads, tiles), dim3(64), 0, up);
+  return go.status();
+}
+
+fg_status fg_latent_prompt_bytes(int64_t k_rows, int32_t heads, int32_t nope, int64_t* bytes) {
+  if (!bytes || k_rows < 0 || k_rows > kMax || heads < 1 || heads > FG_ATTN_MAX_HEADS || (nope != 64 && nope != 128)) return FG_EINVAL;
+  *bytes = 4 * k_rows * heads * nope;
+  return FG_OK;
+}
+
+fg_status fg_latent_prompt(const void* q, int64_t q_t, int64_t q_h, const int32_t* q_starts, int64_t q_rows, const void* latent,
+                           int64_t ld, const int32_t* k_starts, int64_t k_rows, int32_t batch, const void* w, int32_t heads,
+                           int32_t rank, int32_t rope, int32_t nope, float scale, void* workspace, int64_t workspace_bytes,
+                           void* out, int64_t out_t, int64_t out_h, float* lse, int64_t lse_t, hipStream_t stream) {
+  int64_t need = 0;
+  if (!sizes_ok(heads, rank, rope, nope, scale) || fg_latent_prompt_bytes(k_rows, heads, nope, &need) != FG_OK || q_rows < 0 || q_rows > kMax || batch < 0 ||
+      batch > FG_ATTN_MAX_BATCH)
+    return FG_EINVAL;
+  if (batch == 0 || q_rows == 0) return FG_OK;
+  if (!q || !q_starts || !k_starts || !w || !out || (k_rows && (!latent || !workspace)) || workspace_bytes < need) return FG_EINVAL;
+  if (!aligned(q, 16) || !aligned(latent, 16) || !aligned(w, 16) || !aligned(q_starts, 4) || !aligned(k_starts, 4) || !aligned(out, 8) || !aligned(lse, 4) ||
+      !aligned(workspace, 16))
+    return FG_EINVAL;
+  if (!multiple(q_t, 8) || !multiple(q_h, 8) || !multiple(ld, 8) || (k_rows > 1 && ld < rank + rope) || !multiple(out_t, 4) || !multiple(out_h, 4) ||
+      (lse && lse_t < heads && q_rows > 1))
+    return FG_EINVAL;
+  if (!distinct({{q_rows, out_t}, {heads, out_h}, {nope, 1}})) return FG_EINVAL;
+  const Rows ws = whole(k_rows ? workspace : nullptr, need), o = rows3(out, 2, q_rows, out_t, heads, out_h, nope), qr = rows3(q, 2, q_rows, q_t, heads, q_h, nope + rope);
+  const Rows lat = {k_rows ? latent : nullptr, k_rows, 2 * (int64_t)(rank + rope), 2 * ld}, wr = whole(w, 4 * (int64_t)heads * nope * rank);
+  const Rows qs = whole(q_starts, 4 * ((int64_t)batch + 1)), ks = whole(k_starts, 4 * ((int64_t)batch + 1)), ls{lse, q_rows, 4 * (int64_t)heads, 4 * lse_t};
+  if (overlaps(o, qr, lat, wr, qs, ks, ws, ls) || overlaps(ls, qr, lat, wr, qs, ks, ws) || overlaps(ws, qr, lat, wr, qs, ks)) return FG_EINVAL;
+  // tiles of 256 queries where they fill the GPU twice, else of 128
+  const int waves = (q_rows + 255) / 256 * heads >= 2 * kCUs ? 8 : 4;
+  const int64_t items = (q_rows + 32 * waves - 1) / (32 * waves) + batch, n = (int64_t)heads * 2 * nope;
+  if (items * heads > kMax - 8 || (k_rows + kExpandTile - 1) / kExpandTile > 65535 || n > kMax) return FG_EINVAL;
+  Launches go{stream};
+  if (k_rows) {
+    const ExpandArgs e{(const char*)latent, (const char*)w, (uint16_t*)workspace, 2 * ld, k_rows, (int32_t)n, rank};
+    go(expand_kernel, dim3((unsigned)(n / kExpandTile), (unsigned)((k_rows + kExpandTile - 1) / kExpandTile)), dim3(256), 4 * kExpandTile * 128, e);
+  }
+  PromptArgs a{};
+  a.q = (const char*)q; a.kv = (const char*)workspace; a.lat = (const char*)latent; a.out = (uint16_t*)out; a.lse = lse;
+  a.q_starts = q_starts; a.k_starts = k_starts;
+  a.q_t = 2 * q_t; a.q_h = 2 * q_h; a.ld = 2 * ld; a.out_t = out_t; a.out_h = out_h; a.lse_t = lse_t;
+  a.q_rows = q_rows; a.k_rows = k_rows; a.batch = batch; a.heads = heads; a.r = rank; a.items = (int32_t)items; a.c = scale * kLog2E;
+  if (nope == 128) rope == 64 ? launch_prompt<128, 64>(a, waves, go) : launch_prompt<128, 32>(a, waves, go);
+  else rope == 64 ? launch_prompt<64, 64>(a, waves, go) : launch_prompt<64, 32>(a, waves, go);
+  return go.status();
+}
+
+}  // extern "C"

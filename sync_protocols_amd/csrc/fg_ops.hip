@@ -1,6 +1,7 @@
 // Entry points of the decoding operators (include/fg.h): argument checks and
 // launches. Nothing is allocated or kept; every call is one or two kernels on
 // the caller's stream, so all of them can be captured into a graph.
+#include "fg_entry.hpp"
 #include "fg_moe.hpp"
 #include "fg_norm.hpp"
 #include "fg_route.hpp"
@@ -9,51 +10,6 @@
 using namespace fg::ops;
 
 namespace {
-
-// Launches on one stream, with their own errors only (an error that an earlier call
-// of the program left behind is not theirs); none after one that failed.
-struct Launches {
-  hipStream_t stream;
-  hipError_t error = hipSuccess;
-  template <class Args>
-  void operator()(void (*kernel)(Args), dim3 grid, dim3 block, size_t lds, Args a) {
-    void* args[1] = {&a};
-    if (error == hipSuccess) error = hipLaunchKernel((const void*)kernel, grid, block, args, lds, stream);
-  }
-  fg_status status() const { return error == hipSuccess ? FG_OK : FG_EHIP; }
-};
-
-constexpr int kCUs = 256;          // compute units of the part
-
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
-// Rows of `bytes` bytes, `pitch` apart (one row: any pitch).
-struct Rows {
-  const void* p;
-  int64_t rows, bytes, pitch;
-  uintptr_t begin() const { return (uintptr_t)p; }
-  uintptr_t end() const { return begin() + (rows - 1) * pitch + bytes; }
-};
-Rows whole(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
-
-// Do they share a byte? Rows that interleave, as columns of one buffer do, need not.
-bool overlap(const Rows& a, const Rows& b) {
-  if (!a.p || !b.p || a.end() <= b.begin() || b.end() <= a.begin()) return false;
-  if (a.rows > b.rows) return overlap(b, a);
-  if (a.pitch == b.pitch && a.rows > 1) {
-    const int64_t d = (int64_t)(b.begin() - a.begin()) % a.pitch, shift = d < 0 ? d + a.pitch : d;
-    if (shift >= a.bytes && shift + b.bytes <= a.pitch) return false;
-  }
-  for (int64_t i = 0; i < a.rows; ++i) {         // the last row of b that starts before the end of a's
-    const uintptr_t from = a.begin() + i * a.pitch, to = from + a.bytes;
-    if (to <= b.begin()) continue;
-    const int64_t j = b.rows == 1 ? 0 : (int64_t)((to - 1 - b.begin()) / b.pitch);
-    if (b.begin() + (j < b.rows ? j : b.rows - 1) * b.pitch + b.bytes > from) return true;
-  }
-  return false;
-}
-template <class... Others>
-bool overlaps(const Rows& a, const Others&... others) { return (overlap(a, others) || ...); }
 
 int pow2_at_least(int v) {
   int p = 1;
@@ -73,13 +29,6 @@ bool rows_ok(const void* x, int64_t ldx, int32_t type, const float* scale, int32
 
 bool w4_ok(const void* w, const void* s, int32_t group, int32_t k) {
   return w && s && (group == 32 || group == 64 || group == 128) && k % group == 0 && aligned(w, 16) && aligned(s, 2);
-}
-
-// A grid of n workgroups for any n below 2^31: more than 2^20 in two dimensions
-// (a dimension holds fewer than 2^32 threads).
-dim3 wide_grid(int64_t n) {
-  const int64_t x = 1 << 20;
-  return n <= x ? dim3((unsigned)n) : dim3((unsigned)x, (unsigned)((n + x - 1) / x));
 }
 
 template <int W, int V>

@@ -1,0 +1,341 @@
+// Latent attention, expanded form, of ragged prompts: keys [W_k c | r] and values
+// W_v c of every head are formed once (expand_kernel), then
+//   out[i][h] = sum_j w_ij v_j,  w = softmax over j <= nk - nq + i of scale (q_nope . k_j + q_rope . r_j)
+// (prompt_kernel), 2 H (2 M + P) flops a pair: matrix instructions bound it.
+//
+// prompt_kernel: a workgroup has W waves of 32 queries of one head; tiles of 64
+// keys and values go through LDS by direct loads, two in turn. Both products are
+// 32x32x16 instructions with the query in the lane:
+//   S^T[key][query] = K Q^T;   O^T[dim][query] += V^T P^T
+// Lane l holds of S^T the keys 8 a + 4 (l / 32) + 0..3, which two at a time are a legal
+// order of the 16 keys of a second product, whose V^T comes by transposing reads of 4 keys; so
+// a query's weights, maximum and sum stay in its lane.
+// The rope part of the keys is read from the latent rows as it is; heads share it.
+// Keys that a query does not see have weight zero, but zero times a NaN or an infinity of their
+// values is NaN: in tiles where some are hidden, keys with such values are multiplied one by one, and only into
+// the queries that see them.
+#pragma once
+
+#include "fg_latent.hpp"
+
+namespace fg {
+namespace ops {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// ------------------------------------------------------------------- expand
+// kv[t][n] = bf16( sum_r lat[t][r] w[n][r] ), n over heads and their 2 M rows: 128 x 128 tiles, four waves of 64 x 64, 64 r at a time
+// through LDS by direct loads, two stages in turn.
+struct ExpandArgs {
+  const char* lat;
+  const char* w;
+  uint16_t* kv;
+  int64_t ld;                        // bytes of a latent row
+  int64_t rows;
+  int32_t n, r;                      // n = heads * 2 M, any multiple of 128
+};
+
+constexpr int kExpandTile = 128;
+__global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = kExpandTile * blockIdx.x, wm = wave >> 1, wn = wave & 1;
+  const int64_t t0 = (int64_t)kExpandTile * blockIdx.y;
+  constexpr int STAGE = kExpandTile * 128;       // bytes of 64 r of one operand
+  // 8 rows of 128 bytes a load; chunks permuted by the row's pair
+  auto load = [&](int k, char* to) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 8 * (4 * wave + i) + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
+      const int64_t t = t0 + row < a.rows ? t0 + row : a.rows - 1;
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(a.lat + t * a.ld + 2 * k + 16 * c),
+                                       (__attribute__((address_space(3))) void*)(to + 1024 * (4 * wave + i)), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(a.w + 2 * ((int64_t)(n0 + row) * a.r + k) + 16 * c),
+                                       (__attribute__((address_space(3))) void*)(to + STAGE + 1024 * (4 * wave + i)), 16, 0, 0);
+    }
+  };
+  f32x16 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+  const int steps = a.r / 64;
+  load(0, lds);
+  for (int s = 0; s < steps; ++s) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (s + 1 < steps) load(64 * (s + 1), lds + (s + 1) % 2 * 2 * STAGE);
+    const char* x = lds + s % 2 * 2 * STAGE;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      bf16x8 u[2], v[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int ru = 64 * wn + 32 * i + l32, rv = 64 * wm + 32 * i + l32;
+        u[i] = *(const bf16x8*)(x + STAGE + ru * 128 + 16 * ((2 * k + half) ^ ((ru >> 1) & 7)));
+        v[i] = *(const bf16x8*)(x + rv * 128 + 16 * ((2 * k + half) ^ ((rv >> 1) & 7)));
+      }
+      // rows of the result are columns n: a lane has 4 consecutive ones of a token
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u[j], v[i], acc[i][j], 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t t = t0 + 64 * wm + 32 * i + l32;
+    if (t >= a.rows) continue;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const int n = n0 + 64 * wn + 32 * j + 2 * e + 4 * half;
+        *(u32x2*)(a.kv + t * a.n + n) = u32x2{f2_bf16(acc[i][j][e], acc[i][j][e + 1]), f2_bf16(acc[i][j][e + 2], acc[i][j][e + 3])};
+      }
+  }
+}
+
+// ------------------------------------------------------------------- prompt
+struct PromptArgs {
+  const char* q;
+  const char* kv;                    // bf16 [keys][heads][2 M]
+  const char* lat;                   // latent rows, for their rope part
+  uint16_t* out;
+  float* lse;
+  const int32_t* q_starts;
+  const int32_t* k_starts;
+  int64_t q_t, q_h, ld;              // bytes
+  int64_t out_t, out_h, lse_t;       // elements
+  int64_t q_rows, k_rows;
+  int32_t batch, heads, r, items;    // items: workgroups a head
+  float c;
+};
+
+template <int M, int P>
+struct PromptShape {
+  static constexpr int KC = (M + P) / 8, VC = M / 8;         // chunks of 16 bytes in a row
+  static constexpr int KB = 64 * 16 * KC, VB = 64 * 16 * VC;
+  static constexpr int STAGE = KB + VB;
+  // 16 rows of one chunk on different banks
+  static __device__ __forceinline__ int key_place(int c, int t) {
+    if constexpr (KC % 16 == 0) return c ^ (t & 15);
+    else if constexpr (KC % 16 == 8) return c ^ ((t >> 1) & 7);
+    else return c ^ ((t >> 2) & 3);
+  }
+  // 32 dims of 4 rows on different banks
+  static __device__ __forceinline__ int value_place(int c, int t) {
+    if constexpr (VC == 16) return c ^ ((t & 3) << 2);
+    else return c ^ ((t & 2) << 1);
+  }
+};
+
+// Request and tile of Q queries of item `item` (in request order); false if there are fewer.
+template <int T, int Q>
+__device__ __forceinline__ bool find_queries(const PromptArgs& a, int item, SplitShared& sh, int& b, int& tile) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int per = (a.batch + T - 1) / T, from = min(tid * per, a.batch), to = min(from + per, a.batch);
+  auto tiles = [&](int i) { return max(0, a.q_starts[i + 1] - a.q_starts[i] + Q - 1) / Q; };
+  int count = 0;
+  for (int i = from; i < to; ++i) count += tiles(i);
+  int upto = lanes_before_and_own(count);
+  if (lane == 63) sh.sum[wave] = upto;
+  if (tid == 0) sh.found[0] = -1;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) upto += sh.sum[w];
+  if (item < upto && item >= upto - count) {
+    int at = upto - count;
+    for (int i = from; i < to; ++i) {
+      const int n = tiles(i);
+      if (item < at + n) {
+        sh.found[0] = i;
+        sh.found[1] = item - at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  b = __builtin_amdgcn_readfirstlane(sh.found[0]);
+  tile = __builtin_amdgcn_readfirstlane(sh.found[1]);
+  return b >= 0;
+}
+
+template <int M, int P, int W>
+__global__ __launch_bounds__(64 * W, 2) void prompt_kernel(PromptArgs a) {
+  typedef PromptShape<M, P> Sh;
+  constexpr int KC = Sh::KC, VC = Sh::VC, KS = (M + P) / 16, DT = M / 32;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  __shared__ SplitShared sh;
+  const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5, m = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // workgroups go round the 8 dies; a die takes neighbouring items, which share a head's keys, in its L2
+  const int total = gridDim.x, share = (total + 7) / 8, id = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
+  if (id >= a.items * a.heads) return;
+  const int h = id / a.items;
+  int b, tile;
+  // last tiles first: they see the most keys
+  if (!find_queries<64 * W, 32 * W>(a, a.items - 1 - (id - h * a.items), sh, b, tile)) return;
+  const int q_first = max(a.q_starts[b], 0), nq = (int)min((int64_t)a.q_starts[b + 1], a.q_rows) - q_first;
+  const int k_first = max(a.k_starts[b], 0), nk = (int)min((int64_t)a.k_starts[b + 1], a.k_rows) - k_first;
+  if (32 * W * tile >= nq) return;     // starts beyond the rows
+  const int i0 = 32 * W * tile, i = i0 + 32 * wave + l32;          // this lane's query
+  const int last = i < nq ? nk - nq + i : -1;                      // the last key that it sees
+  const int wave_first = nk - nq + i0 + 32 * wave;                 // what the wave's first query sees
+  const int wave_last = min(wave_first + 31, nk - 1);
+  const int keys = min(nk, nk - nq + min(i0 + 32 * W, nq)), tiles = keys <= 0 ? 0 : (keys + 63) / 64;
+
+  bf16x8 q[KS];
+  const char* qrow = a.q + (int64_t)(q_first + min(i, nq - 1)) * a.q_t + h * a.q_h;
+#pragma unroll
+  for (int s = 0; s < KS; ++s) q[s] = *(const bf16x8*)(qrow + 2 * (16 * s + 8 * half));
+  f32x16 o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
+  float top = kNone, l = 0.0f;
+
+  const int64_t kv_row = (int64_t)a.heads * 4 * M;
+  const char* kv = a.kv + (int64_t)k_first * kv_row + h * (4 * M);
+  const char* rope = a.lat + (int64_t)k_first * a.ld + 2 * a.r;
+  auto load = [&](int t) {
+    char* to = lds + (t & 1) * Sh::STAGE;
+#pragma unroll
+    for (int n = 0; n < (KC + W - 1) / W; ++n) {
+      if (KC % W != 0 && n * W + wave >= KC) break;
+      const int slot = (n * W + wave) * 64 + lane, row = slot / KC, c = Sh::key_place(slot - row * KC, row);
+      const int64_t key = min(64 * t + row, nk - 1);
+      const char* from = c < M / 8 ? kv + key * kv_row + 16 * c : rope + key * a.ld + 16 * (c - M / 8);
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                       (__attribute__((address_space(3))) void*)(to + (n * W + wave) * 1024), 16, 0, 0);
+    }
+#pragma unroll
+    for (int n = 0; n < VC / W; ++n) {
+      const int slot = (n * W + wave) * 64 + lane, row = slot / VC, c = Sh::value_place(slot % VC, row);
+      const int64_t key = min(64 * t + row, nk - 1);
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(kv + key * kv_row + 2 * M + 16 * c),
+                                       (__attribute__((address_space(3))) void*)(to + Sh::KB + (n * W + wave) * 1024), 16, 0, 0);
+    }
+  };
+  if (tiles > 0) load(0);
+  for (int t = 0; t < tiles; ++t) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();                   // tile t is there, and all waves are done with tile t - 1
+    if (t + 1 < tiles) load(t + 1);
+    if (64 * t > wave_last) continue;  // no query of this wave sees any of it
+    const char* kt = lds + (t & 1) * Sh::STAGE;
+    const char* vt = kt + Sh::KB;
+    f32x16 s[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[u][e] = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const bf16x8 key = *(const bf16x8*)(kt + (32 * u + l32) * (16 * KC) + 16 * Sh::key_place(2 * ks + half, 32 * u + l32));
+        s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[ks], s[u], 0, 0, 0);
+      }
+    const bool hidden = 64 * t + 63 > wave_first || 64 * t + 64 > nk;      // some query of the wave does not see all of it
+    float high = kNone;
+    if (hidden) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int key = 64 * t + 32 * u + 8 * (e / 4) + 4 * half + e % 4;
+          s[u][e] = key <= last ? s[u][e] : kNone;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) high = fmaxf(high, s[u][e]);
+    high *= a.c;
+    if (__any(high > top + kSlack)) {
+      const uint32_t w = __float_as_uint(high);
+      const auto x = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+      const float up = fmaxf(top, fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])));
+      const float f = top == kNone ? 0.0f : exp2f(top - up);
+      top = up;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] *= f;
+    }
+    const float at = top == kNone ? 0.0f : top;
+    bf16x8 w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      u32x4 pk;
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k / 2][8 * (k & 1) + e], a.c, -at));
+        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k / 2][8 * (k & 1) + e + 1], a.c, -at));
+        l += x + y;
+        pk[e / 2] = f2_bf16(x, y);
+      }
+      w[k] = __builtin_bit_cast(bf16x8, pk);
+    }
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        // keys 16 k + 4 half + 0..3 and 8 more, dims 32 d + lane % 32
+        const int row = 16 * k + 4 * half + (m >> 2), c = 4 * d + 2 * ((lane >> 4) & 1) + ((m & 3) >> 1);
+        const char* from = vt + row * (16 * VC) + 16 * Sh::value_place(c, row) + 8 * (m & 1);
+        const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)from));
+        const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(from + 8 * (16 * VC))));
+        u32x4 v = {x[0], x[1], y[0], y[1]};
+        if (hidden) {
+          bool odd = false;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) odd = odd || (v[j] & 0x7f80u) == 0x7f80u || (v[j] & 0x7f800000u) == 0x7f800000u;
+          if (__any(odd)) {
+            // one key at a time, kept by the queries that see it
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j)
+#pragma unroll 1
+              for (int g = 0; g < 2; ++g) {
+                u32x4 one, pw;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t mask = half == g && e == j / 2 ? (j & 1 ? 0xffff0000u : 0xffffu) : 0u;
+                  one[e] = v[e] & mask;
+                  pw[e] = __builtin_bit_cast(u32x4, w[k])[e] & mask;
+                }
+                const f32x16 sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, one), __builtin_bit_cast(bf16x8, pw), o[d], 0, 0, 0);
+                const int key = 64 * t + 16 * k + 4 * g + j % 4 + 8 * (j / 4);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[d][e] = key <= last ? sum[e] : o[d][e];
+              }
+            continue;
+          }
+        }
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v), w[k], o[d], 0, 0, 0);
+      }
+  }
+  const uint32_t lw = __float_as_uint(l);
+  const auto x = __builtin_amdgcn_permlane32_swap(lw, lw, false, false);
+  const float all = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+  if (i >= nq) return;
+  const float inv = all == 0.0f ? 0.0f : 1.0f / all;
+  uint16_t* to = a.out + (int64_t)(q_first + i) * a.out_t + h * a.out_h;
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; e += 4)
+      *(u32x2*)(to + 32 * d + 2 * e + 4 * half) =
+          u32x2{f2_bf16(o[d][e] * inv, o[d][e + 1] * inv), f2_bf16(o[d][e + 2] * inv, o[d][e + 3] * inv)};
+  if (a.lse && half == 0)
+    a.lse[(int64_t)(q_first + i) * a.lse_t + h] = all == 0.0f ? kNone : ((top == kNone ? 0.0f : top) + log2f(all)) / kLog2E;
+}
+
+}  // namespace ops
+}  // namespace fg

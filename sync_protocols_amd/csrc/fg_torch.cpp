@@ -15,7 +15,9 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include "fg.h"
+#include <cmath>
+
+#include "fg_attention.h"
 
 namespace {
 
@@ -102,7 +104,7 @@ void* ptr(const Tensor* t) { return t ? t->data_ptr() : nullptr; }
 // allocator is told that the caller's tensors are used on the other stream, and that
 // new outputs, which the caller goes on with, may be used on the current one.
 struct Call {
-  const Tensor* used[16];
+  const Tensor* used[20];
   int n = 0;
   c10::Device device;
   std::optional<c10::Stream> other;
@@ -155,12 +157,22 @@ struct Call {
     if (!is_type(*given, type) || !is_shape(*given, shape) || given->device() != device) refuse(what);
     no_gradient(*given);
   }
+  // A tensor of the caller's that the launch writes into; all are checked before the first is marked.
+  void check_write(const Tensor* t) const {
+    if (!t) return;
+    if (t->device() != device) refuse("tensors are on different devices");
+    no_gradient(*t);
+  }
+  void write(const Tensor* t) {
+    if (!t) return;
+    use(t);
+    if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+  }
   // The output `given`, which has been checked, or a new one. Autograd, which may have
   // saved a given one, is told that it is written.
   Tensor out(const Tensor* given, at::IntArrayRef shape, ScalarType type) {
     if (given) {
-      use(given);
-      if (!given->is_inference()) given->unsafeGetTensorImpl()->bump_version();
+      write(given);
       return *given;
     }
     const Tensor t = memory(shape, type);
@@ -435,6 +447,298 @@ PyObject* moe_few(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
+// ------------------------------------------------------------ paged caches
+// lens, add, table, ring, ends, page, tokens, lens_out, ends_out, starts, slots, positions, stream
+//   -> (lens_out, ends_out, starts, slots, positions)
+PyObject* page_step(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (!counted(n_args, 13)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Tensor &lens = tensor(a[0]), &add = tensor(a[1]), &table = tensor(a[2]), &ring = tensor(a[3]), &ends = tensor(a[4]);
+    const Tensor *lens_in = maybe(a[7]), *ends_in = maybe(a[8]), *starts_in = maybe(a[9]), *slots_in = maybe(a[10]), *pos_in = maybe(a[11]);
+    const int32_t page = int32_of(a[5], "page must be an int32"), tokens = int32_of(a[6], "tokens must be an int32");
+    if (page < 1 || tokens < 0) refuse("page must be positive, tokens not negative");
+    ROWS2D(table, "table");
+    const int64_t batch = table.size(0), width = table.size(1);
+    if (!is_type(lens, at::kInt) || !vector_of(lens, batch) || !is_type(add, at::kInt) || !vector_of(add, batch) || !is_type(table, at::kInt))
+      refuse("lens and add must be int32 [batch], table int32 [batch, pages]");
+    if (!is_type(ring, at::kInt) || ring.dim() != 1 || !ring.is_contiguous() || ring.size(0) < 1) refuse("ring must be contiguous int32 [n_pages]");
+    if (!is_type(ends, at::kLong) || !vector_of(ends, 2)) refuse("ends must be int64 [2]");
+    fits_int32(batch, "too many requests");
+    fits_int32(width, "the table is too wide");
+    fits_int32(ring.size(0), "too many pages");
+    Call c(table);
+    const int64_t nb[1] = {batch}, two[1] = {2}, ns[1] = {batch + 1}, nt[1] = {tokens};
+    c.check(lens_in, nb, at::kInt, "lens_out must be int32 [batch]");
+    c.check(ends_in, two, at::kLong, "ends_out must be int64 [2]");
+    c.check(starts_in, ns, at::kInt, "starts must be int32 [batch + 1]");
+    c.check(slots_in, nt, at::kLong, "slots must be int64 [tokens]");
+    c.check(pos_in, nt, at::kInt, "positions must be int32 [tokens]");
+    for (const Tensor* t : {lens_in, ends_in, starts_in, slots_in, pos_in})
+      if (t && !t->is_contiguous()) refuse("given outputs must be contiguous");
+    c.check_write(&table); c.check_write(&ring);
+    c.use(&lens); c.use(&add); c.use(&ends);
+    c.on(a[12]);
+    c.write(&table);
+    c.write(&ring);
+    const Tensor lo = c.out(lens_in, nb, at::kInt), eo = c.out(ends_in, two, at::kLong), st = c.out(starts_in, ns, at::kInt);
+    const Tensor sl = c.out(slots_in, nt, at::kLong), po = c.out(pos_in, nt, at::kInt);
+    launch(c, "fg_page_step", [&] {
+      return fg_page_step((const int32_t*)lens.data_ptr(), (const int32_t*)add.data_ptr(), (int32_t)batch, (int32_t*)table.data_ptr(),
+                          batch > 1 ? table.stride(0) : width, (int32_t)width, (int32_t*)ring.data_ptr(), (const int64_t*)ends.data_ptr(),
+                          (int32_t)ring.size(0), page, (int32_t*)lo.data_ptr(), (int64_t*)eo.data_ptr(), (int32_t*)st.data_ptr(),
+                          (int64_t*)sl.data_ptr(), (int32_t*)po.data_ptr(), tokens, c.handle);
+    });
+    return tuple({wrap(lo), wrap(eo), wrap(st), wrap(sl), wrap(po)});
+  });
+}
+
+// Strides of a dimension of size 1 do not matter: as if it were dense.
+int64_t stride_of(const Tensor& t, int64_t dim, int64_t dense) { return t.size(dim) > 1 ? t.stride(dim) : dense; }
+bool columns_consecutive(const Tensor& t) { return t.size(-1) <= 1 || t.stride(-1) == 1; }
+int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+
+// k, k_cache, slots, v, v_cache, k_scale, v_scale, stream -> None
+PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (!counted(n_args, 8)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Tensor &k = tensor(a[0]), &kc = tensor(a[1]), &slots = tensor(a[2]);
+    const Tensor *v = maybe(a[3]), *vc = maybe(a[4]), *ks = maybe(a[5]), *vs = maybe(a[6]);
+    if (!v != !vc) refuse("v and v_cache come together");
+    const bool heads_there = k.dim() == 3;
+    if ((k.dim() != 2 && k.dim() != 3) || kc.dim() != k.dim() + 1) refuse("rows must be [n, heads, dim] with a cache [n_pages, page, heads, dim], or [n, dim] with [n_pages, page, dim]");
+    const bool e4m3 = is_type(kc, at::kFloat8_e4m3fn);
+    if (!e4m3 && !is_type(kc, at::kBFloat16)) refuse("caches must be bf16 or float8_e4m3fn");
+    const int64_t n = k.size(0), heads = heads_there ? k.size(1) : 1, dim = k.size(-1), pages = kc.size(0), page = kc.size(1);
+    if (!is_type(slots, at::kLong) || !vector_of(slots, n)) refuse("slots must be int64 [n]");
+    if (heads < 1 || dim < 1 || pages < 1 || page < 1) refuse("rows and caches must not be empty");
+    fits_int32(heads, "too many heads");
+    fits_int32(dim, "rows are too long");
+    fits_int32(pages, "too many pages");
+    fits_int32(page, "pages are too long");
+    Call c(k);
+    fg_append_t part[2];
+    const Tensor* xs[2] = {&k, v};
+    const Tensor* cs[2] = {&kc, vc};
+    const Tensor* ss[2] = {ks, vs};
+    if (!v && vs) refuse("v_scale needs v");
+    for (int i = 0; i < (v ? 2 : 1); ++i) {
+      const Tensor &x = *xs[i], &cache = *cs[i];
+      if (!is_type(x, at::kBFloat16) || x.sizes() != k.sizes() || !columns_consecutive(x)) refuse("new rows must be bf16 with consecutive columns, v like k");
+      if (cache.scalar_type() != kc.scalar_type() || cache.dim() != kc.dim() || cache.size(0) != pages || cache.size(1) != page ||
+          cache.size(-1) != dim || (heads_there && cache.size(2) != heads) || !columns_consecutive(cache))
+        refuse("caches must have consecutive columns, the rows' heads and columns, and be alike");
+      if (e4m3 != (ss[i] != nullptr)) refuse("float8_e4m3fn caches need scales, bf16 caches take none");
+      const int64_t sshape[3] = {pages, heads, page};
+      if (ss[i]) {
+        c.check(ss[i], sshape, at::kFloat, "scales must be float32 [n_pages, heads, page]");
+        if (!ss[i]->is_contiguous()) refuse("scales must be contiguous");
+      }
+      const int64_t width = up8(dim);
+      part[i].x = x.data_ptr();
+      part[i].x_head = heads_there ? stride_of(x, 1, width) : width;
+      part[i].x_row = stride_of(x, 0, width * heads);
+      part[i].cache = cache.data_ptr();
+      part[i].head_stride = heads_there ? stride_of(cache, 2, width) : width;
+      part[i].row_stride = stride_of(cache, 1, width * heads);
+      part[i].page_stride = stride_of(cache, 0, width * heads * page);
+      part[i].scale = (float*)ptr(ss[i]);
+    }
+    c.check_write(&kc); c.check_write(vc); c.check_write(ks); c.check_write(vs);
+    c.use(&k); c.use(v); c.use(&slots);
+    c.on(a[7]);
+    c.write(&kc); c.write(vc); c.write(ks); c.write(vs);
+    launch(c, "fg_kv_append", [&] {
+      return fg_kv_append(&part[0], v ? &part[1] : nullptr, e4m3 ? FG_E4M3 : FG_BF16, (const int64_t*)slots.data_ptr(), n, (int32_t)heads,
+                          (int32_t)dim, (int32_t)pages, (int32_t)page, c.handle);
+    });
+    return none();
+  });
+}
+
+// Tables and lengths of the requests in a cache of `pages` pages.
+fg_pages_t requests(Call& c, const Tensor& table, const Tensor& lens, int64_t batch, int64_t pages, int64_t page) {
+  ROWS2D(table, "table");
+  if (!is_type(table, at::kInt) || table.size(0) != batch || table.size(1) < 1 || !is_type(lens, at::kInt) || !vector_of(lens, batch))
+    refuse("table must be int32 [batch, pages], lens int32 [batch]");
+  if (page < 16 || page % 16) refuse("pages must have a multiple of 16 rows");
+  if (pages < 1) refuse("the cache must have pages");
+  fits_int32(batch, "too many requests");
+  fits_int32(table.size(1), "the table is too wide");
+  fits_int32(pages, "too many pages");
+  fits_int32(page, "pages are too long");
+  c.use(&table);
+  c.use(&lens);
+  return {(const int32_t*)table.data_ptr(), batch > 1 ? table.stride(0) : table.size(1), (int32_t)table.size(1), (const int32_t*)lens.data_ptr(),
+          (int32_t)batch, (int32_t)pages, (int32_t)page};
+}
+
+// The scale of the scores; None: one over the root of n.
+float score_scale(PyObject* o, int64_t n) {
+  const float s = o == Py_None ? (float)(1.0 / std::sqrt((double)n)) : (float)number(o);
+  if (!(s > 0.0f) || !(s < INFINITY)) refuse("scale must be positive and finite");
+  return s;
+}
+
+// Output [n][heads][dim], and lse [n][heads] if it is asked for (True) or given.
+struct AttentionOut {
+  Tensor out, lse;
+  bool has_lse = false;
+  const Tensor *out_in, *lse_in = nullptr;
+  int64_t shape[3];
+  AttentionOut(const Call& c, PyObject* o, PyObject* l, int64_t n, int64_t heads, int64_t dim) : out_in(maybe(o)), shape{n, heads, dim} {
+    c.check(out_in, shape, at::kBFloat16, "out must be bf16 [rows, heads, dim]");
+    if (out_in && !columns_consecutive(*out_in)) refuse("out must have consecutive columns");
+    if (PyBool_Check(l) || l == Py_None) {
+      has_lse = l == Py_True;
+    } else {
+      lse_in = &tensor(l);
+      has_lse = true;
+      c.check(lse_in, at::IntArrayRef(shape, 2), at::kFloat, "lse must be float32 [rows, heads]");
+      if (!lse_in->is_contiguous()) refuse("lse must be contiguous");
+    }
+  }
+  void make(Call& c) {
+    out = c.out(out_in, shape, at::kBFloat16);
+    if (has_lse) lse = c.out(lse_in, at::IntArrayRef(shape, 2), at::kFloat);
+  }
+  int64_t row() const { return stride_of(out, 0, shape[1] * shape[2]); }
+  int64_t head() const { return stride_of(out, 1, shape[2]); }
+  float* lse_ptr() const { return has_lse ? (float*)lse.data_ptr() : nullptr; }
+  PyObject* result() const { return has_lse ? tuple({wrap(out), wrap(lse)}) : wrap(out); }
+};
+
+Tensor workspace_of(const Call& c, const Tensor* given, int64_t bytes) {
+  const int64_t shape[1] = {bytes};
+  return given ? *given : c.memory(shape, at::kByte);
+}
+
+void check_queries(const Tensor& q) {
+  if (!is_type(q, at::kBFloat16) || q.dim() != 3 || !columns_consecutive(q)) refuse("q must be bf16 [rows, heads, dim] with consecutive columns");
+  if (q.size(1) < 1 || q.size(1) > FG_ATTN_MAX_HEADS) refuse("1 to 65535 heads");
+}
+
+// q, k_cache, v_cache, table, lens, scale, window, k_scale, v_scale, out, lse, workspace, stream -> out or (out, lse)
+PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (!counted(n_args, 13)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Tensor &q = tensor(a[0]), &k = tensor(a[1]), &v = tensor(a[2]), &table = tensor(a[3]), &lens = tensor(a[4]);
+    const Tensor *ks = maybe(a[7]), *vs = maybe(a[8]), *ws_in = maybe(a[11]);
+    check_queries(q);
+    const bool e4m3 = is_type(k, at::kFloat8_e4m3fn);
+    if ((!e4m3 && !is_type(k, at::kBFloat16)) || k.scalar_type() != v.scalar_type() || k.dim() != 4 || v.sizes() != k.sizes() ||
+        !columns_consecutive(k) || !columns_consecutive(v))
+      refuse("caches must be bf16 or float8_e4m3fn [n_pages, page, heads, dim] with consecutive columns");
+    const int64_t batch = q.size(0), heads = q.size(1), dim = q.size(2), kv = k.size(2);
+    if (k.size(3) != dim || (dim != 64 && dim != 128 && dim != 256)) refuse("queries and caches must have 64, 128 or 256 columns");
+    if (kv < 1 || heads % kv) refuse("the queries' heads must be a multiple of the cache's");
+    if (batch > FG_ATTN_MAX_BATCH) refuse("up to 65535 requests");
+    const float scale = score_scale(a[5], dim);
+    const int32_t window = int32_of(a[6], "window must be an int32");
+    if (window < 0) refuse("window must not be negative");
+    if (e4m3 != (ks != nullptr) || e4m3 != (vs != nullptr)) refuse("float8_e4m3fn caches need k_scale and v_scale, bf16 caches take none");
+    Call c(q);
+    const int64_t sshape[3] = {k.size(0), kv, k.size(1)};
+    c.check(ks, sshape, at::kFloat, "scales must be float32 [n_pages, heads, page]");
+    c.check(vs, sshape, at::kFloat, "scales must be float32 [n_pages, heads, page]");
+    if ((ks && !ks->is_contiguous()) || (vs && !vs->is_contiguous())) refuse("scales must be contiguous");
+    AttentionOut o(c, a[9], a[10], batch, heads, dim);
+    if (ws_in && !ws_in->is_contiguous()) refuse("workspace must be contiguous");
+    const fg_pages_t pages = requests(c, table, lens, batch, k.size(0), k.size(1));
+    c.use(&q); c.use(&k); c.use(&v); c.use(ks); c.use(vs); c.use(ws_in);
+    c.on(a[12]);
+    o.make(c);
+    int64_t need = 0;
+    if (fg_paged_attention_bytes((int32_t)batch, (int32_t)kv, (int32_t)(heads / kv), (int32_t)dim, &need) != FG_OK) refuse("too large");
+    const Tensor ws = workspace_of(c, ws_in, need);
+    const fg_cache_t kp{k.data_ptr(), stride_of(k, 0, k.size(1) * kv * dim), stride_of(k, 1, kv * dim), stride_of(k, 2, dim), (const float*)ptr(ks)};
+    const fg_cache_t vp{v.data_ptr(), stride_of(v, 0, v.size(1) * kv * dim), stride_of(v, 1, kv * dim), stride_of(v, 2, dim), (const float*)ptr(vs)};
+    launch(c, "fg_paged_attention", [&] {
+      return fg_paged_attention(q.data_ptr(), stride_of(q, 0, heads * dim), stride_of(q, 1, dim), &kp, &vp, e4m3 ? FG_E4M3 : FG_BF16, &pages,
+                                (int32_t)kv, (int32_t)(heads / kv), (int32_t)dim, window, scale, ws.data_ptr(), (int64_t)ws.nbytes(),
+                                o.out.data_ptr(), o.row(), o.head(), o.lse_ptr(), heads, c.handle);
+    });
+    return o.result();
+  });
+}
+
+// Sizes of latent attention, from the queries, the weights and the rows' columns.
+struct LatentSizes {
+  int64_t rows, heads, rank, rope, nope;
+  LatentSizes(const Tensor& q, const Tensor& w, int64_t columns, int64_t nope_) : rows(q.size(0)), heads(q.size(1)), nope(nope_) {
+    if (!is_type(w, at::kBFloat16) || w.dim() != 3 || !w.is_contiguous() || w.size(0) != heads || w.size(1) != 2 * nope)
+      refuse("w must be contiguous bf16 [heads, 2 nope, rank]");
+    rank = w.size(2);
+    rope = columns - rank;
+    if ((rank != 256 && rank != 512) || (rope != 32 && rope != 64) || (nope != 64 && nope != 128)) refuse("rank 256 or 512, rope 32 or 64, nope 64 or 128");
+    if (q.size(2) != nope + rope) refuse("q must have nope + rope columns, the latent rows rank + rope");
+  }
+};
+
+// q, w, cache, table, lens, nope, scale, out, lse, workspace, stream -> out or (out, lse)
+PyObject* latent_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (!counted(n_args, 11)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Tensor &q = tensor(a[0]), &w = tensor(a[1]), &cache = tensor(a[2]), &table = tensor(a[3]), &lens = tensor(a[4]);
+    const Tensor* ws_in = maybe(a[9]);
+    check_queries(q);
+    if (!is_type(cache, at::kBFloat16) || cache.dim() != 3 || !columns_consecutive(cache)) refuse("cache must be bf16 [n_pages, page, rank + rope] with consecutive columns");
+    const LatentSizes z(q, w, cache.size(2), int32_of(a[5], "nope must be an int32"));
+    if (z.rows > FG_ATTN_MAX_BATCH) refuse("up to 65535 requests");
+    const float scale = score_scale(a[6], z.nope + z.rope);
+    Call c(q);
+    AttentionOut o(c, a[7], a[8], z.rows, z.heads, z.nope);
+    if (ws_in && !ws_in->is_contiguous()) refuse("workspace must be contiguous");
+    const fg_pages_t pages = requests(c, table, lens, z.rows, cache.size(0), cache.size(1));
+    c.use(&q); c.use(&w); c.use(&cache); c.use(ws_in);
+    c.on(a[10]);
+    o.make(c);
+    int64_t need = 0;
+    if (fg_latent_attention_bytes((int32_t)z.rows, (int32_t)z.heads, (int32_t)z.rank, &need) != FG_OK) refuse("too large");
+    const Tensor ws = workspace_of(c, ws_in, need);
+    launch(c, "fg_latent_attention", [&] {
+      return fg_latent_attention(q.data_ptr(), stride_of(q, 0, z.heads * q.size(2)), stride_of(q, 1, q.size(2)), w.data_ptr(), cache.data_ptr(),
+                                 stride_of(cache, 0, cache.size(1) * cache.size(2)), stride_of(cache, 1, cache.size(2)), &pages, (int32_t)z.heads,
+                                 (int32_t)z.rank, (int32_t)z.rope, (int32_t)z.nope, scale, ws.data_ptr(), (int64_t)ws.nbytes(), o.out.data_ptr(), o.row(),
+                                 o.head(), o.lse_ptr(), z.heads, c.handle);
+    });
+    return o.result();
+  });
+}
+
+// q, latent, w, q_starts, k_starts, nope, scale, out, lse, workspace, stream -> out or (out, lse)
+PyObject* latent_prompt(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (!counted(n_args, 11)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Tensor &q = tensor(a[0]), &lat = tensor(a[1]), &w = tensor(a[2]), &qs = tensor(a[3]), &ks = tensor(a[4]);
+    const Tensor* ws_in = maybe(a[9]);
+    check_queries(q);
+    ROWS2D(lat, "latent");
+    if (!is_type(lat, at::kBFloat16)) refuse("latent must be bf16 [rows, rank + rope]");
+    const LatentSizes z(q, w, lat.size(1), int32_of(a[5], "nope must be an int32"));
+    const float scale = score_scale(a[6], z.nope + z.rope);
+    if (!is_type(qs, at::kInt) || qs.dim() != 1 || qs.size(0) < 1 || !vector_of(qs, qs.size(0)) || !is_type(ks, at::kInt) || !vector_of(ks, qs.size(0)))
+      refuse("q_starts and k_starts must be int32 [batch + 1]");
+    const int64_t batch = qs.size(0) - 1;
+    if (batch > FG_ATTN_MAX_BATCH) refuse("up to 65535 requests");
+    Call c(q);
+    AttentionOut o(c, a[7], a[8], z.rows, z.heads, z.nope);
+    if (ws_in && !ws_in->is_contiguous()) refuse("workspace must be contiguous");
+    c.use(&q); c.use(&lat); c.use(&w); c.use(&qs); c.use(&ks); c.use(ws_in);
+    c.on(a[10]);
+    int64_t need = 0;
+    if (fg_latent_prompt_bytes(lat.size(0), (int32_t)z.heads, (int32_t)z.nope, &need) != FG_OK) refuse("too large");
+    o.make(c);
+    const Tensor ws = workspace_of(c, ws_in, need);
+    launch(c, "fg_latent_prompt", [&] {
+      return fg_latent_prompt(q.data_ptr(), stride_of(q, 0, z.heads * q.size(2)), stride_of(q, 1, q.size(2)), (const int32_t*)qs.data_ptr(), z.rows,
+                              lat.data_ptr(), ld(lat), (const int32_t*)ks.data_ptr(), lat.size(0), (int32_t)batch, w.data_ptr(), (int32_t)z.heads,
+                              (int32_t)z.rank, (int32_t)z.rope, (int32_t)z.nope, scale, ws.data_ptr(), (int64_t)ws.nbytes(), o.out.data_ptr(), o.row(),
+                              o.head(), o.lse_ptr(), z.heads, c.handle);
+    });
+    return o.result();
+  });
+}
+
 PyObject* setup(PyObject*, PyObject* error) {
   Py_INCREF(error);
   Py_XDECREF(g_error);
@@ -448,6 +752,11 @@ PyMethodDef methods[] = {
     {"moe_route", (PyCFunction)(void*)moe_route, METH_FASTCALL, nullptr},
     {"w4_linear", (PyCFunction)(void*)w4_linear, METH_FASTCALL, nullptr},
     {"moe_few", (PyCFunction)(void*)moe_few, METH_FASTCALL, nullptr},
+    {"page_step", (PyCFunction)(void*)page_step, METH_FASTCALL, nullptr},
+    {"kv_append", (PyCFunction)(void*)kv_append, METH_FASTCALL, nullptr},
+    {"paged_attention", (PyCFunction)(void*)paged_attention, METH_FASTCALL, nullptr},
+    {"latent_attention", (PyCFunction)(void*)latent_attention, METH_FASTCALL, nullptr},
+    {"latent_prompt", (PyCFunction)(void*)latent_prompt, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "fg_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

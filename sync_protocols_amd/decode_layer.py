@@ -13,7 +13,9 @@ With the experts spread over GPUs every one runs the same step on its share
     python -m sync_protocols_amd.decode_layer [--tokens N] [--hidden ..] [--width ..]
 
 runs it on random weights, call by call and as a graph, and prints the time of each
-and how far the results are from the same step in float32.
+and how far the results are from the same step in float32. With --attention paged
+or latent a step starts at the layer's input instead: attention_layer's half, over a
+paged cache of --context tokens a request, in front of this one.
 """
 from __future__ import annotations
 
@@ -137,6 +139,34 @@ def _time_us(f, repeat: int) -> float:
     return start.elapsed_time(end) / repeat * 1e3
 
 
+def _whole_layer(c) -> None:
+    from . import attention_layer as A
+    page, new = 64, 3 * c.repeat + 16
+    width = -(-(c.context + new) // page)
+    pages = A.Pages(c.tokens, width, c.tokens * width, page)
+    if c.attention == "paged":
+        attention = A.random_paged(c.hidden, c.heads // 128, max(1, c.heads // 512), 128, pages)
+    else:
+        attention = A.random_latent(c.hidden, c.heads // 128, 512, 64, 128, pages)
+    experts = random_layer(c.hidden, c.width, c.heads, c.experts, c.local, c.top_k, norm_out=c.norm_out)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for cache in (attention.k, attention.v) if c.attention == "paged" else (attention.cache,):
+        cache.normal_(generator=g)
+    pages.step(torch.full_like(pages.lens, c.context), 0 if c.context == 0 else c.tokens * c.context)
+    captured = A.CapturedDecode(attention, experts, c.tokens)
+    captured.x.normal_(generator=g)
+    captured.add.fill_(1)
+    before = pages.lens.clone(), pages.ends.clone()
+    want = A.decode_step(attention, experts, captured.x, captured.add)
+    pages.lens.copy_(before[0])
+    pages.ends.copy_(before[1])
+    got = captured.replay()
+    torch.cuda.synchronize()
+    print(f"{c.tokens} requests of {c.context} tokens, {c.attention} attention: graph equals calls: {torch.equal(got.y, want.y)}")
+    print(f"call by call {_time_us(lambda: A.decode_step(attention, experts, captured.x, captured.add, *captured.workspace), c.repeat):.1f} us, "
+          f"as a graph {_time_us(captured.replay, c.repeat):.1f} us a step")
+
+
 def main(argv=None) -> None:
     p = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     p.add_argument("--tokens", type=int, default=4)
@@ -148,7 +178,11 @@ def main(argv=None) -> None:
     p.add_argument("--top-k", type=int, default=8)
     p.add_argument("--norm-out", choices=("bf16", "i8", "e4m3"), default="e4m3")
     p.add_argument("--repeat", type=int, default=50)
+    p.add_argument("--attention", choices=("none", "paged", "latent"), default="none")
+    p.add_argument("--context", type=int, default=4096, help="tokens that a request has in the cache")
     c = p.parse_args(argv)
+    if c.attention != "none":
+        return _whole_layer(c)
     layer = random_layer(c.hidden, c.width, c.heads, c.experts, c.local, c.top_k, norm_out=c.norm_out)
     captured = CapturedStep(layer, c.tokens, c.heads)
     g = torch.Generator(device="cuda").manual_seed(1)

@@ -37,6 +37,8 @@ EXPORTS = ("fg_init", "fg_gather_gemm", "fg_gather_gemm_staged", "fg_gather_gemm
            "fg_pingpong", "fg_stress", "fg_combine", "fg_litmus", "fg_stats", "fg_views", "fg_capacity",
            "fg_gather_gemm_noalloc", "fg_add_rmsnorm", "fg_moe_route", "fg_w4_linear", "fg_moe_few_bytes", "fg_moe_few",
            "fg_destroy", "fg_strerror")
+ATTENTION_EXPORTS = ("fg_page_step", "fg_kv_append", "fg_paged_attention_bytes", "fg_paged_attention", "fg_latent_attention_bytes",
+                     "fg_latent_attention", "fg_latent_prompt_bytes", "fg_latent_prompt")       # include/fg_attention.h
 
 
 class FgConfig(C.Structure):
@@ -54,6 +56,21 @@ class FgRoute(C.Structure):
                 ("stream_len", C.POINTER(C.c_int32)), ("src_row", C.c_void_p), ("dst_row", C.c_void_p),
                 ("m_pad", C.c_int32), ("group_off", C.POINTER(C.c_int32)),
                 ("topk", C.c_void_p), ("topk_k", C.c_int32), ("expert_base", C.c_int32)]
+
+
+class FgAppend(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("x_row", C.c_int64), ("x_head", C.c_int64), ("cache", C.c_void_p),
+                ("page_stride", C.c_int64), ("row_stride", C.c_int64), ("head_stride", C.c_int64), ("scale", C.c_void_p)]
+
+
+class FgPages(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("ldt", C.c_int64), ("width", C.c_int32), ("lens", C.c_void_p), ("batch", C.c_int32),
+                ("n_pages", C.c_int32), ("page", C.c_int32)]
+
+
+class FgCache(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("page_stride", C.c_int64), ("row_stride", C.c_int64), ("head_stride", C.c_int64),
+                ("scale", C.c_void_p)]
 
 
 class FgStats(C.Structure):
@@ -128,10 +145,22 @@ def load_library() -> C.CDLL:
     lib.fg_moe_few_bytes.argtypes = [i32, i32, i32, C.POINTER(i64)]
     lib.fg_moe_few.argtypes = [vp, i64, i32, vp, i32, vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32,
                                vp, i64, vp, i64, vp]
+    pi64 = C.POINTER(i64)
+    lib.fg_page_step.argtypes = [vp, vp, i32, vp, i64, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, i32, vp]
+    lib.fg_kv_append.argtypes = [C.POINTER(FgAppend), C.POINTER(FgAppend), i32, vp, i64, i32, i32, i32, i32, vp]
+    lib.fg_paged_attention_bytes.argtypes = [i32, i32, i32, i32, pi64]
+    lib.fg_paged_attention.argtypes = [vp, i64, i64, C.POINTER(FgCache), C.POINTER(FgCache), i32, C.POINTER(FgPages), i32, i32, i32, i32, f32,
+                                       vp, i64, vp, i64, i64, vp, i64, vp]
+    lib.fg_latent_attention_bytes.argtypes = [i32, i32, i32, pi64]
+    lib.fg_latent_attention.argtypes = [vp, i64, i64, vp, vp, i64, i64, C.POINTER(FgPages), i32, i32, i32, i32, f32, vp, i64, vp, i64, i64,
+                                        vp, i64, vp]
+    lib.fg_latent_prompt_bytes.argtypes = [i64, i32, i32, pi64]
+    lib.fg_latent_prompt.argtypes = [vp, i64, i64, vp, i64, vp, i64, vp, i64, i32, vp, i32, i32, i32, i32, f32, vp, i64, vp, i64, i64, vp, i64,
+                                     vp]
     lib.fg_destroy.argtypes = [vp]
     lib.fg_strerror.argtypes = [C.c_int]
     lib.fg_strerror.restype = C.c_char_p
-    for f in EXPORTS[:-1]:
+    for f in EXPORTS[:-1] + ATTENTION_EXPORTS:
         getattr(lib, f).restype = C.c_int
     _lib = lib
     return lib

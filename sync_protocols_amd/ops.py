@@ -1,12 +1,15 @@
-"""The decoding operators of libfg.so (include/fg.h) on torch tensors: residual
-RMS norm with 8-bit output, router choice, products with 4-bit weights, and the
-expert layer for few tokens.
+"""The decoding operators of libfg.so on torch tensors. The expert half of a
+decoder layer (include/fg.h): residual RMS norm with 8-bit output, router choice,
+products with 4-bit weights, and the expert layer for few tokens. The attention
+half (include/fg_attention.h): pages and slots of a step, rows written into a paged cache,
+attention of one new token over it, and latent attention, for one new token and
+for prompts.
 
 Every function checks its tensors' types, shapes, strides and device, launches on
 the current stream (or on `stream`) without synchronising, and raises
 fg.FgError (code fg.EINVAL) for arguments it does not take. Outputs are allocated
 unless given. All of them may be captured into a graph; nothing is kept between
-calls. The formulas and limits stand at the entry points in include/fg.h.
+calls. The formulas and limits stand at the entry points in the two headers.
 
 There is no backward pass: tensors that require gradients are refused unless
 gradients are off (torch.no_grad()). Given buffers count as written in place.
@@ -35,6 +38,7 @@ NORM_MAX_N = 65536
 W4_MAX_ROWS = 1048576
 FEW_MAX_SIZE, FEW_MAX_ROW_BYTES = 16777216, 67108864
 MOE_FEW_TOKENS, MOE_FEW_TOPK, MOE_FEW_EXPERTS = 64, 16, 1024
+ATTN_MAX_BATCH, ATTN_MAX_HEADS, APPEND_MAX_DIM = 65535, 65535, 1024
 
 
 class NormResult(NamedTuple):
@@ -99,13 +103,17 @@ def w4_linear(x: torch.Tensor, w: W4Weight, *, x_scale: Optional[torch.Tensor] =
     return (_native or load_extension()).w4_linear(x, x_scale, w.q, w.scale, w.zero, bias, out, stream)
 
 
+def _bytes(name: str, *sizes: int) -> int:
+    v = C.c_int64(0)
+    code = getattr(fg.load_library(), name)(*sizes, C.byref(v))
+    if code != fg.OK:
+        raise fg.FgError(code, name)
+    return v.value
+
+
 def moe_few_bytes(tokens: int, k: int, width: int) -> int:
     """Workspace bytes of moe_few."""
-    v = C.c_int64(0)
-    code = fg.load_library().fg_moe_few_bytes(tokens, k, width, C.byref(v))
-    if code != fg.OK:
-        raise fg.FgError(code, "fg_moe_few_bytes")
-    return v.value
+    return _bytes("fg_moe_few_bytes", tokens, k, width)
 
 
 def moe_few(x: torch.Tensor, w1: Union[torch.Tensor, W4Weight], w2: Union[torch.Tensor, W4Weight], topk: torch.Tensor,
@@ -118,3 +126,84 @@ def moe_few(x: torch.Tensor, w1: Union[torch.Tensor, W4Weight], w2: Union[torch.
     a = w1 if isinstance(w1, W4Weight) else (w1, None, None)
     b = w2 if isinstance(w2, W4Weight) else (w2, None, None)
     return (_native or load_extension()).moe_few(x, x_scale, *a, *b, topk, weights, expert_base, out, workspace, stream)
+
+
+class PageStep(NamedTuple):
+    lens: torch.Tensor               # int32 [batch]
+    ends: torch.Tensor               # int64 [2]
+    starts: torch.Tensor             # int32 [batch + 1]
+    slots: torch.Tensor              # int64 [tokens], -1 where there is no token
+    positions: torch.Tensor          # int32 [tokens]
+
+
+def page_step(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, ring: torch.Tensor, ends: torch.Tensor, *, page: int,
+              tokens: int, lens_out: Optional[torch.Tensor] = None, ends_out: Optional[torch.Tensor] = None,
+              starts: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+              stream=None) -> PageStep:
+    """One scheduling step: request b of lens[b] tokens wants add[b] new ones (0 none;
+    negative: it has ended and its pages go back). Pages come from `ring` (int32
+    [n_pages], numbers ends[0]..ends[1]-1 are free) into `table` (int32 [batch, pages]), both
+    written in place; lens_out and ends_out may be lens and ends themselves. A
+    request that does not get its pages, or whose tokens no longer fit `tokens`,
+    keeps its length. Feed `slots` to kv_append, `lens` to the attention."""
+    return PageStep(*(_native or load_extension()).page_step(lens, add, table, ring, ends, page, tokens, lens_out, ends_out, starts, slots,
+                                                             positions, stream))
+
+
+def kv_append(k: torch.Tensor, k_cache: torch.Tensor, slots: torch.Tensor, *, v: Optional[torch.Tensor] = None,
+              v_cache: Optional[torch.Tensor] = None, k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+              stream=None) -> None:
+    """Write bf16 rows [n, heads, dim] into caches [n_pages, page, heads, dim] (or
+    [n, dim] into [n_pages, page, dim], as latent rows are) at slots int64 [n]; rows with
+    a slot outside the cache are skipped. bf16 caches, or float8_e4m3fn ones with
+    scales float32 [n_pages, heads, page], one a row and head."""
+    (_native or load_extension()).kv_append(k, k_cache, slots, v, v_cache, k_scale, v_scale, stream)
+
+
+def paged_attention_bytes(batch: int, kv_heads: int, group: int, dim: int) -> int:
+    """Workspace bytes of paged_attention for kv_heads * group query heads."""
+    return _bytes("fg_paged_attention_bytes", batch, kv_heads, group, dim)
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, *,
+                    scale: Optional[float] = None, window: int = 0, k_scale: Optional[torch.Tensor] = None,
+                    v_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    lse: Union[bool, torch.Tensor] = False, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of one new token a request, bf16 q [batch, heads, dim], over the
+    lens[b] tokens that `table` names in caches [n_pages, page, kv_heads, dim] (bf16, or
+    float8_e4m3fn with k_scale and v_scale as kv_append writes them), or the last
+    `window` of them. bf16 [batch, heads, dim], or (that, lse float32 [batch, heads])
+    with lse True or a buffer. scale: 1 / sqrt(dim) unless given."""
+    return (_native or load_extension()).paged_attention(q, k_cache, v_cache, table, lens, scale, window, k_scale, v_scale, out, lse, workspace,
+                                                         stream)
+
+
+def latent_attention_bytes(batch: int, heads: int, rank: int) -> int:
+    """Workspace bytes of latent_attention."""
+    return _bytes("fg_latent_attention_bytes", batch, heads, rank)
+
+
+def latent_attention(q: torch.Tensor, w: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, *, nope: int,
+                     scale: Optional[float] = None, out: Optional[torch.Tensor] = None, lse: Union[bool, torch.Tensor] = False,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Latent attention of one new token a request, absorbed form: bf16 q [batch,
+    heads, nope + rope] over rows [latent | rotary key] of a cache [n_pages, page, rank + rope],
+    with w [heads, 2 nope, rank], the keys' nope rows of a head before the values'.
+    bf16 [batch, heads, nope], or (that, lse). scale: 1 / sqrt(nope + rope) unless given."""
+    return (_native or load_extension()).latent_attention(q, w, cache, table, lens, nope, scale, out, lse, workspace, stream)
+
+
+def latent_prompt_bytes(k_rows: int, heads: int, nope: int) -> int:
+    """Workspace bytes of latent_prompt."""
+    return _bytes("fg_latent_prompt_bytes", k_rows, heads, nope)
+
+
+def latent_prompt(q: torch.Tensor, latent: torch.Tensor, w: torch.Tensor, q_starts: torch.Tensor, *, nope: int,
+                  k_starts: Optional[torch.Tensor] = None, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                  lse: Union[bool, torch.Tensor] = False, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Latent attention of prompts, expanded form: request b has the queries
+    q_starts[b]..q_starts[b + 1]-1 of bf16 q [rows, heads, nope + rope], the last tokens of the rows
+    k_starts[b]..k_starts[b + 1]-1 (q_starts unless given) of bf16 latent [rows, rank + rope]; each
+    sees itself and what is before it. w as for latent_attention. bf16 [rows, heads, nope], or (that, lse)."""
+    return (_native or load_extension()).latent_prompt(q, latent, w, q_starts, q_starts if k_starts is None else k_starts, nope, scale, out, lse,
+                                                       workspace, stream)
