@@ -27,7 +27,7 @@ Rows rows3(const void* p, int64_t element, int64_t n, int64_t ns, int64_t heads,
 // has two units (256 tokens) at least, whose reads outweigh the sums that it leaves.
 constexpr int kPagedPlaces = 2 * kCUs, kPagedLeast = 2;
 int paged_target(int64_t parts) {
-  const int64_t t = 2 * kPagedPlaces / parts;
+  const int64_t t = kPagedPlaces / parts;
   return (int)(t < 1 ? 1 : t);
 }
 // 16-head tiles of a workgroup, as many as the group fills and the registers hold, and the workgroups that this makes of all heads
@@ -190,18 +190,17 @@ fg_status fg_paged_attention(const void* q, int64_t q_b, int64_t q_h, const fg_c
   a.v_page = es * v->page_stride; a.v_head = es * v->head_stride; a.v_tok = (int32_t)(es * v->row_stride);
   a.kv = kv; a.group = group; a.heads = (int32_t)heads; a.c = scale * kLog2E;
   Launches go{stream};
-  const dim3 grid((unsigned)items, (unsigned)parts);
+  const dim3 grid((unsigned)target, (unsigned)parts);
   const int tiles = head_tiles(group, dim);
   if (dim == 64) launch_paged<64>(e4m3, a, tiles, grid, go);
   else if (dim == 128) launch_paged<128>(e4m3, a, tiles, grid, go);
   else launch_paged<256>(e4m3, a, tiles, grid, go);
-  // a table this narrow leaves one piece a request
-  if ((int64_t)pages->width * pages->page > (int64_t)kPagedLeast * kPagedUnit) {
+  // a table this narrow leaves one unit, and so one piece, a request
+  if ((int64_t)pages->width * pages->page > kPagedUnit) {
     const JoinArgs j{a.split.pieces, a.part, a.ml, a.out, lse, out_b, out_h, lse_b, (int32_t)heads};
-    const dim3 jg((unsigned)heads, (unsigned)batch), jb(64 * kJoinWaves);
-    if (dim == 64) go(join_kernel<64, false>, jg, jb, 0, j);
-    else if (dim == 128) go(join_kernel<128, false>, jg, jb, 0, j);
-    else go(join_kernel<256, false>, jg, jb, 0, j);
+    if (dim == 64) launch_join<64>(j, batch, target, go);
+    else if (dim == 128) launch_join<128>(j, batch, target, go);
+    else launch_join<256>(j, batch, target, go);
   }
   return go.status();
 }

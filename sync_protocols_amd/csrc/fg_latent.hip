@@ -22,27 +22,39 @@ bool sizes_ok(int32_t heads, int32_t rank, int32_t rope, int32_t nope, float sca
 }
 
 // 16-head tiles of a workgroup, and the workgroups that this makes of all heads.
-int head_tiles(int32_t heads) { return heads <= 16 ? 1 : heads <= 32 ? 2 : heads <= 64 ? 4 : 8; }
+int head_tiles(int32_t heads) { return heads <= 16 ? 1 : heads <= 32 ? 2 : 4; }
 int64_t head_parts(int32_t heads) { return (heads + 16 * head_tiles(heads) - 1) / (16 * head_tiles(heads)); }
-// One workgroup a compute unit, which its LDS fills.
+// Workgroups of four waves that share tiles of 64 rows, one a compute unit, or, up to 32 heads, of two waves and 32 rows, two a unit: their LDS fills it.
+int latent_tile(int32_t heads) { return head_tiles(heads) > 2 ? 64 : 32; }
 int latent_target(int32_t heads) {
-  const int64_t t = kCUs / head_parts(heads);
+  const int64_t t = kCUs * (64 / latent_tile(heads)) / head_parts(heads);
   return (int)(t < 1 ? 1 : t);
 }
 constexpr int kLatentLeast = 2;
 
-template <int R, int P, int HT, int S>
+template <int R, int P, int G, int HW>
 void launch_latent(const LatentArgs& a, dim3 grid, Launches& go) {
-  go(latent_kernel<R, P, HT, S>, grid, dim3(64 * HT * S), LatentShape<R, P, HT, S>::LDS, a);
+  go(latent_kernel<R, P, G, HW>, grid, dim3(128 * G), LatentShape<R, P, G, HW>::LDS, a);
 }
 template <int R, int P>
 void launch_latent(const LatentArgs& a, dim3 grid, Launches& go) {
   switch (head_tiles(a.heads)) {
-    case 1: launch_latent<R, P, 1, 4>(a, grid, go); break;
-    case 2: launch_latent<R, P, 2, 2>(a, grid, go); break;
-    case 4: launch_latent<R, P, 4, 1>(a, grid, go); break;
-    default: launch_latent<R, P, 8, 1>(a, grid, go);
+    case 1: launch_latent<R, P, 1, 1>(a, grid, go); break;
+    case 2: launch_latent<R, P, 1, 2>(a, grid, go); break;
+    default: launch_latent<R, P, 2, 2>(a, grid, go);
   }
+}
+
+// Many pieces a request: more than 16, if lengths are even.
+template <int R, bool MANY>
+void launch_join_as(const LatentArgs& a, Launches& go) {
+  typedef LatentJoinShape<R, MANY> Sh;
+  go(latent_join_kernel<R, MANY>, dim3((unsigned)a.tiles, (unsigned)a.split.batch, Sh::Z), dim3(64 * Sh::WAVES), 0, a);
+}
+template <int R>
+void launch_join(const LatentArgs& a, Launches& go) {
+  const bool many = a.split.target > 16 * a.split.batch;
+  many ? launch_join_as<R, true>(a, go) : launch_join_as<R, false>(a, go);
 }
 
 template <int M, int P>
@@ -59,9 +71,9 @@ extern "C" {
 
 fg_status fg_latent_attention_bytes(int32_t batch, int32_t heads, int32_t rank, int64_t* bytes) {
   if (!bytes || batch < 0 || batch > FG_ATTN_MAX_BATCH || heads < 1 || heads > FG_ATTN_MAX_HEADS || (rank != 256 && rank != 512)) return FG_EINVAL;
-  const int64_t items = batch + latent_target(heads), rows = (int64_t)batch * heads;
-  // absorbed queries, weighted means (two numbers each); sums of the pieces; pieces of every request
-  *bytes = 6 * rows * rank + items * heads * (4 * rank + 8) + 8 * (int64_t)batch;
+  const int64_t places = batch + latent_target(heads), tiles = (heads + 15) / 16;
+  // absorbed queries; sums of the pieces; weighted means; pieces of every request
+  *bytes = (int64_t)batch * heads * (2 * (rank + 64) + 4 * rank) + places * tiles * 16 * (4 * rank + 8) + 8 * (int64_t)batch;
   return FG_OK;
 }
 
@@ -75,7 +87,7 @@ fg_status fg_latent_attention(const void* q, int64_t q_b, int64_t q_h, const voi
       (int64_t)pages->width * pages->page > kMax)
     return FG_EINVAL;
   const int64_t batch = pages->batch, parts = head_parts(heads);
-  if (batch * ((int64_t)pages->width * pages->page / kLatentTile + 2) > kMax) return FG_EINVAL;
+  if (batch * ((int64_t)pages->width * pages->page / 32 + 2) > kMax) return FG_EINVAL;
   if (batch == 0) return FG_OK;
   if (!q || !w || !cache || !pages->table || !pages->lens || !out || !workspace || workspace_bytes < need) return FG_EINVAL;
   if (!aligned(q, 16) || !aligned(w, 16) || !aligned(cache, 16) || !aligned(out, 2) || !aligned(lse, 4) || !aligned(workspace, 16) ||
@@ -90,41 +102,36 @@ fg_status fg_latent_attention(const void* q, int64_t q_b, int64_t q_h, const voi
   const Rows wr = whole(w, 4 * (int64_t)heads * nope * rank), le = whole(pages->lens, 4 * batch);
   const Rows t{pages->table, batch, 4 * (int64_t)pages->width, 4 * pages->ldt}, ls{lse, batch, 4 * (int64_t)heads, 4 * lse_b};
   if (overlaps(o, qr, wr, cr, t, le, ws, ls) || overlaps(ls, qr, wr, cr, t, le, ws) || overlaps(ws, qr, wr, cr, t, le)) return FG_EINVAL;
-  const int64_t items = batch + latent_target(heads), rows = batch * heads;
+  const int64_t places = batch + latent_target(heads), tiles = (heads + 15) / 16;
   char* at = (char*)workspace;
-  char* const absorbed = at;
-  at += 2 * rows * rank;
-  char* const mean = at;
-  at += 4 * rows * rank;
   LatentArgs a{};
+  char* const absorbed = at;
+  at += batch * heads * 2 * (rank + 64);
   a.part = (float*)at;
-  at += 4 * items * heads * rank;
+  at += places * tiles * 64 * rank;
   a.ml = (float*)at;
-  at += 8 * items * heads;
+  at += places * tiles * 128;
+  a.mean = (uint16_t*)at;
+  at += batch * heads * 4 * rank;
   a.split = SplitArgs{pages->lens, pages->table, pages->ldt, pages->batch, pages->width, pages->n_pages, pages->page, 0, latent_target(heads), kLatentLeast,
                       (int32_t*)at};
   a.a = absorbed;
-  a.q = (const char*)q + 2 * nope;
   a.cache = (const char*)cache;
-  a.out = (uint16_t*)mean; a.lse = lse;
-  a.q_b = 2 * q_b; a.q_h = 2 * q_h; a.c_page = 2 * page_stride; a.c_tok = (int32_t)(2 * row_stride); a.lse_b = lse_b;
-  a.heads = heads; a.c = scale * kLog2E;
+  a.lse = lse;
+  a.c_page = 2 * page_stride; a.c_tok = (int32_t)(2 * row_stride); a.lse_b = lse_b;
+  a.heads = heads; a.tiles = (int32_t)tiles; a.parts = (int32_t)parts; a.c = scale * kLog2E;
   Launches go{stream};
-  const unsigned tiles = (unsigned)((batch + 15) / 16);
-  const HeadsArgs absorb{(const char*)q, (const char*)w, (uint16_t*)absorbed, 2 * q_b, 2 * q_h, 4 * (int64_t)nope * rank, (int64_t)heads * rank, rank,
-                         (int32_t)batch, heads, nope, rank};
-  go(heads_product_kernel<true>, dim3((unsigned)rank / 128, (unsigned)heads, tiles), dim3(64), 0, absorb);
-  const dim3 grid((unsigned)items, (unsigned)parts);
+  const unsigned b_tiles = (unsigned)((batch + 15) / 16);
+  const AbsorbArgs absorb{(const char*)q, (const char*)w, absorbed, 2 * q_b, 2 * q_h, 4 * (int64_t)nope * rank, (int32_t)batch, heads, nope, rank, rope};
+  go(absorb_kernel, dim3((unsigned)rank / 128, (unsigned)heads, b_tiles), dim3(64), 0, absorb);
+  const dim3 grid((unsigned)((a.split.target + 7) / 8 * 8 * parts));
   if (rank == 512) rope == 64 ? launch_latent<512, 64>(a, grid, go) : launch_latent<512, 32>(a, grid, go);
   else rope == 64 ? launch_latent<256, 64>(a, grid, go) : launch_latent<256, 32>(a, grid, go);
-  if ((int64_t)pages->width * pages->page > (int64_t)kLatentLeast * kLatentTile) {
-    const JoinArgs j{a.split.pieces, a.part, a.ml, a.out, lse, 2 * (int64_t)heads * rank, 2 * rank, lse_b, heads};
-    const dim3 jg((unsigned)heads, (unsigned)batch), jb(64 * kJoinWaves);
-    rank == 512 ? go(join_kernel<512, true>, jg, jb, 0, j) : go(join_kernel<256, true>, jg, jb, 0, j);
-  }
-  const HeadsArgs up{mean, (const char*)w + 2 * (int64_t)nope * rank, (uint16_t*)out, 4 * (int64_t)heads * rank, 4 * rank, 4 * (int64_t)nope * rank,
-                     out_b, out_h, (int32_t)batch, heads, rank, nope};
-  go(heads_product_kernel<false>, dim3((unsigned)nope / 16, (unsigned)heads, tiles), dim3(64), 0, up);
+  rank == 512 ? launch_join<512>(a, go) : launch_join<256>(a, go);
+  const ValuesArgs up{(const char*)a.mean, (const char*)w + 2 * (int64_t)nope * rank, (uint16_t*)out, 4 * (int64_t)nope * rank, out_b, out_h, (int32_t)batch, heads};
+  const dim3 ug((unsigned)heads, (b_tiles + kValueTiles - 1) / kValueTiles);
+  if (rank == 512) nope == 128 ? go(values_product_kernel<512, 128>, ug, dim3(512), values_lds(512), up) : go(values_product_kernel<512, 64>, ug, dim3(256), values_lds(512), up);
+  else nope == 128 ? go(values_product_kernel<256, 128>, ug, dim3(512), values_lds(256), up) : go(values_product_kernel<256, 64>, ug, dim3(256), values_lds(256), up);
   return go.status();
 }
 

@@ -140,7 +140,8 @@ struct BlockList {
     at = (int32_t)(t - i * s.page);
     page = i < s.width ? s.table[b * s.ldt + i] : -1;
   }
-  __device__ __forceinline__ Blocks get(const SplitArgs& s, const Piece& p, int block) const {
+  template <class P>
+  __device__ __forceinline__ Blocks get(const SplitArgs& s, const P& p, int block) const {
     Blocks x;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -181,198 +182,201 @@ __global__ __launch_bounds__(64 * kPagedWaves) void paged_kernel(PagedArgs a) {
   __shared__ SplitShared sh;
   __shared__ float top[W][16 * HT], sum[W][16 * HT];
   __shared__ float red[W][16][DP + 4];
-  Piece p;
-  if (!find_piece<64 * W, kPagedUnit>(a.split, blockIdx.x, sh, p)) return;
+  Pieces<kPagedUnit> p;
+  if (!p.template find<64 * W>(a.split, blockIdx.x, sh)) return;
   const int lane = threadIdx.x & 63, m = lane & 15, quarter = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tiles = (a.group + 16 * HT - 1) / (16 * HT), h = blockIdx.y / tiles, head0 = 16 * HT * (blockIdx.y % tiles);
-  bf16x8 q[HT][KS];
+  do {
+    bf16x8 q[HT][KS];
 #pragma unroll
-  for (int t = 0; t < HT; ++t) {
-    const int i = head0 + 16 * t + m;
-    const char* row = a.q + p.b * a.q_b + (h * a.group + min(i, a.group - 1)) * a.q_h;
+    for (int t = 0; t < HT; ++t) {
+      const int i = head0 + 16 * t + m;
+      const char* row = a.q + p.b * a.q_b + (h * a.group + min(i, a.group - 1)) * a.q_h;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      u32x4 w = *(const u32x4*)(row + 2 * Tile::q_dim(s, quarter));
-      if (i >= a.group) w = u32x4{0u, 0u, 0u, 0u};
-      q[t][s] = __builtin_bit_cast(bf16x8, w);
-    }
-  }
-  f32x4 o[HT][NV];
-  float top_m[HT], l[HT];
-#pragma unroll
-  for (int t = 0; t < HT; ++t) {
-    top_m[t] = kNone;
-    l[t] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) o[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-  // this wave's tiles of 32 tokens
-  const int block0 = p.begin / 16, n = (p.end - p.begin + 31) / 32, t0 = n * wave / W, t1 = n * (wave + 1) / W;
-  Tile x;
-  BlockList list;
-  Blocks now, next;
-  auto place = [&](int t) {
-    const int block = block0 + 2 * t;
-    if (t == t0 || block - list.block0 >= 64) list.fetch(a.split, p.b, block, lane);
-    return list.get(a.split, p, block);
-  };
-  if (t0 < t1) {
-    now = place(t0);
-    x.load_k(a, now, h, m, quarter);
-  }
-  for (int t = t0; t < t1; ++t) {
-    x.load_v(a, now, h, m, quarter);
-    f32x4 s[HT][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-      for (int ht = 0; ht < HT; ++ht) s[ht][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const bf16x8 key = x.key(i, ks);
-#pragma unroll
-        for (int ht = 0; ht < HT; ++ht) s[ht][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(key, q[ht][ks], s[ht][i], 0, 0, 0);
+      for (int s = 0; s < KS; ++s) {
+        u32x4 w = *(const u32x4*)(row + 2 * Tile::q_dim(s, quarter));
+        if (i >= a.group) w = u32x4{0u, 0u, 0u, 0u};
+        q[t][s] = __builtin_bit_cast(bf16x8, w);
       }
-#pragma unroll
-      for (int ht = 0; ht < HT; ++ht)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) s[ht][i][r] *= E4M3 ? a.c * x.ks[i][r] : a.c;
     }
-    const bool full = now.full();
-    if (t + 1 < t1) {
-      next = place(t + 1);
-      x.load_k(a, next, h, m, quarter);
+    f32x4 o[HT][NV];
+    float top_m[HT], l[HT];
+#pragma unroll
+    for (int t = 0; t < HT; ++t) {
+      top_m[t] = kNone;
+      l[t] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) o[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    if (!full) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int at = 4 * quarter + r;
-          const bool seen = at >= now.lo[i] && at < now.hi[i];
-#pragma unroll
-          for (int ht = 0; ht < HT; ++ht) s[ht][i][r] = seen ? s[ht][i][r] : kNone;
-          // a weight of zero does not take out a NaN or an infinity
-#pragma unroll
-          for (int w = 0; w < Tile::VW; ++w) x.v[4 * i + r][w] = seen ? x.v[4 * i + r][w] : 0u;
-          if constexpr (E4M3) x.vs[i][r] = seen ? x.vs[i][r] : 0.0f;
-        }
+    // this wave's tiles of 32 tokens
+    const int block0 = p.begin / 16, n = (p.end - p.begin + 31) / 32, t0 = n * wave / W, t1 = n * (wave + 1) / W;
+    Tile x;
+    BlockList list;
+    Blocks now, next;
+    auto place = [&](int t) {
+      const int block = block0 + 2 * t;
+      if (t == t0 || block - list.block0 >= 64) list.fetch(a.split, p.b, block, lane);
+      return list.get(a.split, p, block);
+    };
+    if (t0 < t1) {
+      now = place(t0);
+      x.load_k(a, now, h, m, quarter);
     }
-    bf16x8 w[HT];
-#pragma unroll
-    for (int ht = 0; ht < HT; ++ht) {
-      float high = s[ht][0][0];
-#pragma unroll
-      for (int r = 1; r < 8; ++r) high = fmaxf(high, s[ht][r / 4][r % 4]);
-      if (__any(high > top_m[ht] + kSlack)) {
-        const float up = fmaxf(top_m[ht], quarters_max(high));
-        const float f = top_m[ht] == kNone ? 0.0f : exp2f(top_m[ht] - up);
-        top_m[ht] = up;
-        l[ht] *= f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) o[ht][j] *= f;
-      }
-      const float at = top_m[ht] == kNone ? 0.0f : top_m[ht];
-      u32x4 pk;
+    for (int t = t0; t < t1; ++t) {
+      x.load_v(a, now, h, m, quarter);
+      f32x4 s[HT][2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float e[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          e[r] = __builtin_amdgcn_exp2f(s[ht][i][r] - at);
-          l[ht] += e[r];
-          if constexpr (E4M3) e[r] *= x.vs[i][r];
+        for (int ht = 0; ht < HT; ++ht) s[ht][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const bf16x8 key = x.key(i, ks);
+#pragma unroll
+          for (int ht = 0; ht < HT; ++ht) s[ht][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(key, q[ht][ks], s[ht][i], 0, 0, 0);
         }
-        pk[2 * i] = f2_bf16(e[0], e[1]);
-        pk[2 * i + 1] = f2_bf16(e[2], e[3]);
-      }
-      w[ht] = __builtin_bit_cast(bf16x8, pk);
-    }
 #pragma unroll
-    for (int j = 0; j < NV; j += 2) {
-      bf16x8 va, vb;
-      x.values(j, va, vb);
+        for (int ht = 0; ht < HT; ++ht)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s[ht][i][r] *= E4M3 ? a.c * x.ks[i][r] : a.c;
+      }
+      const bool full = now.full();
+      if (t + 1 < t1) {
+        next = place(t + 1);
+        x.load_k(a, next, h, m, quarter);
+      }
+      if (!full) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int at = 4 * quarter + r;
+            const bool seen = at >= now.lo[i] && at < now.hi[i];
+#pragma unroll
+            for (int ht = 0; ht < HT; ++ht) s[ht][i][r] = seen ? s[ht][i][r] : kNone;
+            // a weight of zero does not take out a NaN or an infinity
+#pragma unroll
+            for (int w = 0; w < Tile::VW; ++w) x.v[4 * i + r][w] = seen ? x.v[4 * i + r][w] : 0u;
+            if constexpr (E4M3) x.vs[i][r] = seen ? x.vs[i][r] : 0.0f;
+          }
+      }
+      bf16x8 w[HT];
 #pragma unroll
       for (int ht = 0; ht < HT; ++ht) {
-        o[ht][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, w[ht], o[ht][j], 0, 0, 0);
-        o[ht][j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, w[ht], o[ht][j + 1], 0, 0, 0);
+        float high = s[ht][0][0];
+#pragma unroll
+        for (int r = 1; r < 8; ++r) high = fmaxf(high, s[ht][r / 4][r % 4]);
+        if (__any(high > top_m[ht] + kSlack)) {
+          const float up = fmaxf(top_m[ht], quarters_max(high));
+          const float f = top_m[ht] == kNone ? 0.0f : exp2f(top_m[ht] - up);
+          top_m[ht] = up;
+          l[ht] *= f;
+#pragma unroll
+          for (int j = 0; j < NV; ++j) o[ht][j] *= f;
+        }
+        const float at = top_m[ht] == kNone ? 0.0f : top_m[ht];
+        u32x4 pk;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float e[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            e[r] = __builtin_amdgcn_exp2f(s[ht][i][r] - at);
+            l[ht] += e[r];
+            if constexpr (E4M3) e[r] *= x.vs[i][r];
+          }
+          pk[2 * i] = f2_bf16(e[0], e[1]);
+          pk[2 * i + 1] = f2_bf16(e[2], e[3]);
+        }
+        w[ht] = __builtin_bit_cast(bf16x8, pk);
+      }
+#pragma unroll
+      for (int j = 0; j < NV; j += 2) {
+        bf16x8 va, vb;
+        x.values(j, va, vb);
+#pragma unroll
+        for (int ht = 0; ht < HT; ++ht) {
+          o[ht][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, w[ht], o[ht][j], 0, 0, 0);
+          o[ht][j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, w[ht], o[ht][j + 1], 0, 0, 0);
+        }
+      }
+      now = next;
+    }
+    // the waves' sums, in wave order
+#pragma unroll
+    for (int ht = 0; ht < HT; ++ht) {
+      const float all = quarters_sum(l[ht]);
+      if (quarter == 0) {
+        // scores of NaN alone: not "nothing seen"
+        top[wave][16 * ht + m] = top_m[ht] == kNone && all != 0.0f ? 0.0f : top_m[ht];
+        sum[wave][16 * ht + m] = all;
       }
     }
-    now = next;
-  }
-  // the waves' sums, in wave order
 #pragma unroll
-  for (int ht = 0; ht < HT; ++ht) {
-    const float all = quarters_sum(l[ht]);
-    if (quarter == 0) {
-      // scores of NaN alone: not "nothing seen"
-      top[wave][16 * ht + m] = top_m[ht] == kNone && all != 0.0f ? 0.0f : top_m[ht];
-      sum[wave][16 * ht + m] = all;
-    }
-  }
+    for (int ht = 0; ht < HT; ++ht) {
 #pragma unroll
-  for (int ht = 0; ht < HT; ++ht) {
+      for (int d0 = 0; d0 < D; d0 += DP) {
+        // D / DP lanes' columns at a time: lane rows of the result hold dims NV row + j
+        __syncthreads();
 #pragma unroll
-    for (int d0 = 0; d0 < D; d0 += DP) {
-      // D / DP lanes' columns at a time: lane rows of the result hold dims NV row + j
-      __syncthreads();
+        for (int r = 0; r < 4; ++r) {
+          const int row = 4 * quarter + r;
+          if (NV * row < d0 || NV * row >= d0 + DP) continue;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 4 * quarter + r;
-        if (NV * row < d0 || NV * row >= d0 + DP) continue;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) red[wave][m][NV * row - d0 + j] = o[ht][j][r];
-      }
-      __syncthreads();
-      const int hd = threadIdx.x >> 4, i = head0 + 16 * ht + hd;           // 16 threads a head
-      if (i < a.group) {
-        float t = kNone;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-          const float u = top[w][16 * ht + hd];
-          t = u > t || u != u ? u : t;
+          for (int j = 0; j < NV; ++j) red[wave][m][NV * row - d0 + j] = o[ht][j][r];
         }
-        float f[W], all = 0.0f;
+        __syncthreads();
+        const int hd = threadIdx.x >> 4, i = head0 + 16 * ht + hd;           // 16 threads a head
+        if (i < a.group) {
+          float t = kNone;
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-          const float u = top[w][16 * ht + hd];
-          f[w] = u == kNone ? 0.0f : exp2f(u - t);
-          all = __builtin_fmaf(f[w], sum[w][16 * ht + hd], all);
-        }
-        constexpr int C = DP / 16;
-        const int c0 = C * (threadIdx.x & 15), hh = h * a.group + i;
-        const bool last = p.count == 1;
-        const float inv = !last ? 1.0f : all == 0.0f ? 0.0f : 1.0f / all;
+          for (int w = 0; w < W; ++w) {
+            const float u = top[w][16 * ht + hd];
+            t = u > t || u != u ? u : t;
+          }
+          float f[W], all = 0.0f;
 #pragma unroll
-        for (int j = 0; j < C; j += 2) {
-          float y[2] = {0.0f, 0.0f};
+          for (int w = 0; w < W; ++w) {
+            const float u = top[w][16 * ht + hd];
+            f[w] = u == kNone ? 0.0f : exp2f(u - t);
+            all = __builtin_fmaf(f[w], sum[w][16 * ht + hd], all);
+          }
+          constexpr int C = DP / 16;
+          const int c0 = C * (threadIdx.x & 15), hh = h * a.group + i;
+          const bool last = p.count == 1;
+          const float inv = !last ? 1.0f : all == 0.0f ? 0.0f : 1.0f / all;
 #pragma unroll
-          for (int w = 0; w < W; ++w)
+          for (int j = 0; j < C; j += 2) {
+            float y[2] = {0.0f, 0.0f};
 #pragma unroll
-            for (int k = 0; k < 2; ++k) y[k] = __builtin_fmaf(f[w], red[w][hd][c0 + j + k], y[k]);
-          if (last) {
-            uint16_t* to = a.out + p.b * a.out_b + hh * a.out_h + d0 + c0 + j;
-            to[0] = f_bf16(y[0] * inv);
-            to[1] = f_bf16(y[1] * inv);
-          } else {
-            float* to = a.part + ((int64_t)p.item * a.heads + hh) * D + d0 + c0 + j;
-            to[0] = y[0];
-            to[1] = y[1];
+            for (int w = 0; w < W; ++w)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) y[k] = __builtin_fmaf(f[w], red[w][hd][c0 + j + k], y[k]);
+            if (last) {
+              uint16_t* to = a.out + p.b * a.out_b + hh * a.out_h + d0 + c0 + j;
+              to[0] = f_bf16(y[0] * inv);
+              to[1] = f_bf16(y[1] * inv);
+            } else {
+              float* to = a.part + ((int64_t)p.place * a.heads + hh) * D + d0 + c0 + j;
+              to[0] = y[0];
+              to[1] = y[1];
+            }
+          }
+          if ((threadIdx.x & 15) == 0 && d0 == 0) {
+            if (last) {
+              if (a.lse) a.lse[p.b * a.lse_b + hh] = all == 0.0f ? kNone : (t + log2f(all)) / kLog2E;
+            } else {
+              float* to = a.ml + 2 * ((int64_t)p.place * a.heads + hh);
+              to[0] = t;
+              to[1] = all;
+            }
           }
         }
-        if ((threadIdx.x & 15) == 0 && d0 == 0) {
-          if (last) {
-            if (a.lse) a.lse[p.b * a.lse_b + hh] = all == 0.0f ? kNone : (t + log2f(all)) / kLog2E;
-          } else {
-            float* to = a.ml + 2 * ((int64_t)p.item * a.heads + hh);
-            to[0] = t;
-            to[1] = all;
-          }
-        }
       }
     }
-  }
+    __syncthreads();                   // top, sum and red have been read
+  } while (p.next(a.split, threadIdx.x));
 }
 
 }  // namespace ops

@@ -1,14 +1,17 @@
 // Work of attention over a paged cache, split over the cache's length.
 //
-// The lengths are on the GPU, so the split is made there: a request's tokens are cut
-// into pieces of about (all tokens) / target, at least `least` units of U tokens,
-// and item i of the grid is the i-th piece of all requests. Every workgroup finds its
-// own from the lengths by two sums over them, which takes less than a launch. A
-// request without tokens has one empty piece, so that its outputs are written too.
-// Pieces of one request that has several leave their sums (running maximum, sum of
-// weights, weighted sum) in the workspace, and join_kernel adds them up in order.
+// The lengths are on the GPU, so the split is made there: the requests' tokens, in
+// units of U, stand one after the other, and every workgroup takes an equal number of
+// consecutive ones, be they part of one request or of many. All workgroups then have the same work whatever the lengths (pieces of one request each,
+// cut as evenly as 64 uneven lengths allow, left a latent cache's workgroups 30 %
+// of the time without any). Every workgroup finds its own units from the lengths by sums
+// over them, which takes less than a launch. A request without tokens counts as one unit, so
+// that its outputs are written too. Pieces of one request that has several leave their
+// sums (running maximum, sum of weights, weighted sum) in the workspace at place w + request, which no other
+// piece has and which is consecutive for a request; join_kernel adds them up in order.
 #pragma once
 
+#include "fg_entry.hpp"
 #include "fg_ops.hpp"
 
 namespace fg {
@@ -26,19 +29,12 @@ struct SplitArgs {
   int64_t ldt;                       // entries
   int32_t batch, width, n_pages, page;
   int32_t window;                    // 0: all tokens
-  int32_t target, least;
-  int32_t* pieces;                   // workspace: {first item, number of items} of every request
-};
-
-struct Piece {
-  int b;
-  int begin, end;                    // tokens, begin a multiple of 16 (of 64 without a window)
-  int first, len;                    // first token that is seen, tokens of the request
-  int item, count;                   // place among all items; pieces of this request
+  int32_t target, least;             // workgroups; units that one has at least where there are few
+  int32_t* pieces;                   // workspace: {first place, number of pieces} of every request
 };
 
 struct SplitShared {
-  int32_t sum[16], found[4];
+  int32_t sum[16], found[2];
 };
 
 __device__ __forceinline__ int seen_tokens(const SplitArgs& a, int b, int& first) {
@@ -48,65 +44,95 @@ __device__ __forceinline__ int seen_tokens(const SplitArgs& a, int b, int& first
   first = a.window > 0 && len > a.window ? len - a.window : 0;
   return len;
 }
-
-// Piece `item`; false if there are fewer. T threads, all of them call it.
-template <int T, int U>
-__device__ __forceinline__ bool find_piece(const SplitArgs& a, int item, SplitShared& sh, Piece& p) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int per = (a.batch + T - 1) / T, from = tid * per, to = min(from + per, a.batch);
-  auto units = [&](int b) {
-    int first;
-    const int len = seen_tokens(a, b, first);
-    return (len - (first & ~15) + U - 1) / U;
-  };
-  int mine = 0;
-  for (int b = from; b < to; ++b) mine += units(b);
-  int v = lanes_reduce<64>(mine, [](int x, int y) { return x + y; });
-  if (lane == 0) sh.sum[wave] = v;
-  if (tid == 0) sh.found[0] = -1;
-  __syncthreads();
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < T / 64; ++w) total += sh.sum[w];
-  const int piece = max(a.least, (total + a.target - 1) / a.target);
-  auto pieces = [&](int u) { return u <= piece ? 1 : (u + piece - 1) / piece; };
-  int count = 0;
-  for (int b = from; b < to; ++b) count += pieces(units(b));
-  int upto = lanes_before_and_own(count);
-  __syncthreads();
-  if (lane == 63) sh.sum[wave] = upto;
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) upto += sh.sum[w];
-  if (item < upto && item >= upto - count) {
-    int at = upto - count;
-    for (int b = from; b < to; ++b) {
-      const int n = pieces(units(b));
-      if (item < at + n) {
-        sh.found[0] = b;
-        sh.found[1] = at;
-        sh.found[2] = n;
-        break;
-      }
-      at += n;
-    }
-  }
-  __syncthreads();
-  p.b = __builtin_amdgcn_readfirstlane(sh.found[0]);
-  if (p.b < 0) return false;
-  const int first_item = __builtin_amdgcn_readfirstlane(sh.found[1]);
-  p.count = __builtin_amdgcn_readfirstlane(sh.found[2]);
-  p.item = item;
-  p.len = seen_tokens(a, p.b, p.first);
-  const int origin = p.first & ~15, u = (p.len - origin + U - 1) / U, k = item - first_item;
-  // pieces of one request differ by one unit at most
-  p.begin = origin + U * (int)((int64_t)u * k / p.count);
-  p.end = min(p.len, origin + U * (int)((int64_t)u * (k + 1) / p.count));
-  if (k == 0 && tid == 0 && blockIdx.y == 0) {
-    a.pieces[2 * p.b] = item;
-    a.pieces[2 * p.b + 1] = p.count;
-  }
-  return true;
+template <int U>
+__device__ __forceinline__ int units_of(const SplitArgs& a, int b) {
+  int first;
+  const int len = seen_tokens(a, b, first);
+  return max(1, (len - (first & ~15) + U - 1) / U);
 }
+
+// The pieces of one workgroup, one after the other.
+template <int U>
+struct Pieces {
+  int b;                             // request
+  int begin, end;                    // tokens, begin a multiple of 16 (of U without a window)
+  int first, len;                    // first token that is seen, tokens of the request
+  int place, count;                  // of this piece's sums; pieces of this request
+  int w, share, more;                // workgroup; its units, one more for the first `more` workgroups
+  int at, left, skip;                // units: before this request, still to do, of this request before this piece
+
+  __device__ __forceinline__ int owner(int unit) const {
+    const uint32_t u = unit, big = (uint32_t)more * (uint32_t)(share + 1);
+    return (int)(u < big ? u / (uint32_t)(share + 1) : more + (u - big) / (uint32_t)share);
+  }
+
+  // T threads, all of them call it; false: nothing to do. `w`: this workgroup's number.
+  template <int T>
+  __device__ __forceinline__ bool find(const SplitArgs& a, int w_, SplitShared& sh) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int per = (a.batch + T - 1) / T, from = min(tid * per, a.batch), to = min(from + per, a.batch);
+    int mine = 0;
+    for (int i = from; i < to; ++i) mine += units_of<U>(a, i);
+    int upto = lanes_before_and_own(mine);
+    if (lane == 63) sh.sum[wave] = upto;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int i = 0; i < T / 64; ++i) {
+      if (i < wave) upto += sh.sum[i];
+      total += sh.sum[i];
+    }
+    total = __builtin_amdgcn_readfirstlane(total);
+    w = w_;
+    const int n = min(a.target, (total + a.least - 1) / a.least);
+    if (w >= n) return false;
+    share = total / n;
+    more = total - n * share;
+    const int start = w * share + min(w, more);
+    if (start < upto && start >= upto - mine) {
+      int before = upto - mine;
+      for (int i = from; i < to; ++i) {
+        const int u = units_of<U>(a, i);
+        if (start < before + u) {
+          sh.found[0] = i;
+          sh.found[1] = before;
+          break;
+        }
+        before += u;
+      }
+    }
+    __syncthreads();
+    b = __builtin_amdgcn_readfirstlane(sh.found[0]);
+    at = __builtin_amdgcn_readfirstlane(sh.found[1]);
+    left = share + (w < more ? 1 : 0);
+    skip = start - at;
+    take(a, tid);
+    return true;
+  }
+  __device__ __forceinline__ void take(const SplitArgs& a, int tid) {
+    len = __builtin_amdgcn_readfirstlane(seen_tokens(a, b, first));
+    first = __builtin_amdgcn_readfirstlane(first);
+    const int origin = first & ~15, u = max(1, (len - origin + U - 1) / U), mine = min(left, u - skip);
+    begin = origin + U * skip;
+    end = min(len, begin + U * mine);
+    const int w0 = owner(at), w1 = owner(at + u - 1);
+    place = w + b;
+    count = w1 - w0 + 1;
+    if (skip == 0 && tid == 0) {
+      a.pieces[2 * b] = place;
+      a.pieces[2 * b + 1] = count;
+    }
+    left -= mine;
+    at += u;
+    skip = 0;
+  }
+  __device__ __forceinline__ bool next(const SplitArgs& a, int tid) {
+    if (left == 0) return false;
+    ++b;
+    take(a, tid);
+    return true;
+  }
+};
 
 // v as the sum of two bf16 numbers, within 2^-16 of it: the first is v rounded, this the rest (none beside an infinity).
 __device__ __forceinline__ float bf16_rest(float v) {
@@ -114,87 +140,107 @@ __device__ __forceinline__ float bf16_rest(float v) {
   return fabsf(hi) < __builtin_inff() ? v - hi : 0.0f;
 }
 
-// Sum of a head's pieces: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i, in order. A workgroup has one request and head; its
-// waves take every 8th piece, a lane D / 64 columns. Bound by the latency of two rounds of loads. PAIR: the result as two bf16 numbers
-// D apart.
+// Sum of a head's pieces: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i, in order. A wave has C columns of one request and head and
+// asks for 16 pieces at once. Where a request may have more pieces than that, K waves share them and other columns are other
+// workgroups', since one compute unit takes long for a row's megabyte (16 heads of 256 pieces and 512 columns: 16 workgroups 19.7 us, 128 of
+// them 5.6). A request of one piece has been written by it.
 struct JoinArgs {
   const int32_t* pieces;
-  const float* part;                 // [items][heads][D]
-  const float* ml;                   // [items][heads][2]: maximum (base 2), sum of weights
+  const float* part;                 // [places][heads][D]
+  const float* ml;                   // [places][heads][2]: maximum (base 2), sum of weights
   uint16_t* out;
   float* lse;                        // or null
   int64_t out_b, out_h, lse_b;       // elements
   int32_t heads;
 };
 
-constexpr int kJoinWaves = 8;
-template <int D, bool PAIR>
-__global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(JoinArgs a) {
-  constexpr int N = D / 64;
-  __shared__ float red[kJoinWaves][D], top[kJoinWaves], sum[kJoinWaves];
+template <int D, bool MANY>
+struct JoinShape {
+  static constexpr int K = MANY ? 8 : 1, C = MANY || D < 128 ? 64 : 128;
+  static constexpr int PARTS = D / C;                          // of a row's columns: workgroups, or waves of one
+  static constexpr int WAVES = MANY ? K : PARTS, Z = MANY ? PARTS : 1;
+};
+template <int D, bool MANY>
+__global__ __launch_bounds__((64 * JoinShape<D, MANY>::WAVES)) void join_kernel(JoinArgs a) {
+  typedef JoinShape<D, MANY> Sh;
+  constexpr int K = Sh::K, C = Sh::C, N = C / 64, B = 16;
+  __shared__ float red[K][C], top[K], sum[K];
   const int b = blockIdx.y, h = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int k = MANY ? wave : 0, col = C * (MANY ? blockIdx.z : wave) + N * lane;
   const int first = a.pieces[2 * b], n = a.pieces[2 * b + 1];
-  if (n < 2) return;                 // written by its only piece
-  float m = kNone, l = 0.0f, o[N];
-#pragma unroll
-  for (int j = 0; j < N; ++j) o[j] = 0.0f;
-  constexpr int B = 8;               // loads of eight pieces at once
-  for (int i = wave; i < n; i += kJoinWaves * B) {
+  if (n < 2) return;
+  float m = kNone, l = 0.0f, o[N] = {};
+  for (int i = k; i < n; i += K * B) {
     float pm[B], pl[B], po[B][N];
 #pragma unroll
-    for (int k = 0; k < B; ++k) {
-      const int at = i + k * kJoinWaves;
+    for (int j = 0; j < B; ++j) {
+      const int at = i + j * K;
       const int64_t row = (int64_t)(first + (at < n ? at : i)) * a.heads + h;
-      pm[k] = at < n ? a.ml[2 * row] : kNone;
-      pl[k] = a.ml[2 * row + 1];
+      const float2 v = *(const float2*)(a.ml + 2 * row);
+      pm[j] = at < n ? v.x : kNone;
+      pl[j] = v.y;
 #pragma unroll
-      for (int j = 0; j < N; ++j) po[k][j] = a.part[row * D + N * lane + j];
+      for (int e = 0; e < N; ++e) po[j][e] = a.part[row * D + col + e];
     }
     float t = m;
 #pragma unroll
-    for (int k = 0; k < B; ++k) t = pm[k] > t || pm[k] != pm[k] ? pm[k] : t;
+    for (int j = 0; j < B; ++j) t = pm[j] > t || pm[j] != pm[j] ? pm[j] : t;
     if (t == kNone) continue;
     const float f = exp2f(m - t);
     l *= f;
 #pragma unroll
-    for (int j = 0; j < N; ++j) o[j] *= f;
+    for (int e = 0; e < N; ++e) o[e] *= f;
 #pragma unroll
-    for (int k = 0; k < B; ++k) {
-      if (pm[k] == kNone) continue;
-      const float g = exp2f(pm[k] - t);
-      l = __builtin_fmaf(g, pl[k], l);
+    for (int j = 0; j < B; ++j) {
+      if (pm[j] == kNone) continue;
+      const float g = exp2f(pm[j] - t);
+      l = __builtin_fmaf(g, pl[j], l);
 #pragma unroll
-      for (int j = 0; j < N; ++j) o[j] = __builtin_fmaf(g, po[k][j], o[j]);
+      for (int e = 0; e < N; ++e) o[e] = __builtin_fmaf(g, po[j][e], o[e]);
     }
     m = t;
   }
-  if (lane == 0) {
-    top[wave] = m;
-    sum[wave] = l;
+  if constexpr (K > 1) {
+    if (lane == 0) {
+      top[k] = m;
+      sum[k] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) red[k][N * lane + e] = o[e];
+    __syncthreads();
+    if (k != 0) return;
+    float t = kNone;
+#pragma unroll
+    for (int w = 0; w < K; ++w) t = top[w] > t || top[w] != top[w] ? top[w] : t;
+    m = t;
+    l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < K; ++w) {
+      if (top[w] == kNone) continue;
+      const float g = exp2f(top[w] - t);
+      l = __builtin_fmaf(g, sum[w], l);
+#pragma unroll
+      for (int e = 0; e < N; ++e) o[e] = __builtin_fmaf(g, red[w][N * lane + e], o[e]);
+    }
   }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint16_t* to = a.out + b * a.out_b + h * a.out_h + col;
 #pragma unroll
-  for (int j = 0; j < N; ++j) red[wave][N * lane + j] = o[j];
-  __syncthreads();
-  float t = kNone;
-#pragma unroll
-  for (int w = 0; w < kJoinWaves; ++w) t = top[w] > t || top[w] != top[w] ? top[w] : t;
-  float all = 0.0f, g[kJoinWaves];
-#pragma unroll
-  for (int w = 0; w < kJoinWaves; ++w) {
-    g[w] = top[w] == kNone ? 0.0f : exp2f(top[w] - t);
-    all = __builtin_fmaf(g[w], sum[w], all);
-  }
-  const float inv = all == 0.0f ? 0.0f : 1.0f / all;
-  for (int d = threadIdx.x; d < D; d += 64 * kJoinWaves) {
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kJoinWaves; ++w)
-      if (top[w] != kNone) v = __builtin_fmaf(g[w], red[w][d], v);
-    uint16_t* to = a.out + b * a.out_b + h * a.out_h + d;
-    to[0] = f_bf16(v * inv);
-    if constexpr (PAIR) to[D] = f_bf16(bf16_rest(v * inv));
-  }
-  if (a.lse && threadIdx.x == 0) a.lse[b * a.lse_b + h] = all == 0.0f ? kNone : (t + log2f(all)) / kLog2E;
+  for (int e = 0; e < N; ++e) to[e] = f_bf16(o[e] * inv);
+  if (a.lse && col == 0) a.lse[b * a.lse_b + h] = l == 0.0f ? kNone : (m + log2f(l)) / kLog2E;
+}
+
+// MANY where requests have more than 16 pieces if their lengths are even.
+template <int D, bool MANY>
+void launch_join_as(const JoinArgs& a, int64_t batch, Launches& go) {
+  typedef JoinShape<D, MANY> Sh;
+  go(join_kernel<D, MANY>, dim3((unsigned)a.heads, (unsigned)batch, Sh::Z), dim3(64 * Sh::WAVES), 0, a);
+}
+template <int D>
+void launch_join(const JoinArgs& a, int64_t batch, int target, Launches& go) {
+  target > 16 * batch ? launch_join_as<D, true>(a, batch, go) : launch_join_as<D, false>(a, batch, go);
 }
 
 }  // namespace ops
