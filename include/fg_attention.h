@@ -100,7 +100,7 @@ typedef struct {
  *   k, v:   bf16 or e4m3 [n_pages][page][kv][dim], rows on 16-byte boundaries, strides multiples of 8 (16 for e4m3);
  *           16 rows of a page are less than 2^31 bytes apart
  *   scales: fp32 [n_pages][kv][page] for e4m3 (the code times its scale is the value), 16-byte aligned
- *   dim 64, 128 or 256; scale > 0; width * page < 2^31
+ *   dim 64, 128 or 256; scale > 0; width * page < 2^31, batch * width * page < 2^38 - 2^9 * batch
  *   out:    bf16 [batch][kv * group][dim], rows consecutive (out_b, out_h >= dim);  lse: fp32 [batch][kv * group] or NULL
  *   workspace: fg_paged_attention_bytes, 16-byte aligned, contents free; calls that may overlap need one each */
 typedef struct {
@@ -125,7 +125,8 @@ fg_status fg_paged_attention(const void* q, int64_t q_b, int64_t q_h, const fg_c
  * weighted mean of c. W_k^T q_nope is rounded to bf16 before its product;
  * the mean is held as two bf16 numbers, within 2^-16.
  *   q:      bf16 [batch][heads][nope + rope], rows on 16-byte boundaries
- *   cache:  bf16 [n_pages][page][rank + rope] rows on 16-byte boundaries (strides multiples of 8, 16 rows less than 2^31 bytes apart)
+ *   cache:  bf16 [n_pages][page][rank + rope] rows on 16-byte boundaries (strides multiples of 8, 16 rows less than 2^31 bytes apart);
+ *           width * page < 2^31, batch * width * page < 2^36 - 2^7 * batch
  *   out:    bf16 [batch][heads][nope];  lse: fp32 [batch][heads] or NULL
  *   workspace: fg_latent_attention_bytes, 16-byte aligned */
 fg_status fg_latent_attention_bytes(int32_t batch, int32_t heads, int32_t rank, int64_t* bytes);
@@ -139,7 +140,7 @@ fg_status fg_latent_attention(const void* q, int64_t q_b, int64_t q_h, const voi
  * k_starts[b]..k_starts[b + 1]-1; query i of nq sees keys 0..nk - nq + i of nk. Keys and values are
  * formed once, rounded to bf16, in the workspace. A NaN or an infinity in a row that a query does not see does not reach it.
  *   q:      bf16 [q_rows][heads][nope + rope], rows on 16-byte boundaries
- *   latent: bf16 [k_rows][ld], rank + rope columns, rows on 16-byte boundaries
+ *   latent: bf16 [k_rows][ld], rank + rope columns, rows on 16-byte boundaries, less than 2^24 bytes apart
  *   starts: int32 [batch + 1], not falling; rows outside 0..q_rows-1, 0..k_rows-1 are left out
  *   out:    bf16 [q_rows][heads][nope], strides multiples of 4, 8-byte aligned; rows of no request are left as they were
  *   lse:    fp32 [q_rows][heads] or NULL

@@ -30,7 +30,6 @@ int latent_target(int32_t heads) {
   const int64_t t = kCUs * (64 / latent_tile(heads)) / head_parts(heads);
   return (int)(t < 1 ? 1 : t);
 }
-constexpr int kLatentLeast = 2;
 
 template <int R, int P, int G, int HW>
 void launch_latent(const LatentArgs& a, dim3 grid, Launches& go) {
@@ -87,6 +86,7 @@ fg_status fg_latent_attention(const void* q, int64_t q_b, int64_t q_h, const voi
       (int64_t)pages->width * pages->page > kMax)
     return FG_EINVAL;
   const int64_t batch = pages->batch, parts = head_parts(heads);
+  // units of all requests are counted in 32 bits
   if (batch * ((int64_t)pages->width * pages->page / 32 + 2) > kMax) return FG_EINVAL;
   if (batch == 0) return FG_OK;
   if (!q || !w || !cache || !pages->table || !pages->lens || !out || !workspace || workspace_bytes < need) return FG_EINVAL;
@@ -113,7 +113,7 @@ fg_status fg_latent_attention(const void* q, int64_t q_b, int64_t q_h, const voi
   at += places * tiles * 128;
   a.mean = (uint16_t*)at;
   at += batch * heads * 4 * rank;
-  a.split = SplitArgs{pages->lens, pages->table, pages->ldt, pages->batch, pages->width, pages->n_pages, pages->page, 0, latent_target(heads), kLatentLeast,
+  a.split = SplitArgs{pages->lens, pages->table, pages->ldt, pages->batch, pages->width, pages->n_pages, pages->page, 0, latent_target(heads),
                       (int32_t*)at};
   a.a = absorbed;
   a.cache = (const char*)cache;
@@ -154,7 +154,7 @@ fg_status fg_latent_prompt(const void* q, int64_t q_t, int64_t q_h, const int32_
   if (!aligned(q, 16) || !aligned(latent, 16) || !aligned(w, 16) || !aligned(q_starts, 4) || !aligned(k_starts, 4) || !aligned(out, 8) || !aligned(lse, 4) ||
       !aligned(workspace, 16))
     return FG_EINVAL;
-  if (!multiple(q_t, 8) || !multiple(q_h, 8) || !multiple(ld, 8) || (k_rows > 1 && ld < rank + rope) || !multiple(out_t, 4) || !multiple(out_h, 4) ||
+  if (!multiple(q_t, 8) || !multiple(q_h, 8) || !multiple(ld, 8) || (k_rows > 1 && ld < rank + rope) || 2 * ld >= 1 << 24 || !multiple(out_t, 4) || !multiple(out_h, 4) ||
       (lse && lse_t < heads && q_rows > 1))
     return FG_EINVAL;
   if (!distinct({{q_rows, out_t}, {heads, out_h}, {nope, 1}})) return FG_EINVAL;
@@ -169,7 +169,7 @@ fg_status fg_latent_prompt(const void* q, int64_t q_t, int64_t q_h, const int32_
   Launches go{stream};
   if (k_rows) {
     const ExpandArgs e{(const char*)latent, (const char*)w, (uint16_t*)workspace, 2 * ld, k_rows, (int32_t)n, rank};
-    go(expand_kernel, dim3((unsigned)(n / kExpandTile), (unsigned)((k_rows + kExpandTile - 1) / kExpandTile)), dim3(256), 4 * kExpandTile * 128, e);
+    go(expand_kernel, dim3((unsigned)(n / kExpandTile), (unsigned)((k_rows + kExpandTile - 1) / kExpandTile)), dim3(256), kExpandStages * kExpandStage, e);
   }
   PromptArgs a{};
   a.q = (const char*)q; a.kv = (const char*)workspace; a.lat = (const char*)latent; a.out = (uint16_t*)out; a.lse = lse;

@@ -102,7 +102,7 @@ __device__ __forceinline__ u32x2 read_turned(const char* from) {
 // 16 bytes a lane from base + off to LDS at `to`, 64 lanes side by side. In assembly, because the compiler lets transposing reads wait for every
 // direct load that it knows of; these have no result registers, and loads_barrier() waits for them. m0 has no other use in this kernel.
 __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, const char* to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)to),
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane((int)(uintptr_t)(__attribute__((address_space(3))) const char*)to)),
                "v"(off), "s"(base));
 }
 
@@ -420,8 +420,9 @@ __device__ __forceinline__ void latent_lse(const LatentArgs& a, int b, int head,
 template <int R, bool MANY>
 __global__ __launch_bounds__((64 * LatentJoinShape<R, MANY>::WAVES)) void latent_join_kernel(LatentArgs a) {
   constexpr int B = LatentJoinShape<R, MANY>::B, JW = MANY ? 1 : 8, K = MANY ? 32 : 1;
-  __shared__ f32x4 red[MANY ? K : 1][16];
-  __shared__ float tops[K][16], sums[K][16];
+  constexpr int W = MANY ? 8 : 1;
+  __shared__ f32x4 red[W][16];
+  __shared__ float tops[W][16], sums[W][16];
   __shared__ __attribute__((aligned(16))) uint16_t out[MANY ? 1 : 16][MANY ? 1 : 2 * R + 8];
   const int lane = threadIdx.x & 63, m = lane & 15, wave = threadIdx.x >> 6;
   const int b = blockIdx.y, tile16 = blockIdx.x, head = 16 * tile16 + m;
@@ -464,18 +465,26 @@ __global__ __launch_bounds__((64 * LatentJoinShape<R, MANY>::WAVES)) void latent
     top = t;
   }
   if constexpr (MANY) {
-    tops[k][m] = top;
-    sums[k][m] = l;
-    red[k][m] = o[0];
+    // the wave's four parts, then the waves, in order
+    const float most = quarters_max(top), w4 = top == kNone ? 0.0f : exp2f(top - most);
+    l = quarters_sum(top == kNone ? 0.0f : l * w4);
+    f32x4 y;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) y[r] = quarters_sum(top == kNone ? 0.0f : o[0][r] * w4);
+    if (lane < 16) {
+      tops[wave][m] = most;
+      sums[wave][m] = l;
+      red[wave][m] = y;
+    }
     __syncthreads();
     if (threadIdx.x >= 16 || head >= a.heads) return;
     float t = kNone;
 #pragma unroll
-    for (int w = 0; w < K; ++w) t = tops[w][m] > t || tops[w][m] != tops[w][m] ? tops[w][m] : t;
+    for (int w = 0; w < W; ++w) t = tops[w][m] > t ? tops[w][m] : t;
     l = 0.0f;
-    f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+    y = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int w = 0; w < K; ++w) {
+    for (int w = 0; w < W; ++w) {
       if (tops[w][m] == kNone) continue;
       const float f = exp2f(tops[w][m] - t);
       l = __builtin_fmaf(f, sums[w][m], l);

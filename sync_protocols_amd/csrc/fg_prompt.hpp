@@ -24,8 +24,8 @@ namespace ops {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // ------------------------------------------------------------------- expand
-// kv[t][n] = bf16( sum_r lat[t][r] w[n][r] ), n over heads and their 2 M rows: 128 x 128 tiles, four waves of 64 x 64, 64 r at a time
-// through LDS by direct loads, two stages in turn.
+// kv[t][n] = bf16( sum_r lat[t][r] w[n][r] ), n over heads and their 2 M rows: 128 x 128 tiles, four waves of 64 x 64, 32 r at a time through LDS
+// by direct loads, four stages in turn, of which three are in flight (with two stages of 64 and one in flight 16384 x 4096 x 512 took 118 us).
 struct ExpandArgs {
   const char* lat;
   const char* w;
@@ -35,24 +35,30 @@ struct ExpandArgs {
   int32_t n, r;                      // n = heads * 2 M, any multiple of 128
 };
 
-constexpr int kExpandTile = 128;
+constexpr int kExpandTile = 128, kExpandStages = 4, kExpandStage = 2 * kExpandTile * 64;
 __global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = kExpandTile * blockIdx.x, wm = wave >> 1, wn = wave & 1;
   const int64_t t0 = (int64_t)kExpandTile * blockIdx.y;
-  constexpr int STAGE = kExpandTile * 128;       // bytes of 64 r of one operand
-  // 8 rows of 128 bytes a load; chunks permuted by the row's pair
-  auto load = [&](int k, char* to) {
+  const int left = (int)min((int64_t)kExpandTile, a.rows - t0) - 1;
+  // 16 rows of 64 bytes a load, two loads of each operand a wave; chunks permuted by the row's group of four, so that 16 rows differ in banks
+  const char* const lat = a.lat + t0 * a.ld;
+  const char* const w = a.w + 2 * (int64_t)n0 * a.r;
+  uint32_t at[2], wt[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 8 * (4 * wave + i) + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
-      const int64_t t = t0 + row < a.rows ? t0 + row : a.rows - 1;
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(a.lat + t * a.ld + 2 * k + 16 * c),
-                                       (__attribute__((address_space(3))) void*)(to + 1024 * (4 * wave + i)), 16, 0, 0);
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(a.w + 2 * ((int64_t)(n0 + row) * a.r + k) + 16 * c),
-                                       (__attribute__((address_space(3))) void*)(to + STAGE + 1024 * (4 * wave + i)), 16, 0, 0);
+  for (int i = 0; i < 2; ++i) {
+    const int row = 16 * (2 * wave + i) + (lane >> 2), c = (lane & 3) ^ ((row >> 2) & 3);
+    at[i] = (uint32_t)min(row, left) * (uint32_t)a.ld + 16 * c;
+    wt[i] = 2 * (uint32_t)row * (uint32_t)a.r + 16 * c;
+  }
+  auto load = [&](int s) {
+    char* to = lds + s % kExpandStages * kExpandStage + 1024 * (2 * wave);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      load_to_lds(lat + 64 * s, at[i], to + 1024 * i);
+      load_to_lds(w + 64 * s, wt[i], to + kExpandStage / 2 + 1024 * i);
     }
   };
   f32x16 acc[2][2];
@@ -62,21 +68,26 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs a) {
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-  const int steps = a.r / 64;
-  load(0, lds);
+  const int steps = a.r / 32;          // at least 8
+  load(0);
+  load(1);
+  load(2);
   for (int s = 0; s < steps; ++s) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (s + 1 < steps) load(64 * (s + 1), lds + (s + 1) % 2 * 2 * STAGE);
-    const char* x = lds + s % 2 * 2 * STAGE;
+    // a wave has four loads a stage: those of the two later stages may be under way
+    if (s + 2 < steps) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    else if (s + 1 < steps) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    lds_barrier();
+    if (s + 3 < steps) load(s + 3);
+    const char* x = lds + s % kExpandStages * kExpandStage;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
       bf16x8 u[2], v[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int ru = 64 * wn + 32 * i + l32, rv = 64 * wm + 32 * i + l32;
-        u[i] = *(const bf16x8*)(x + STAGE + ru * 128 + 16 * ((2 * k + half) ^ ((ru >> 1) & 7)));
-        v[i] = *(const bf16x8*)(x + rv * 128 + 16 * ((2 * k + half) ^ ((rv >> 1) & 7)));
+        u[i] = *(const bf16x8*)(x + kExpandStage / 2 + ru * 64 + 16 * ((2 * k + half) ^ ((ru >> 2) & 3)));
+        v[i] = *(const bf16x8*)(x + rv * 64 + 16 * ((2 * k + half) ^ ((rv >> 2) & 3)));
       }
       // rows of the result are columns n: a lane has 4 consecutive ones of a token
 #pragma unroll
@@ -85,17 +96,23 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(ExpandArgs a) {
         for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u[j], v[i], acc[i][j], 0, 0, 0);
     }
   }
+  // rows of 256 bytes go out through LDS: stored from the registers they would be pieces of 8 bytes, which take as long as the products
+  constexpr int OUT = 2 * kExpandTile + 16;
+  static_assert(kExpandTile * OUT <= kExpandStages * kExpandStage, "the tile fits the stages");
+  lds_barrier();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t t = t0 + 64 * wm + 32 * i + l32;
-    if (t >= a.rows) continue;
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int e = 0; e < 16; e += 4) {
-        const int n = n0 + 64 * wn + 32 * j + 2 * e + 4 * half;
-        *(u32x2*)(a.kv + t * a.n + n) = u32x2{f2_bf16(acc[i][j][e], acc[i][j][e + 1]), f2_bf16(acc[i][j][e + 2], acc[i][j][e + 3])};
-      }
+      for (int e = 0; e < 16; e += 4)
+        *(u32x2*)(lds + (64 * wm + 32 * i + l32) * OUT + 2 * (64 * wn + 32 * j + 2 * e + 4 * half)) =
+            u32x2{f2_bf16(acc[i][j][e], acc[i][j][e + 1]), f2_bf16(acc[i][j][e + 2], acc[i][j][e + 3])};
+  lds_barrier();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = 16 * i + (threadIdx.x >> 4), c = threadIdx.x & 15;
+    if (row <= left) *(u32x4*)(a.kv + (t0 + row) * a.n + n0 + 8 * c) = *(const u32x4*)(lds + row * OUT + 16 * c);
   }
 }
 
@@ -115,22 +132,18 @@ struct PromptArgs {
   float c;
 };
 
+// In LDS: 64 rows of keys' nope part, of their rope part and of values, 4, 8 or 16 chunks of 16 bytes each.
 template <int M, int P>
 struct PromptShape {
-  static constexpr int KC = (M + P) / 8, VC = M / 8;         // chunks of 16 bytes in a row
-  static constexpr int KB = 64 * 16 * KC, VB = 64 * 16 * VC;
-  static constexpr int STAGE = KB + VB;
+  static constexpr int KC = M / 8, RC = P / 8;
+  static constexpr int KB = 1024 * KC, KEYS = KB + 1024 * RC, STAGE = KEYS + KB;
   // 16 rows of one chunk on different banks
+  template <int N>
   static __device__ __forceinline__ int key_place(int c, int t) {
-    if constexpr (KC % 16 == 0) return c ^ (t & 15);
-    else if constexpr (KC % 16 == 8) return c ^ ((t >> 1) & 7);
-    else return c ^ ((t >> 2) & 3);
+    return c ^ (N == 16 ? t & 15 : N == 8 ? (t >> 1) & 7 : (t >> 2) & 3);
   }
   // 32 dims of 4 rows on different banks
-  static __device__ __forceinline__ int value_place(int c, int t) {
-    if constexpr (VC == 16) return c ^ ((t & 3) << 2);
-    else return c ^ ((t & 2) << 1);
-  }
+  static __device__ __forceinline__ int value_place(int c, int t) { return c ^ (KC == 16 ? (t & 3) << 2 : (t & 2) << 1); }
 };
 
 // Request and tile of Q queries of item `item` (in request order); false if there are fewer.
@@ -167,7 +180,7 @@ __device__ __forceinline__ bool find_queries(const PromptArgs& a, int item, Spli
 template <int M, int P, int W>
 __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(PromptArgs a) {
   typedef PromptShape<M, P> Sh;
-  constexpr int KC = Sh::KC, VC = Sh::VC, KS = (M + P) / 16, DT = M / 32;
+  constexpr int KC = Sh::KC, RC = Sh::RC, KS = (M + P) / 16, DT = M / 32;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   __shared__ SplitShared sh;
   const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5, m = lane & 15;
@@ -199,67 +212,137 @@ __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(PromptArgs a) {
     for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
   float top = kNone, l = 0.0f;
 
-  const int64_t kv_row = (int64_t)a.heads * 4 * M;
+  const uint32_t kv_row = (uint32_t)a.heads * 4 * M;
   const char* kv = a.kv + (int64_t)k_first * kv_row + h * (4 * M);
   const char* rope = a.lat + (int64_t)k_first * a.ld + 2 * a.r;
-  auto load = [&](int t) {
-    char* to = lds + (t & 1) * Sh::STAGE;
+  // a wave's loads of one area: N chunks of 64 rows, `row` bytes apart from `base` on; rows behind the last key are it again
+  auto area = [&](auto chunks, const char* base, uint32_t pitch, int left, char* to, auto place) {
+    constexpr int N = decltype(chunks)::value;
 #pragma unroll
-    for (int n = 0; n < (KC + W - 1) / W; ++n) {
-      if (KC % W != 0 && n * W + wave >= KC) break;
-      const int slot = (n * W + wave) * 64 + lane, row = slot / KC, c = Sh::key_place(slot - row * KC, row);
-      const int64_t key = min(64 * t + row, nk - 1);
-      const char* from = c < M / 8 ? kv + key * kv_row + 16 * c : rope + key * a.ld + 16 * (c - M / 8);
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
-                                       (__attribute__((address_space(3))) void*)(to + (n * W + wave) * 1024), 16, 0, 0);
-    }
-#pragma unroll
-    for (int n = 0; n < VC / W; ++n) {
-      const int slot = (n * W + wave) * 64 + lane, row = slot / VC, c = Sh::value_place(slot % VC, row);
-      const int64_t key = min(64 * t + row, nk - 1);
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(kv + key * kv_row + 2 * M + 16 * c),
-                                       (__attribute__((address_space(3))) void*)(to + Sh::KB + (n * W + wave) * 1024), 16, 0, 0);
+    for (int n = 0; n < (N + W - 1) / W; ++n) {
+      if (N % W != 0 && n * W + wave >= N) break;
+      const int slot = (n * W + wave) * 64 + lane, row = slot / N, c = place(slot % N, row);
+      load_to_lds(base, (uint32_t)min(row, left) * pitch + 16 * c, to + (n * W + wave) * 1024);
     }
   };
+  auto load = [&](int t) {
+    char* to = lds + (t & 1) * Sh::STAGE;
+    const int left = nk - 1 - 64 * t;
+    const char* rows = kv + 64 * (int64_t)t * kv_row;
+    area(std::integral_constant<int, KC>(), rows, kv_row, left, to, [](int c, int r) { return Sh::template key_place<KC>(c, r); });
+    area(std::integral_constant<int, RC>(), rope + 64 * (int64_t)t * a.ld, (uint32_t)a.ld, left, to + Sh::KB,
+         [](int c, int r) { return Sh::template key_place<RC>(c, r); });
+    area(std::integral_constant<int, KC>(), rows + 2 * M, kv_row, left, to + Sh::KEYS, [](int c, int r) { return Sh::value_place(c, r); });
+  };
   if (tiles > 0) load(0);
-  for (int t = 0; t < tiles; ++t) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();                   // tile t is there, and all waves are done with tile t - 1
+  bf16x8 w[4];
+  // Values of tile t: 16 keys (k) and 32 dims (d) at a time, keys 16 k + 4 half + 0..3 and 8 more, dims 32 d + lane % 32
+  const int vrow = 4 * half + (m >> 2), vc = 2 * ((lane >> 4) & 1) + ((m & 3) >> 1);
+  auto value = [&](const char* vt, int n) {
+    const int k = n / DT, d = n % DT;
+    const char* from = vt + (16 * k + vrow) * (16 * KC) + 16 * Sh::value_place(4 * d + vc, vrow) + 8 * (m & 1);
+    const u32x2 x = read_turned(from), y = read_turned(from + 8 * (16 * KC));
+    return u32x4{x[0], x[1], y[0], y[1]};
+  };
+  auto add_values = [&](int t) {
+    const char* vt = lds + (t & 1) * Sh::STAGE + Sh::KEYS;
+    if (64 * t + 63 <= wave_first && 64 * t + 64 <= nk) {
+      constexpr int N = 4 * DT, AHEAD = 3;
+      u32x4 v[AHEAD + 1];
+#pragma unroll
+      for (int n = 0; n < AHEAD; ++n) v[n] = value(vt, n);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        if (n + AHEAD < N) v[(n + AHEAD) % (AHEAD + 1)] = value(vt, n + AHEAD);
+        o[n % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v[n % (AHEAD + 1)]), w[n / DT], o[n % DT], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      return;
+    }
+#pragma unroll
+    for (int n = 0; n < 4 * DT; ++n) {
+      const int k = n / DT, d = n % DT;
+      const u32x4 v = value(vt, n);
+      bool odd = false;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) odd = odd || (v[j] & 0x7f80u) == 0x7f80u || (v[j] & 0x7f800000u) == 0x7f800000u;
+      if (!__any(odd)) {
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v), w[k], o[d], 0, 0, 0);
+        continue;
+      }
+      // one key at a time, kept by the queries that see it
+#pragma unroll 1
+      for (int j = 0; j < 8; ++j)
+#pragma unroll 1
+        for (int g = 0; g < 2; ++g) {
+          u32x4 one, pw;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t mask = half == g && e == j / 2 ? (j & 1 ? 0xffff0000u : 0xffffu) : 0u;
+            one[e] = v[e] & mask;
+            pw[e] = __builtin_bit_cast(u32x4, w[k])[e] & mask;
+          }
+          const f32x16 sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, one), __builtin_bit_cast(bf16x8, pw), o[d], 0, 0, 0);
+          const int key = 64 * t + 16 * k + 4 * g + j % 4 + 8 * (j / 4);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[d][e] = key <= last ? sum[e] : o[d][e];
+        }
+    }
+  };
+  // A round adds the values of the tile before, then forms the scores and weights of the next one (in the other order the compiler's registers do
+  // not suffice).
+  int held = -1;                       // tile whose weights wait for their values, or none
+  for (int t = 0; t <= tiles; ++t) {
+    if (held >= 0) add_values(held);
+    held = -1;
+    if (t == tiles) break;
+    loads_barrier();                   // tile t is there, and all waves are done with tile t - 1
     if (t + 1 < tiles) load(t + 1);
     if (64 * t > wave_last) continue;  // no query of this wave sees any of it
+    held = t;
     const char* kt = lds + (t & 1) * Sh::STAGE;
-    const char* vt = kt + Sh::KB;
     f32x16 s[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[u][e] = 0.0f;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
+    constexpr int AHEAD = 2;
+    bf16x8 key[AHEAD + 1][2];
+    auto read_keys = [&](int ks) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const bf16x8 key = *(const bf16x8*)(kt + (32 * u + l32) * (16 * KC) + 16 * Sh::key_place(2 * ks + half, 32 * u + l32));
-        s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[ks], s[u], 0, 0, 0);
+        const int row = 32 * u + l32, c = 2 * ks + half;
+        key[ks % (AHEAD + 1)][u] = *(const bf16x8*)(ks < M / 16 ? kt + row * (16 * KC) + 16 * Sh::template key_place<KC>(c, row)
+                                                               : kt + Sh::KB + row * (16 * RC) + 16 * Sh::template key_place<RC>(c - KC, row));
       }
-    const bool hidden = 64 * t + 63 > wave_first || 64 * t + 64 > nk;      // some query of the wave does not see all of it
-    float high = kNone;
-    if (hidden) {
+    };
+#pragma unroll
+    for (int ks = 0; ks < AHEAD; ++ks) read_keys(ks);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      if (ks + AHEAD < KS) read_keys(ks + AHEAD);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key[ks % (AHEAD + 1)][u], q[ks], s[u], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (64 * t + 63 > wave_first || 64 * t + 64 > nk) {      // some query of the wave does not see all of it
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int key = 64 * t + 32 * u + 8 * (e / 4) + 4 * half + e % 4;
-          s[u][e] = key <= last ? s[u][e] : kNone;
+          const int key_at = 64 * t + 32 * u + 8 * (e / 4) + 4 * half + e % 4;
+          s[u][e] = key_at <= last ? s[u][e] : kNone;
         }
     }
+    float high = kNone;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int e = 0; e < 16; ++e) high = fmaxf(high, s[u][e]);
     high *= a.c;
     if (__any(high > top + kSlack)) {
-      const uint32_t w = __float_as_uint(high);
-      const auto x = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+      const uint32_t hw = __float_as_uint(high);
+      const auto x = __builtin_amdgcn_permlane32_swap(hw, hw, false, false);
       const float up = fmaxf(top, fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])));
       const float f = top == kNone ? 0.0f : exp2f(top - up);
       top = up;
@@ -268,7 +351,6 @@ __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(PromptArgs a) {
       for (int d = 0; d < DT; ++d) o[d] *= f;
     }
     const float at = top == kNone ? 0.0f : top;
-    bf16x8 w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       u32x4 pk;
@@ -281,58 +363,32 @@ __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(PromptArgs a) {
       }
       w[k] = __builtin_bit_cast(bf16x8, pk);
     }
-    typedef short s16x4 __attribute__((ext_vector_type(4)));
-    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        // keys 16 k + 4 half + 0..3 and 8 more, dims 32 d + lane % 32
-        const int row = 16 * k + 4 * half + (m >> 2), c = 4 * d + 2 * ((lane >> 4) & 1) + ((m & 3) >> 1);
-        const char* from = vt + row * (16 * VC) + 16 * Sh::value_place(c, row) + 8 * (m & 1);
-        const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)from));
-        const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(from + 8 * (16 * VC))));
-        u32x4 v = {x[0], x[1], y[0], y[1]};
-        if (hidden) {
-          bool odd = false;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) odd = odd || (v[j] & 0x7f80u) == 0x7f80u || (v[j] & 0x7f800000u) == 0x7f800000u;
-          if (__any(odd)) {
-            // one key at a time, kept by the queries that see it
-#pragma unroll 1
-            for (int j = 0; j < 8; ++j)
-#pragma unroll 1
-              for (int g = 0; g < 2; ++g) {
-                u32x4 one, pw;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const uint32_t mask = half == g && e == j / 2 ? (j & 1 ? 0xffff0000u : 0xffffu) : 0u;
-                  one[e] = v[e] & mask;
-                  pw[e] = __builtin_bit_cast(u32x4, w[k])[e] & mask;
-                }
-                const f32x16 sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, one), __builtin_bit_cast(bf16x8, pw), o[d], 0, 0, 0);
-                const int key = 64 * t + 16 * k + 4 * g + j % 4 + 8 * (j / 4);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[d][e] = key <= last ? sum[e] : o[d][e];
-              }
-            continue;
-          }
-        }
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v), w[k], o[d], 0, 0, 0);
-      }
   }
   const uint32_t lw = __float_as_uint(l);
   const auto x = __builtin_amdgcn_permlane32_swap(lw, lw, false, false);
   const float all = __uint_as_float(x[0]) + __uint_as_float(x[1]);
-  if (i >= nq) return;
   const float inv = all == 0.0f ? 0.0f : 1.0f / all;
-  uint16_t* to = a.out + (int64_t)(q_first + i) * a.out_t + h * a.out_h;
+  // rows of 2 M bytes go out through LDS, a wave's own 32 at a time
+  constexpr int OUT = 2 * M + 16;
+  static_assert(32 * W * OUT <= 2 * Sh::STAGE, "the rows fit the stages");
+  lds_barrier();                       // all waves are done with the last tile
+  char* const rows_out = lds + wave * (32 * OUT);
 #pragma unroll
   for (int d = 0; d < DT; ++d)
 #pragma unroll
     for (int e = 0; e < 16; e += 4)
-      *(u32x2*)(to + 32 * d + 2 * e + 4 * half) =
-          u32x2{f2_bf16(o[d][e] * inv, o[d][e + 1] * inv), f2_bf16(o[d][e + 2] * inv, o[d][e + 3] * inv)};
+      *(u32x2*)(rows_out + l32 * OUT + 2 * (32 * d + 2 * e + 4 * half)) = u32x2{f2_bf16(o[d][e] * inv, o[d][e + 1] * inv), f2_bf16(o[d][e + 2] * inv, o[d][e + 3] * inv)};
+  uint16_t* const to = a.out + h * a.out_h;
+#pragma unroll
+  for (int n = 0; n < KC / 2; ++n) {
+    const int slot = 64 * n + lane, row = slot / KC, c = slot % KC, qi = i0 + 32 * wave + row;
+    const u32x4 v = *(const u32x4*)(rows_out + row * OUT + 16 * c);
+    if (qi >= nq) continue;
+    u32x2* at = (u32x2*)(to + (int64_t)(q_first + qi) * a.out_t + 8 * c);       // rows start on 8-byte boundaries
+    at[0] = u32x2{v[0], v[1]};
+    at[1] = u32x2{v[2], v[3]};
+  }
+  if (i >= nq) return;
   if (a.lse && half == 0)
     a.lse[(int64_t)(q_first + i) * a.lse_t + h] = all == 0.0f ? kNone : ((top == kNone ? 0.0f : top) + log2f(all)) / kLog2E;
 }

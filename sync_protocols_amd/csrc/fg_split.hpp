@@ -29,7 +29,7 @@ struct SplitArgs {
   int64_t ldt;                       // entries
   int32_t batch, width, n_pages, page;
   int32_t window;                    // 0: all tokens
-  int32_t target, least;             // workgroups; units that one has at least where there are few
+  int32_t target;                    // workgroups, at most one a unit
   int32_t* pieces;                   // workspace: {first place, number of pieces} of every request
 };
 
@@ -84,7 +84,7 @@ struct Pieces {
     }
     total = __builtin_amdgcn_readfirstlane(total);
     w = w_;
-    const int n = min(a.target, (total + a.least - 1) / a.least);
+    const int n = min(a.target, total);
     if (w >= n) return false;
     share = total / n;
     more = total - n * share;
