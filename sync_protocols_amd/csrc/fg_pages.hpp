@@ -31,27 +31,53 @@ struct PageStepArgs {
   int32_t batch, width, n_pages, page, tokens, fill;       // fill: this kernel writes slots and positions
 };
 
-// Inclusive prefix sum over a workgroup of T threads, and its total.
-template <int T>
-__device__ __forceinline__ int64_t sum_upto(int64_t v, int64_t& total, int64_t* buf) {
+// Sums that stop at the largest number: what they are compared with is below 2^31.
+__device__ __forceinline__ uint32_t plus(uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); }
+
+// Inclusive prefix sums of N numbers over a workgroup of T threads, and their totals.
+template <int T, int N>
+__device__ __forceinline__ void sums_upto(uint32_t (&v)[N], uint32_t (&total)[N], uint32_t (&buf)[N][T / 64]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int64_t u = __shfl_up(v, d);
-    if (lane >= d) v += u;
+  for (int i = 0; i < N; ++i) {
+    auto moved = [&](auto ctrl, auto rows) {
+      return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v[i], decltype(ctrl)::value, decltype(rows)::value, 0xf, false);
+    };
+    typedef std::integral_constant<int, 0xf> all;
+    v[i] = plus(v[i], moved(std::integral_constant<int, 0x111>(), all()));      // row_shr:1, 2, 4, 8
+    v[i] = plus(v[i], moved(std::integral_constant<int, 0x112>(), all()));
+    v[i] = plus(v[i], moved(std::integral_constant<int, 0x114>(), all()));
+    v[i] = plus(v[i], moved(std::integral_constant<int, 0x118>(), all()));
+    v[i] = plus(v[i], moved(std::integral_constant<int, 0x142>(), std::integral_constant<int, 0xa>()));      // row_bcast:15 into rows 1 and 3
+    v[i] = plus(v[i], moved(std::integral_constant<int, 0x143>(), std::integral_constant<int, 0xc>()));      // row_bcast:31 into rows 2 and 3
   }
   __syncthreads();                       // buf's last readers
-  if (lane == 63) buf[wave] = v;
-  __syncthreads();
-  int64_t before = 0;
-  total = 0;
 #pragma unroll
-  for (int w = 0; w < T / 64; ++w) {
-    const int64_t u = buf[w];
-    before += w < wave ? u : 0;
-    total += u;
+  for (int i = 0; i < N; ++i)
+    if (lane == 63) buf[i][wave] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint32_t before = 0;
+    total[i] = 0;
+#pragma unroll
+    for (int w = 0; w < T / 64; ++w) {
+      const uint32_t u = buf[i][w];
+      if (w < wave) before = plus(before, u);
+      total[i] = plus(total[i], u);
+    }
+    v[i] = plus(v[i], before);
   }
-  return v + before;
+}
+template <int T>
+__device__ __forceinline__ uint32_t max_of_all(uint32_t v, uint32_t (&buf)[T / 64]) {
+  v = lanes_max<64>(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < T / 64; ++w) v = buf[w] > v ? buf[w] : v;
+  return v;
 }
 
 // The last entry of at[0..n) that is not above i; at[0] <= i.
@@ -78,66 +104,86 @@ __device__ __forceinline__ void put_none(const PageStepArgs& a, int64_t t) {
 
 template <int T>
 __global__ __launch_bounds__(T) void page_step_kernel(PageStepArgs a) {
-  __shared__ int64_t buf[T / 64];
+  __shared__ uint32_t buf[2][T / 64], buf1[1][T / 64];
   __shared__ int32_t fresh[T], back[T], given[T], held_at[T], len_at[T];
   const int tid = threadIdx.x;
   const int64_t head = a.ends[0], tail = a.ends[1], size = a.n_pages;
-  const int64_t free_pages = tail < head ? 0 : tail - head > size ? size : tail - head;
+  const uint32_t free_pages = (uint32_t)(tail < head ? 0 : tail - head > size ? size : tail - head);
   const int64_t h0 = (head % size + size) % size, t0 = (tail % size + size) % size;
-  int64_t asked = 0, wanted = 0, taken = 0, served_tokens = 0, returned = 0;
+  uint32_t asked = 0, wanted = 0, taken = 0, served_tokens = 0, returned = 0;
   if (tid == 0) a.starts[0] = 0;
   for (int first = 0; first < a.batch; first += T) {
     const int b = first + tid;
     const bool in = b < a.batch;
-    const int64_t len = in && a.lens[b] > 0 ? a.lens[b] : 0;
-    const int64_t add = in ? a.add[b] : 0, want = add > 0 ? add : 0;
-    const int64_t held = (len + a.page - 1) / a.page, wants = (len + want + a.page - 1) / a.page;
-    const bool fits = in && wants <= a.width;
-    const int64_t need = fits ? wants - held : 0;
-    int64_t all;
-    // served: pages, then tokens, in request order; what does not come through asks for its share all the same
-    const int64_t upto = asked + sum_upto<T>(need, all, buf);
-    asked += all;
-    bool ok = fits && (need == 0 || upto <= free_pages);
-    const int64_t tokens_upto = wanted + sum_upto<T>(ok ? want : 0, all, buf);
-    wanted += all;
-    ok = ok && tokens_upto <= a.tokens;
-    const int64_t got = ok ? want : 0, got_upto = sum_upto<T>(got, all, buf);
-    const int64_t tokens_here = all;
-    const int64_t pages = ok ? need : 0, pages_upto = sum_upto<T>(pages, all, buf);
-    const int64_t pages_here = all;
+    const uint32_t len = in && a.lens[b] > 0 ? a.lens[b] : 0, page = a.page;
+    const int32_t add = in ? a.add[b] : 0;
+    const uint32_t want = add > 0 ? add : 0;
+    const uint32_t held = len / page + (len % page != 0), wants = (len + want) / page + ((len + want) % page != 0);     // len + want is below 2^32
+    const bool fits = in && wants <= (uint32_t)a.width;
+    const uint32_t need = fits ? wants - held : 0;
+    const uint32_t ends = in && add < 0 ? (held < (uint32_t)a.width ? held : a.width) : 0;
+    // Served: pages, then tokens, in request order; what does not come through asks for its share all the same. So those that
+    // need pages and get them are the first that need any, and their places among the pages are those of all.
+    uint32_t sums[2] = {need, ends}, all[2];
+    sums_upto<T>(sums, all, buf);
+    const uint32_t pages_upto = plus(asked, sums[0]);
+    const bool paged = fits && (need == 0 || pages_upto <= free_pages);
+    uint32_t tokens[1] = {paged ? want : 0}, all_tokens[1];
+    sums_upto<T>(tokens, all_tokens, buf1);
+    const uint32_t tokens_upto = plus(wanted, tokens[0]);
+    const bool ok = paged && tokens_upto <= (uint32_t)a.tokens;
+    const uint32_t last_page = max_of_all<T>(ok && need ? pages_upto : 0, buf[0]), last_token = max_of_all<T>(ok ? tokens_upto : 0, buf[1]);
+    const uint32_t pages_here = last_page > taken ? last_page - taken : 0, tokens_here = last_token > served_tokens ? last_token - served_tokens : 0;
     // pages of ended requests, as many as the ring has places for
-    const int64_t ends = in && add < 0 ? (held < a.width ? held : a.width) : 0;
-    const int64_t room = size - free_pages - returned;
-    const int64_t ends_upto = sum_upto<T>(ends, all, buf);
-    const int64_t back_here = all < room ? all : room;
+    const uint32_t room = (uint32_t)size - free_pages - returned, back_here = all[1] < room ? all[1] : room;
+    auto place = [](uint32_t v, uint32_t from) { return (int32_t)(v < from ? 0 : v - from > 0x7fffffffu ? 0x7fffffffu : v - from); };
+    const uint32_t start = plus(wanted, tokens[0] - (paged ? want : 0)), total = served_tokens + tokens_here;
     if (in) {
-      a.lens_out[b] = add < 0 ? 0 : (int32_t)(len + got);
-      a.starts[b + 1] = (int32_t)(served_tokens + got_upto);
+      a.lens_out[b] = add < 0 ? 0 : (int32_t)(len + (ok ? want : 0));
+      a.starts[b + 1] = (int32_t)(tokens_upto < total ? tokens_upto : total);
     }
-    fresh[tid] = (int32_t)(pages_upto - pages);
-    given[tid] = (int32_t)(got_upto - got);
-    const int64_t from = ends_upto - ends;
-    back[tid] = (int32_t)(from < 0x7fffffff ? from : 0x7fffffff);
+    fresh[tid] = place(plus(asked, sums[0] - need), taken);
+    given[tid] = place(start, served_tokens);
+    back[tid] = place(sums[1] - ends, 0);
     held_at[tid] = (int32_t)held;
     len_at[tid] = (int32_t)len;
     __syncthreads();
-    for (int64_t i = tid; i < pages_here; i += T) {
-      const int r = last_upto(fresh, T, (int)i);
-      int64_t at = h0 + taken + i;
-      if (at >= size) at -= size;
-      a.table[(first + r) * a.ldt + held_at[r] + (i - fresh[r])] = a.ring[at];
+    // four at a time, their searches and loads beside each other
+    constexpr int B = 4;
+    for (uint32_t i = tid; i < pages_here; i += B * T) {
+      int r[B];
+      int32_t v[B];
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        const uint32_t n = i + j * T < pages_here ? i + j * T : i;
+        r[j] = last_upto(fresh, T, (int)n);
+        int64_t at = h0 + taken + n;
+        v[j] = a.ring[at >= size ? at - size : at];
+      }
+#pragma unroll
+      for (int j = 0; j < B; ++j)
+        if (i + j * T < pages_here) a.table[(int64_t)(first + r[j]) * a.ldt + held_at[r[j]] + ((int)(i + j * T) - fresh[r[j]])] = v[j];
     }
-    for (int64_t i = tid; i < back_here; i += T) {
-      const int r = last_upto(back, T, (int)i);
-      a.ring[(t0 + returned + i) % size] = a.table[(first + r) * a.ldt + (i - back[r])];
+    for (uint32_t i = tid; i < back_here; i += B * T) {
+      int32_t v[B];
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        const uint32_t n = i + j * T < back_here ? i + j * T : i;
+        const int r = last_upto(back, T, (int)n);
+        v[j] = a.table[(int64_t)(first + r) * a.ldt + ((int)n - back[r])];
+      }
+#pragma unroll
+      for (int j = 0; j < B; ++j)
+        if (i + j * T < back_here) a.ring[(t0 + returned + i + j * T) % size] = v[j];
     }
     __syncthreads();
     if (a.fill)
-      for (int64_t i = tid; i < tokens_here; i += T) {
+      for (uint32_t i = tid; i < tokens_here; i += T) {
         const int r = last_upto(given, T, (int)i);
-        put_token(a, served_tokens + i, first + r, len_at[r] + (int)(i - given[r]));
+        put_token(a, (int64_t)served_tokens + i, first + r, len_at[r] + ((int)i - given[r]));
       }
+    asked = plus(asked, all[0]);
+    wanted = plus(wanted, all_tokens[0]);
     taken += pages_here;
     served_tokens += tokens_here;
     returned += back_here;
@@ -147,7 +193,7 @@ __global__ __launch_bounds__(T) void page_step_kernel(PageStepArgs a) {
     a.ends_out[1] = tail + returned;
   }
   if (a.fill)
-    for (int64_t t = served_tokens + tid; t < a.tokens; t += T) put_none(a, t);
+    for (int64_t t = (int64_t)served_tokens + tid; t < a.tokens; t += T) put_none(a, t);
 }
 
 // Tokens of a large step: starts in LDS where they fit.

@@ -88,6 +88,16 @@ def test_page_step_of_one_long_prompt_and_of_none():
     assert got.slots.tolist() == [-1] * 9 and got.starts.tolist() == [0] and got.ends.tolist() == ends
 
 
+def test_page_step_of_sums_beyond_32_bits():
+    """Asked tokens and pages that add up beyond any 32-bit number; only what comes before them is served."""
+    page, width, n = 1 << 20, 2000, 300
+    table = torch.arange(n * width, dtype=torch.int32).reshape(n, width)
+    ring = torch.arange(5000, dtype=torch.int32)
+    check_step([7] * n, [1, 3] + [1 << 30] * (n - 3) + [2], table, ring, [2, 5002], page, 10)
+    check_step([7] * n, [1, 3] + [2 ** 31 - 1] * (n - 2), table, ring, [2, 5002], page, 10)
+    check_step([2 ** 31 - 1] * n, [2 ** 31 - 1, -1, 1] * (n // 3), table, ring, [2, 2002], 1 << 20, 10)
+
+
 def test_pages_go_round():
     """Many steps of requests that come and go, state on the GPU alone: no page has two owners, none is lost."""
     rng = random.Random(4)
@@ -350,6 +360,34 @@ def test_paged_strided_queries_outputs_and_workspace():
     assert (out[:, 2] == 7).all() and (out[..., 64:] == 7).all()
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_append_and_paged_beyond_32_bits(e4m3):
+    """Pages further apart than 32 bits of bytes."""
+    g = A.gen(12)
+    page, kv, dim, stride, n = 16, 2, 128, (1 << 31) + 4096, 3
+    lens = [40, 16]
+    table = torch.tensor([[2, 0, 1], [2, -1, -1]], dtype=torch.int32)
+    typ = E4M3 if e4m3 else BF
+    caches = []
+    for _ in range(2):
+        room = torch.empty((n - 1) * stride + page * kv * dim, dtype=torch.uint8 if e4m3 else BF, device=DEV).view(typ)
+        caches.append(room.as_strided((n, page, kv, dim), (stride, kv * dim, dim, 1)))
+    k, v = (torch.randn(n * page, kv, dim, generator=g).bfloat16() for _ in range(2))
+    scales = [torch.zeros(n, kv, page, device=DEV) if e4m3 else None for _ in range(2)]
+    ops.kv_append(dev(k), caches[0], torch.arange(n * page, device=DEV), v=dev(v), v_cache=caches[1], k_scale=scales[0], v_scale=scales[1])
+
+    def seen(x, c, s):
+        if not e4m3:
+            assert torch.equal(c.cpu(), x.reshape(n, page, kv, dim))
+            return x.double().reshape(n, page, kv, dim)
+        return c.cpu().double() * s.transpose(1, 2).cpu().double()[..., None]
+
+    q = torch.randn(2, 4, dim, generator=g).bfloat16()
+    got = ops.paged_attention(dev(q), *caches, dev(table), torch.tensor(lens, dtype=torch.int32, device=DEV), k_scale=scales[0], v_scale=scales[1])
+    want = A.paged(q, seen(k, caches[0], scales[0]), seen(v, caches[1], scales[1]), table, lens, dim ** -0.5)
+    A.close(got, *want[:2])
+
+
 def test_parts_of_a_cache_are_joined_by_lse():
     g = A.gen(9)
     table, n = A.place(g, [640], 16, 40)
@@ -445,6 +483,16 @@ def test_latent_strided_rows_outputs_and_workspace():
     assert (out[:, 5] == 3).all() and (out[..., :16] == 3).all()
 
 
+def test_latent_pages_beyond_32_bits():
+    lens = [40, 16]
+    q, w, cache, table = latent_inputs(lens, 5, 256, 32, 64, 16)
+    n, stride = cache.shape[0], (1 << 30) + 4096
+    far = torch.empty((n - 1) * stride + 16 * 288, dtype=BF, device=DEV).as_strided((n, 16, 288), (stride, 288, 1))
+    far.copy_(dev(cache))
+    got = ops.latent_attention(*dev(q, w), far, dev(table), torch.tensor(lens, dtype=torch.int32, device=DEV), nope=64)
+    A.close(got, *A.latent(q, w, cache, table, lens, 64, 96 ** -0.5)[:2])
+
+
 # ------------------------------------------------------------------ prompt
 def starts_of(counts):
     s = [0]
@@ -535,6 +583,24 @@ def test_prompt_starts_beyond_the_rows_are_left_out():
     out = torch.full((90, 2, 64), 2.0, dtype=BF, device=DEV)
     ops.latent_prompt(*dev(q, lat, w, torch.tensor([95, 300], dtype=torch.int32)), nope=64, out=out)
     assert (out == 2).all()
+
+
+def test_prompt_rows_beyond_32_bits():
+    """A workspace and inputs of more than 4 GiB: the last of 70 requests, and the first."""
+    heads, rank, rope, nope, n, each = 128, 256, 32, 128, 70, 1000
+    g = torch.Generator(device=DEV).manual_seed(13)
+    lat = torch.randn(n * each, rank + rope, generator=g, device=DEV).bfloat16()
+    w = (torch.randn(heads, 2 * nope, rank, generator=g, device=DEV) / math.sqrt(rank)).bfloat16()
+    q = torch.randn(n, heads, nope + rope, generator=g, device=DEV).bfloat16()
+    far = torch.empty((n - 1) * (1 << 26) + heads * (nope + rope), dtype=BF, device=DEV).as_strided(q.shape, (1 << 26, nope + rope, 1))
+    far.copy_(q)
+    out = torch.empty((n - 1) * (1 << 26) + heads * nope, dtype=BF, device=DEV).as_strided((n, heads, nope), (1 << 26, nope, 1))
+    ks = torch.arange(0, n * each + 1, each, dtype=torch.int32, device=DEV)
+    ops.latent_prompt(far, lat, w, torch.arange(n + 1, dtype=torch.int32, device=DEV), k_starts=ks, nope=nope, out=out)
+    for b in (0, n - 1):
+        h = [0, 77, 127]
+        want = A.prompt(q[b:b + 1, h].cpu(), lat[b * each:(b + 1) * each].cpu(), w[h].cpu(), [0, 1], [0, each], nope, (nope + rope) ** -0.5)
+        A.close(out[b:b + 1, h], *want[:2])
 
 
 def test_both_forms_agree():
