@@ -31,8 +31,16 @@ int paged_target(int64_t parts) {
   const int64_t t = kPagedPlaces / parts;
   return (int)(t < 1 ? 1 : t);
 }
-// 16-head tiles of a workgroup, as many as the group fills and the registers hold, and the workgroups that this makes of all heads
-int head_tiles(int32_t group, int32_t dim) { return group <= 16 ? 1 : group <= 32 || dim == 256 ? 2 : 4; }
+// 16-head tiles of a workgroup, and the workgroups that this makes of all heads. More tiles read a cache fewer times, but a compute unit holds fewer
+// waves with their sums; with neighbours on one die the second reader mostly finds the rows in its L2. 16 requests, one key head, bf16, us:
+//   dim, heads          16384 tokens each, 1, 2, 4 tiles      65536 tokens each
+//   64, 32              22, 22                                58, 49
+//   64, 64              33, 25, 39                            99, 61, 75
+//   128, 32             31, 41                                110, 112
+//   128, 64             47, 43, 64                            177, 143, 136
+//   128, 128            81, 62, 62                            313, 238, 168
+//   256, 32             63, 82                                224, 242
+int head_tiles(int32_t group, int32_t dim) { return group <= 16 || dim == 256 ? 1 : dim == 64 ? 2 : group <= 32 ? 1 : group <= 64 ? 2 : 4; }
 int64_t head_parts(int32_t kv, int32_t group, int32_t dim) {
   const int per = 16 * head_tiles(group, dim);
   return (int64_t)kv * ((group + per - 1) / per);
@@ -42,8 +50,10 @@ template <int D, bool E4M3>
 void launch_paged(const PagedArgs& a, int tiles, dim3 grid, Launches& go) {
   const dim3 block(64 * kPagedWaves);
   if (tiles == 1) go(paged_kernel<D, E4M3, 1>, grid, block, 0, a);
-  else if (tiles == 2) go(paged_kernel<D, E4M3, 2>, grid, block, 0, a);
-  else if constexpr (D < 256) go(paged_kernel<D, E4M3, 4>, grid, block, 0, a);
+  else if constexpr (D < 256) {
+    if (tiles == 2) go(paged_kernel<D, E4M3, 2>, grid, block, 0, a);
+    else if constexpr (D == 128) go(paged_kernel<D, E4M3, 4>, grid, block, 0, a);
+  }
 }
 
 template <int D>
@@ -178,7 +188,6 @@ fg_status fg_paged_attention(const void* q, int64_t q_b, int64_t q_h, const fg_c
   const int64_t parts = head_parts(kv, group, dim);
   const int target = paged_target(parts);
   const int64_t items = batch + target;
-  if (parts > 65535) return FG_EINVAL;
   char* w = (char*)workspace;
   a.part = (float*)w;
   a.ml = (float*)(w + 4 * items * heads * dim);
@@ -191,7 +200,7 @@ fg_status fg_paged_attention(const void* q, int64_t q_b, int64_t q_h, const fg_c
   a.v_page = es * v->page_stride; a.v_head = es * v->head_stride; a.v_tok = (int32_t)(es * v->row_stride);
   a.kv = kv; a.group = group; a.heads = (int32_t)heads; a.c = scale * kLog2E;
   Launches go{stream};
-  const dim3 grid((unsigned)target, (unsigned)parts);
+  const dim3 grid((unsigned)((target + 7) / 8 * 8 * parts));
   const int tiles = head_tiles(group, dim);
   if (dim == 64) launch_paged<64>(e4m3, a, tiles, grid, go);
   else if (dim == 128) launch_paged<128>(e4m3, a, tiles, grid, go);
