@@ -146,7 +146,7 @@ fg_status fg_latent_prompt(const void* q, int64_t q_t, int64_t q_h, const int32_
                            int32_t rank, int32_t rope, int32_t nope, float scale, void* workspace, int64_t workspace_bytes,
                            void* out, int64_t out_t, int64_t out_h, float* lse, int64_t lse_t, hipStream_t stream) {
   int64_t need = 0;
-  if (!sizes_ok(heads, rank, rope, nope, scale) || fg_latent_prompt_bytes(k_rows, heads, nope, &need) != FG_OK || q_rows < 0 || q_rows > kMax || batch < 0 ||
+  if (!sizes_ok(heads, rank, rope, nope, scale) || fg_latent_prompt_bytes(k_rows, heads, nope, &need) != FG_OK || q_rows < 0 || q_rows > kMax - 1024 || batch < 0 ||
       batch > FG_ATTN_MAX_BATCH)
     return FG_EINVAL;
   if (batch == 0 || q_rows == 0) return FG_OK;

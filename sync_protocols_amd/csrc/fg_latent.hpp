@@ -128,7 +128,7 @@ struct RowTiles {
   __device__ __forceinline__ void enter(const SplitArgs& s, int lane) {       // the piece p, or the first one after it that has rows
     more = true;
     t = 0;
-    while ((tiles = (p.end - p.begin + T - 1) / T) <= 0)
+    while ((tiles = steps_of<T>(p.end - p.begin)) == 0)
       if (!p.next(s, 1)) {
         more = false;
         return;
@@ -239,7 +239,7 @@ __global__ __launch_bounds__(128 * G) void latent_kernel(LatentArgs a) {
         l[ht] = 0.0f;
       }
     }
-    const int tiles = (p.end - p.begin + T - 1) / T;
+    const int tiles = steps_of<T>(p.end - p.begin);
     for (int t = 0; t < tiles; ++t, ++g) {
       loads_barrier();                 // this tile is there, and all waves are done with the one before
       const char* tile = lds + (g & 1) * Sh::TILE;

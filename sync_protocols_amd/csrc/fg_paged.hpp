@@ -213,7 +213,7 @@ __global__ __launch_bounds__(64 * kPagedWaves) void paged_kernel(PagedArgs a) {
       for (int j = 0; j < NV; ++j) o[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
     // this wave's tiles of 32 tokens
-    const int block0 = p.begin / 16, n = (p.end - p.begin + 31) / 32, t0 = n * wave / W, t1 = n * (wave + 1) / W;
+    const int block0 = p.begin / 16, n = steps_of<32>(p.end - p.begin), t0 = n * wave / W, t1 = n * (wave + 1) / W;
     Tile x;
     BlockList list;
     Blocks now, next;

@@ -44,11 +44,14 @@ __device__ __forceinline__ int seen_tokens(const SplitArgs& a, int b, int& first
   first = a.window > 0 && len > a.window ? len - a.window : 0;
   return len;
 }
+// Up to 2^31 - 1 tokens in steps of N.
+template <int N>
+__device__ __forceinline__ int steps_of(int tokens) { return (int)(((uint32_t)tokens + (N - 1)) / N); }
 template <int U>
 __device__ __forceinline__ int units_of(const SplitArgs& a, int b) {
   int first;
   const int len = seen_tokens(a, b, first);
-  return max(1, (len - (first & ~15) + U - 1) / U);
+  return max(1, steps_of<U>(len - (first & ~15)));
 }
 
 // The pieces of one workgroup, one after the other.
@@ -112,9 +115,9 @@ struct Pieces {
   __device__ __forceinline__ void take(const SplitArgs& a, int tid) {
     len = __builtin_amdgcn_readfirstlane(seen_tokens(a, b, first));
     first = __builtin_amdgcn_readfirstlane(first);
-    const int origin = first & ~15, u = max(1, (len - origin + U - 1) / U), mine = min(left, u - skip);
+    const int origin = first & ~15, u = max(1, steps_of<U>(len - origin)), mine = min(left, u - skip);
     begin = origin + U * skip;
-    end = min(len, begin + U * mine);
+    end = mine == u - skip ? len : begin + U * mine;
     const int w0 = owner(at), w1 = owner(at + u - 1);
     place = w + b;
     count = w1 - w0 + 1;

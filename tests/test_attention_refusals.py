@@ -142,7 +142,7 @@ def _prompt(**kw):
 @pytest.mark.parametrize("kw", [
     dict(q=None), dict(qs=None), dict(ks=None), dict(lat=None), dict(w=None), dict(ws=None), dict(out=None), dict(q_rows=-1), dict(k_rows=-1), dict(batch=-1),
     dict(batch=65536), dict(heads=0), dict(rank=100), dict(rope=16), dict(nope=32), dict(scale=-0.5), dict(wsb=1000), dict(q=P + 2), dict(q_t=4), dict(ld=568),
-    dict(ld=579), dict(ld=1 << 23), dict(lat=P + 2 * GAP + 2), dict(out=P + 6 * GAP + 4), dict(out_h=130), dict(out_h=64), dict(lse=P + 7 * GAP, lse_t=2), dict(out=P), dict(out=P + GAP),
+    dict(ld=579), dict(ld=1 << 23), dict(k_rows=65535 * 128 + 1, wsb=1 << 40), dict(q_rows=2 ** 31 - 1), dict(batch=60000, heads=40000, wsb=1 << 40), dict(lat=P + 2 * GAP + 2), dict(out=P + 6 * GAP + 4), dict(out_h=130), dict(out_h=64), dict(lse=P + 7 * GAP, lse_t=2), dict(out=P), dict(out=P + GAP),
     dict(out=P + 2 * GAP), dict(out=P + 3 * GAP), dict(out=P + 5 * GAP), dict(ws=P + 2 * GAP), dict(lse=P + 6 * GAP, lse_t=4)])
 def test_prompt_refuses(kw):
     assert _prompt(**kw) == fg.EINVAL

@@ -388,6 +388,26 @@ def test_append_and_paged_beyond_32_bits(e4m3):
     A.close(got, *want[:2])
 
 
+@pytest.mark.parametrize("kind", ["paged", "latent"])
+def test_as_many_tokens_as_a_length_counts(kind):
+    """2^31 - 16 tokens, of which only the first and the last page are there."""
+    g = A.gen(14)
+    width = 2 ** 27 - 1
+    table = torch.full((1, width), -1, dtype=torch.int32, device=DEV)
+    table[0, 0], table[0, -1] = 1, 0
+    lens = torch.tensor([16 * width], dtype=torch.int32, device=DEV)
+    small = torch.tensor([[1, 0]], dtype=torch.int32)
+    if kind == "paged":
+        q = torch.randn(1, 2, 64, generator=g).bfloat16()
+        k, _, kd = caches_of(g, 2, 16, 1, 64, False)
+        v, _, vd = caches_of(g, 2, 16, 1, 64, False)
+        A.close(ops.paged_attention(dev(q), k, v, table, lens), *A.paged(q, kd, vd, small, [32], 0.125)[:2])
+        A.close(ops.paged_attention(dev(q), k, v, table, lens, window=20), *A.paged(q, kd, vd, small[:, 1:], [16], 0.125)[:2])
+    else:
+        q, w, cache, _ = latent_inputs([32], 2, 256, 32, 64, 16)
+        A.close(ops.latent_attention(*dev(q, w, cache[:2]), table, lens, nope=64), *A.latent(q, w, cache[:2], small, [32], 64, 96 ** -0.5)[:2])
+
+
 def test_parts_of_a_cache_are_joined_by_lse():
     g = A.gen(9)
     table, n = A.place(g, [640], 16, 40)
