@@ -122,8 +122,8 @@ fg_status fg_latent_attention(const void* q, int64_t q_b, int64_t q_h, const voi
   a.heads = heads; a.tiles = (int32_t)tiles; a.parts = (int32_t)parts; a.c = scale * kLog2E;
   Launches go{stream};
   const unsigned b_tiles = (unsigned)((batch + 15) / 16);
-  const AbsorbArgs absorb{(const char*)q, (const char*)w, absorbed, 2 * q_b, 2 * q_h, 4 * (int64_t)nope * rank, (int32_t)batch, heads, nope, rank, rope};
-  go(absorb_kernel, dim3((unsigned)rank / 128, (unsigned)heads, b_tiles), dim3(64), 0, absorb);
+  const AbsorbArgs absorb{(const char*)q, (const char*)w, absorbed, 2 * q_b, 2 * q_h, 4 * (int64_t)nope * rank, (int32_t)batch, heads, rank, rope};
+  go(nope == 128 ? absorb_kernel<128> : absorb_kernel<64>, dim3((unsigned)rank / 128, (unsigned)heads, b_tiles), dim3(64), 0, absorb);
   const dim3 grid((unsigned)((a.split.target + 7) / 8 * 8 * parts));
   if (rank == 512) rope == 64 ? launch_latent<512, 64>(a, grid, go) : launch_latent<512, 32>(a, grid, go);
   else rope == 64 ? launch_latent<256, 64>(a, grid, go) : launch_latent<256, 32>(a, grid, go);

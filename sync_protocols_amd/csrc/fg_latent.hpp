@@ -534,9 +534,10 @@ struct AbsorbArgs {
   const char* w;
   char* a;
   int64_t x_b, x_h, w_h;             // bytes
-  int32_t batch, heads, k, n, rope;  // k a multiple of 32, n of 128
+  int32_t batch, heads, n, rope;     // n a multiple of 128
 };
 
+template <int K>
 __global__ __launch_bounds__(64) void absorb_kernel(AbsorbArgs a) {
   const int lane = threadIdx.x, m = lane & 15, quarter = lane >> 4;
   const int h = blockIdx.y, b0 = 16 * blockIdx.z;
@@ -549,19 +550,24 @@ __global__ __launch_bounds__(64) void absorb_kernel(AbsorbArgs a) {
 #pragma unroll
   for (int j = 0; j < N; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const int n0 = 128 * blockIdx.x;               // lane's columns n0 + 8 m + 0..7
-  for (int k = 0; k < a.k; k += 32) {
-    const bf16x8 xv = *(const bf16x8*)(x + 2 * (k + 8 * quarter));
-    u32x4 r[8];
+  bf16x8 xv[K / 32];
+  u32x4 r[K / 32][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = *(const u32x4*)(w + 2 * ((int64_t)(k + 8 * quarter + i) * a.n + n0 + 8 * m));
+  for (int k = 0; k < K / 32; ++k) {
+    xv[k] = *(const bf16x8*)(x + 2 * (32 * k + 8 * quarter));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[k][i] = *(const u32x4*)(w + 2 * ((int64_t)(32 * k + 8 * quarter + i) * a.n + n0 + 8 * m));
+  }
+  __builtin_amdgcn_sched_barrier(0);   // all loads before the first product
+#pragma unroll
+  for (int k = 0; k < K / 32; ++k)
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       u32x4 v;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) v[t] = __builtin_amdgcn_perm(r[2 * t + 1][j / 2], r[2 * t][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
-      acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, __builtin_bit_cast(bf16x8, v), acc[j], 0, 0, 0);
+      for (int t = 0; t < 4; ++t) v[t] = __builtin_amdgcn_perm(r[k][2 * t + 1][j / 2], r[k][2 * t][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
+      acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[k], __builtin_bit_cast(bf16x8, v), acc[j], 0, 0, 0);
     }
-  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int b = b0 + 4 * quarter + i;
@@ -575,7 +581,7 @@ __global__ __launch_bounds__(64) void absorb_kernel(AbsorbArgs a) {
     const int chunks = a.rope / 8;
     for (int i = lane; i < 16 * chunks; i += 64) {
       const int b = b0 + i / chunks, c = i % chunks;
-      if (b < a.batch) *(u32x4*)at(b, a.n / 8 + c) = *(const u32x4*)(a.x + b * a.x_b + h * a.x_h + 2 * (a.k + 8 * c));
+      if (b < a.batch) *(u32x4*)at(b, a.n / 8 + c) = *(const u32x4*)(a.x + b * a.x_b + h * a.x_h + 2 * (K + 8 * c));
     }
   }
 }
