@@ -34,7 +34,7 @@ struct PageStepArgs {
 // Sums that stop at the largest number: what they are compared with is below 2^31.
 __device__ __forceinline__ uint32_t plus(uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); }
 
-// Inclusive prefix sums of N numbers over a workgroup of T threads, and their totals.
+// Inclusive prefix sums of N numbers over a workgroup of T threads, and their totals; buf has no reader left.
 template <int T, int N>
 __device__ __forceinline__ void sums_upto(uint32_t (&v)[N], uint32_t (&total)[N], uint32_t (&buf)[N][T / 64]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -51,7 +51,6 @@ __device__ __forceinline__ void sums_upto(uint32_t (&v)[N], uint32_t (&total)[N]
     v[i] = plus(v[i], moved(std::integral_constant<int, 0x142>(), std::integral_constant<int, 0xa>()));      // row_bcast:15 into rows 1 and 3
     v[i] = plus(v[i], moved(std::integral_constant<int, 0x143>(), std::integral_constant<int, 0xc>()));      // row_bcast:31 into rows 2 and 3
   }
-  __syncthreads();                       // buf's last readers
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (lane == 63) buf[i][wave] = v[i];
@@ -69,15 +68,19 @@ __device__ __forceinline__ void sums_upto(uint32_t (&v)[N], uint32_t (&total)[N]
     v[i] = plus(v[i], before);
   }
 }
-template <int T>
-__device__ __forceinline__ uint32_t max_of_all(uint32_t v, uint32_t (&buf)[T / 64]) {
-  v = lanes_max<64>(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
+// The largest of N numbers; buf has no reader left.
+template <int T, int N>
+__device__ __forceinline__ void max_of_all(uint32_t (&v)[N], uint32_t (&buf)[N][T / 64]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = lanes_max<64>(v[i]);
+    if ((threadIdx.x & 63) == 0) buf[i][threadIdx.x >> 6] = v[i];
+  }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < T / 64; ++w) v = buf[w] > v ? buf[w] : v;
-  return v;
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int w = 0; w < T / 64; ++w) v[i] = buf[i][w] > v[i] ? buf[i][w] : v[i];
 }
 
 // The last entry of at[0..n) that is not above i; at[0] <= i.
@@ -104,7 +107,7 @@ __device__ __forceinline__ void put_none(const PageStepArgs& a, int64_t t) {
 
 template <int T>
 __global__ __launch_bounds__(T) void page_step_kernel(PageStepArgs a) {
-  __shared__ uint32_t buf[2][T / 64], buf1[1][T / 64];
+  __shared__ uint32_t buf[2][T / 64], buf1[1][T / 64], buf2[2][T / 64];
   __shared__ int32_t fresh[T], back[T], given[T], held_at[T], len_at[T];
   const int tid = threadIdx.x;
   const int64_t head = a.ends[0], tail = a.ends[1], size = a.n_pages;
@@ -132,8 +135,9 @@ __global__ __launch_bounds__(T) void page_step_kernel(PageStepArgs a) {
     sums_upto<T>(tokens, all_tokens, buf1);
     const uint32_t tokens_upto = plus(wanted, tokens[0]);
     const bool ok = paged && tokens_upto <= (uint32_t)a.tokens;
-    const uint32_t last_page = max_of_all<T>(ok && need ? pages_upto : 0, buf[0]), last_token = max_of_all<T>(ok ? tokens_upto : 0, buf[1]);
-    const uint32_t pages_here = last_page > taken ? last_page - taken : 0, tokens_here = last_token > served_tokens ? last_token - served_tokens : 0;
+    uint32_t last[2] = {ok && need ? pages_upto : 0, ok ? tokens_upto : 0};
+    max_of_all<T>(last, buf2);
+    const uint32_t pages_here = last[0] > taken ? last[0] - taken : 0, tokens_here = last[1] > served_tokens ? last[1] - served_tokens : 0;
     // pages of ended requests, as many as the ring has places for
     const uint32_t room = (uint32_t)size - free_pages - returned, back_here = all[1] < room ? all[1] : room;
     auto place = [](uint32_t v, uint32_t from) { return (int32_t)(v < from ? 0 : v - from > 0x7fffffffu ? 0x7fffffffu : v - from); };
