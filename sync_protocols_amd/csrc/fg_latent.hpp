@@ -70,7 +70,7 @@ struct LatentShape {
   static constexpr int TILE = T * ROW;
   static constexpr int WEIGHTS = 2 * TILE;      // in LDS: [G][HW][N2][NB][64 lanes] packed weights of 4 rows, ...
   // A weight as two bf16 numbers where the matrix instructions wait for memory anyway: 131072 tokens with 16 heads take the same 33.5 us, and 1001
-  // tokens come out 0.0024 off instead of 0.0028 (0.0016 is the result's own rounding). With four waves LDS has no room for them.
+  // tokens come out 0.0025 off instead of 0.0028 (0.0016 is the result's own rounding). With four waves LDS has no room for them.
   static constexpr int N2 = G == 1 ? 2 : 1;
   static constexpr int HIGHS = WEIGHTS + N2 * G * HW * NB * 512;  // ... largest scores [G][2][HW][16], ...
   static constexpr int FLAGS = HIGHS + G * HW * 128;         // ... and whether a wave found one that raises the maximum
