@@ -122,8 +122,8 @@ fg_status fg_paged_attention(const void* q, int64_t q_b, int64_t q_h, const fg_c
  *
  * fg_latent_attention: the absorbed form of one new token a request, over a paged cache of
  * rows: the score of a token is scale ((W_k^T q_nope) . c + q_rope . r), the result W_v applied to the
- * weighted mean of c. W_k^T q_nope is rounded to bf16 before its product;
- * the mean is held as two bf16 numbers, within 2^-16.
+ * weighted mean of c. W_k^T q_nope is rounded to bf16 before its product,
+ * or held as two bf16 numbers, within 2^-16, where there are up to 16 heads; so is the mean, and so are the weights of up to 32 heads.
  *   q:      bf16 [batch][heads][nope + rope], rows on 16-byte boundaries
  *   cache:  bf16 [n_pages][page][rank + rope] rows on 16-byte boundaries (strides multiples of 8, 16 rows less than 2^31 bytes apart);
  *           width * page < 2^31, batch * width * page < 2^36 - 2^7 * batch

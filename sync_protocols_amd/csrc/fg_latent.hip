@@ -23,6 +23,8 @@ bool sizes_ok(int32_t heads, int32_t rank, int32_t rope, int32_t nope, float sca
 
 // 16-head tiles of a workgroup, and the workgroups that this makes of all heads.
 int head_tiles(int32_t heads) { return heads <= 16 ? 1 : heads <= 32 ? 2 : 4; }
+// Absorbed queries, twice where they are pairs.
+int64_t query_bytes(int64_t batch, int32_t heads, int32_t row) { return batch * heads * row * (heads <= 16 ? 4 : 2); }
 int64_t head_parts(int32_t heads) { return (heads + 16 * head_tiles(heads) - 1) / (16 * head_tiles(heads)); }
 // Workgroups of four waves that share tiles of 64 rows, one a compute unit, or, up to 32 heads, of two waves and 32 rows, two a unit: their LDS fills it.
 int latent_tile(int32_t heads) { return head_tiles(heads) > 2 ? 64 : 32; }
@@ -72,7 +74,7 @@ fg_status fg_latent_attention_bytes(int32_t batch, int32_t heads, int32_t rank, 
   if (!bytes || batch < 0 || batch > FG_ATTN_MAX_BATCH || heads < 1 || heads > FG_ATTN_MAX_HEADS || (rank != 256 && rank != 512)) return FG_EINVAL;
   const int64_t places = batch + latent_target(heads), tiles = (heads + 15) / 16;
   // absorbed queries; sums of the pieces; weighted means; pieces of every request
-  *bytes = (int64_t)batch * heads * (2 * (rank + 64) + 4 * rank) + places * tiles * 16 * (4 * rank + 8) + 8 * (int64_t)batch;
+  *bytes = query_bytes(batch, heads, rank + 64) + (int64_t)batch * heads * 4 * rank + places * tiles * 16 * (4 * rank + 8) + 8 * (int64_t)batch;
   return FG_OK;
 }
 
@@ -106,7 +108,7 @@ fg_status fg_latent_attention(const void* q, int64_t q_b, int64_t q_h, const voi
   char* at = (char*)workspace;
   LatentArgs a{};
   char* const absorbed = at;
-  at += batch * heads * 2 * (rank + 64);
+  at += query_bytes(batch, heads, rank + 64);
   a.part = (float*)at;
   at += places * tiles * 64 * rank;
   a.ml = (float*)at;
@@ -116,13 +118,15 @@ fg_status fg_latent_attention(const void* q, int64_t q_b, int64_t q_h, const voi
   a.split = SplitArgs{pages->lens, pages->table, pages->ldt, pages->batch, pages->width, pages->n_pages, pages->page, 0, latent_target(heads),
                       (int32_t*)at};
   a.a = absorbed;
+  a.rest = 2 * batch * heads * (rank + rope);
   a.cache = (const char*)cache;
   a.lse = lse;
   a.c_page = 2 * page_stride; a.c_tok = (int32_t)(2 * row_stride); a.lse_b = lse_b;
   a.heads = heads; a.tiles = (int32_t)tiles; a.parts = (int32_t)parts; a.c = scale * kLog2E;
   Launches go{stream};
   const unsigned b_tiles = (unsigned)((batch + 15) / 16);
-  const AbsorbArgs absorb{(const char*)q, (const char*)w, absorbed, 2 * q_b, 2 * q_h, 4 * (int64_t)nope * rank, (int32_t)batch, heads, rank, rope};
+  const AbsorbArgs absorb{(const char*)q, (const char*)w, absorbed, 2 * q_b, 2 * q_h, 4 * (int64_t)nope * rank, heads <= 16 ? a.rest : 0,
+                          (int32_t)batch, heads, rank, rope};
   go(nope == 128 ? absorb_kernel<128> : absorb_kernel<64>, dim3((unsigned)rank / 128, (unsigned)heads, b_tiles), dim3(64), 0, absorb);
   const dim3 grid((unsigned)((a.split.target + 7) / 8 * 8 * parts));
   if (rank == 512) rope == 64 ? launch_latent<512, 64>(a, grid, go) : launch_latent<512, 32>(a, grid, go);

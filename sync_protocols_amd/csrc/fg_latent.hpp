@@ -31,6 +31,7 @@ struct LatentArgs {
   float* lse;
   float* part;                       // [places][head tiles][R / 16][64 lanes][4]: sums as the instructions leave them
   float* ml;                         // [places][16 head tiles][2]
+  int64_t rest;                      // bytes from the queries to their rests (kQueryPairs)
   int64_t c_page, lse_b;             // bytes, elements
   int32_t c_tok, heads, tiles, parts;           // 16-head tiles; parts: workgroups that share rows, each with other heads
   float c;
@@ -70,8 +71,11 @@ struct LatentShape {
   static constexpr int TILE = T * ROW;
   static constexpr int WEIGHTS = 2 * TILE;      // in LDS: [G][HW][N2][NB][64 lanes] packed weights of 4 rows, ...
   // A weight as two bf16 numbers where the matrix instructions wait for memory anyway: 131072 tokens with 16 heads take the same 33.5 us, and 1001
-  // tokens come out 0.0025 off instead of 0.0028 (0.0016 is the result's own rounding). With four waves LDS has no room for them.
+  // tokens come out 0.0025 off instead of 0.0028 (0.0017 is the result's own rounding). With four waves LDS has no room for them.
   static constexpr int N2 = G == 1 ? 2 : 1;
+  // The same for the absorbed queries where registers have room for it, one tile of 16 heads: nothing but the result's own rounding is left
+  // (35 us; 1001 tokens 7.1 instead of 6.8).
+  static constexpr bool kQueryPairs = G * HW == 1;
   static constexpr int HIGHS = WEIGHTS + N2 * G * HW * NB * 512;  // ... largest scores [G][2][HW][16], ...
   static constexpr int FLAGS = HIGHS + G * HW * 128;         // ... and whether a wave found one that raises the maximum
   static constexpr int LDS = FLAGS + 4 * W;
@@ -210,9 +214,9 @@ __global__ __launch_bounds__(128 * G) void latent_kernel(LatentArgs a) {
   // The queries of all heads of the workgroup, through the buffer that no rows are coming to. One load after the other: unrolled, their addresses
   // spilled what the tiles need (64 requests, 128 heads: 117 us instead of 105).
   auto ask_queries = [&] {
-    if (wave >= G * HW) return;
-    const int first = 16 * (HW * G * head_part + wave);
-    const char* from = a.a + ((int64_t)p.b * a.heads + min(first, a.heads - 1)) * Sh::ROW;
+    if (wave >= (Sh::kQueryPairs ? 2 : G * HW)) return;
+    const int first = 16 * (HW * G * head_part + (Sh::kQueryPairs ? 0 : wave));
+    const char* from = a.a + (Sh::kQueryPairs && wave == 1 ? a.rest : 0) + ((int64_t)p.b * a.heads + min(first, a.heads - 1)) * Sh::ROW;
 #pragma unroll 1
     for (int i = 0; i < Sh::LOADS; ++i) {
       const int slot = 64 * i + lane, row = slot / NC, there = max(0, min(row, a.heads - 1 - first));
@@ -222,7 +226,7 @@ __global__ __launch_bounds__(128 * G) void latent_kernel(LatentArgs a) {
   ask_queries();
   bool stored = false;                 // stores of the last piece's sums were asked for after the queries
   for (;;) {
-    bf16x8 q[HW][KS];
+    bf16x8 q[HW][KS], rest[Sh::kQueryPairs ? R / 32 : 1];
     f32x4 o[HW][J];
     float top[HW], l[HW];
     {
@@ -238,6 +242,12 @@ __global__ __launch_bounds__(128 * G) void latent_kernel(LatentArgs a) {
           u32x4 w = *(const u32x4*)(buffer + key_at[s % Sh::kKeyBases] + Sh::key_offset(0, s) + 16 * Sh::ROW * (HW * group + ht));
           if (16 * (tile16 + ht) + m >= a.heads) w = u32x4{0u, 0u, 0u, 0u};
           q[ht][s] = __builtin_bit_cast(bf16x8, w);
+          if constexpr (Sh::kQueryPairs) {
+            if (s >= R / 32) continue;
+            w = *(const u32x4*)(buffer + key_at[s % Sh::kKeyBases] + Sh::key_offset(1, s));
+            if (m >= a.heads) w = u32x4{0u, 0u, 0u, 0u};
+            rest[s] = __builtin_bit_cast(bf16x8, w);
+          }
         }
 #pragma unroll
         for (int j = 0; j < J; ++j) o[ht][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -292,6 +302,10 @@ __global__ __launch_bounds__(128 * G) void latent_kernel(LatentArgs a) {
         for (int i = 0; i < B; ++i)
 #pragma unroll
           for (int ht = 0; ht < HW; ++ht) s[ht][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(key[ks % (kKeysAhead + 1)][i], q[ht][ks], s[ht][i], 0, 0, 0);
+        if constexpr (Sh::kQueryPairs)
+          if (ks < R / 32)
+#pragma unroll
+            for (int i = 0; i < B; ++i) s[0][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(key[ks % (kKeysAhead + 1)][i], rest[ks], s[0][i], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
       // this wave's weights, if no score is far above the maximum so far
@@ -526,7 +540,7 @@ __global__ __launch_bounds__((64 * LatentJoinShape<R, MANY>::WAVES)) void latent
   }
 }
 
-// absorb_kernel: a[b][h][n] = bf16( sum_k x[b][h][k] w[h][k][n] ), the keys' weights on the query's side, written with the rope part
+// absorb_kernel: a[b][h][n] = bf16( sum_k x[b][h][k] w[h][k][n] ) and, for pairs, what the rounding left, the keys' weights on the query's side, written with the rope part
 // behind them. The matrix has k rows of n, so a lane takes 8 k of 8 n and one byte permutation per pair of k and n
 // turns them. A wave has 16 rows of x and 128 columns; the weights are read once per 16 rows.
 struct AbsorbArgs {
@@ -534,6 +548,7 @@ struct AbsorbArgs {
   const char* w;
   char* a;
   int64_t x_b, x_h, w_h;             // bytes
+  int64_t rest;                      // bytes from a to what its rounding left, 0: not kept
   int32_t batch, heads, n, rope;     // n a multiple of 128
 };
 
@@ -576,6 +591,10 @@ __global__ __launch_bounds__(64) void absorb_kernel(AbsorbArgs a) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) v[t] = f2_bf16(acc[2 * t][i], acc[2 * t + 1][i]);
     *(u32x4*)at(b, n0 / 8 + m) = v;
+    if (a.rest == 0) continue;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) v[t] = f2_bf16(bf16_rest(acc[2 * t][i]), bf16_rest(acc[2 * t + 1][i]));
+    *(u32x4*)(at(b, n0 / 8 + m) + a.rest) = v;
   }
   if (blockIdx.x == 0) {
     const int chunks = a.rope / 8;

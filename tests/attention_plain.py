@@ -136,7 +136,8 @@ def rounded(x, err):
 
 
 def latent(q, w, cache, table, lens, nope, scale):
-    """Absorbed form: the keys' weights on the query's side are rounded to bf16, as the operator says."""
+    """Absorbed form: the keys' weights on the query's side are rounded to bf16, or up to 16 heads
+    held as two bf16 numbers (the second, at most 2^-8 of the first, is off by 2^-8 of itself), as the operator says."""
     batch, heads, _ = q.shape
     rank, page = w.shape[2], cache.shape[1]
     out = torch.zeros(batch, heads, nope, dtype=torch.float64)
@@ -151,7 +152,8 @@ def latent(q, w, cache, table, lens, nope, scale):
         c, r = rows[:, :rank], rows[:, rank:]
         for h in range(heads):
             x, rot, up, down = q[b, h, :nope].double(), q[b, h, nope:].double(), w[h, :nope], w[h, nope:]
-            a, a_tol = rounded(x @ up, (nope + 8) * U * (x.abs() @ up.abs()))
+            a, a_err = x @ up, (nope + 8) * U * (x.abs() @ up.abs())
+            a, a_tol = (a, 2.0 ** -16 * a.abs() + a_err) if heads <= 16 else rounded(a, a_err)
             s_tol = c.abs() @ a_tol + (rows.shape[1] + 8) * U * (c.abs() @ a.abs() + r.abs() @ rot.abs())
             mean, mean_tol, lse[b, h], lse_tol[b, h] = attend(c @ a + r @ rot, s_tol, c, scale)
             # the mean is not rounded to one bf16: take that part out of the bound again
