@@ -12,7 +12,7 @@
 //   U^T[dim][head] += C^T W^T      C^T by transposing reads: 4 tokens of a dim in a lane,
 //                                  the tokens of the lane's own scores
 // LDS gives about 100 bytes a clock, so what is read from it has to serve many heads
-// (16 heads a wave, all rows and columns each: 64 requests, 128 heads 122 us): two waves share
+// (16 heads a wave, all rows and columns each: 64 requests, 128 heads 122 us; as follows 116, and 105 with the steps noted below): two waves share
 // 16 HW heads, each takes half of the rows for the scores and half of the columns for the sum. Their weights change places through
 // LDS, 16 bytes a lane, as operands of the second product; each wave holds all of A's columns in registers.
 // Chunks of 16 bytes lie permuted in a row, so that what a read takes from 16 (8) rows falls on different banks.
