@@ -8,7 +8,7 @@
  * may be captured into a graph; pointers are device pointers owned by the caller;
  * errors FG_EINVAL (shapes, types, NULLs, alignment, outputs on memory that is
  * still read) and FG_EHIP (a launch failed). Rows, requests of 0: FG_OK, nothing is
- * launched. Results do not depend on timing.
+ * launched (but by fg_page_step, which has outputs without them too). Results do not depend on timing.
  *
  * The cache: n_pages pages of `page` rows (tokens), page a multiple of 16. A request's
  * token t lies in row t % page of page table[request][t / page]. Strides are in
@@ -58,7 +58,8 @@ extern "C" {
  *   ring:       int32 [n_pages], written;  ends: int64 [2]
  *   lens_out:   int32 [batch], may be lens;  ends_out: int64 [2], may be ends
  *   starts:     int32 [batch + 1];  slots: int64 [tokens];  positions: int32 [tokens]
- *   page >= 1 (here); width * page < 2^31. No other two may share memory. */
+ *   page >= 1 (here); width * page < 2^31. No other two may share memory. With batch 0 only starts, ends and
+ *   the outputs of `tokens` are needed: starts[0] = 0, ends_out = ends. */
 fg_status fg_page_step(const int32_t* lens, const int32_t* add, int32_t batch, int32_t* table, int64_t ldt, int32_t width,
                        int32_t* ring, const int64_t* ends, int32_t n_pages, int32_t page, int32_t* lens_out, int64_t* ends_out,
                        int32_t* starts, int64_t* slots, int32_t* positions, int32_t tokens, hipStream_t stream);

@@ -69,7 +69,6 @@ fg_status fg_page_step(const int32_t* lens, const int32_t* add, int32_t batch, i
                        int32_t* ring, const int64_t* ends, int32_t n_pages, int32_t page, int32_t* lens_out, int64_t* ends_out,
                        int32_t* starts, int64_t* slots, int32_t* positions, int32_t tokens, hipStream_t stream) {
   if (batch < 0 || width < 1 || n_pages < 1 || page < 1 || tokens < 0 || ldt < width || (int64_t)width * page > kMaxTokens) return FG_EINVAL;
-  if (batch == 0 && tokens == 0) return FG_OK;
   if (!starts || !ends || !ends_out || (batch && (!lens || !add || !table || !ring || !lens_out)) || (tokens && (!slots || !positions))) return FG_EINVAL;
   if (!aligned(lens, 4) || !aligned(add, 4) || !aligned(table, 4) || !aligned(ring, 4) || !aligned(ends, 8) || !aligned(lens_out, 4) ||
       !aligned(ends_out, 8) || !aligned(starts, 4) || !aligned(slots, 8) || !aligned(positions, 4))
