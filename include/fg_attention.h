@@ -143,7 +143,7 @@ fg_status fg_latent_attention(const void* q, int64_t q_b, int64_t q_h, const voi
  *   q:      bf16 [q_rows][heads][nope + rope], rows on 16-byte boundaries
  *   latent: bf16 [k_rows][ld], rank + rope columns, rows on 16-byte boundaries, less than 2^24 bytes apart
  *   k_rows <= 65535 * 128, q_rows < 2^31 - 1024, (q_rows / 128 + batch + 1) * heads < 2^31 - 8, heads * 2 nope < 2^31
- *   starts: int32 [batch + 1], not falling; rows outside 0..q_rows-1, 0..k_rows-1 are left out
+ *   starts: int32 [batch + 1], not falling; one outside 0..q_rows, 0..k_rows counts as the nearest of these
  *   out:    bf16 [q_rows][heads][nope], strides multiples of 4, 8-byte aligned; rows of no request are left as they were
  *   lse:    fp32 [q_rows][heads] or NULL
  *   workspace: fg_latent_prompt_bytes, 16-byte aligned */

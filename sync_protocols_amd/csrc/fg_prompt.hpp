@@ -146,12 +146,15 @@ struct PromptShape {
   static __device__ __forceinline__ int value_place(int c, int t) { return c ^ (KC == 16 ? (t & 3) << 2 : (t & 2) << 1); }
 };
 
+// Starts lie within the rows: one outside counts as the nearest. So all requests together have no more tiles than there are items.
+__device__ __forceinline__ int start_of(const int32_t* starts, int i, int64_t rows) { return min(max(starts[i], 0), (int)rows); }
+
 // Request and tile of Q queries of item `item` (in request order); false if there are fewer.
 template <int T, int Q>
 __device__ __forceinline__ bool find_queries(const PromptArgs& a, int item, SplitShared& sh, int& b, int& tile) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int per = (a.batch + T - 1) / T, from = min(tid * per, a.batch), to = min(from + per, a.batch);
-  auto tiles = [&](int i) { return max(0, a.q_starts[i + 1] - a.q_starts[i] + Q - 1) / Q; };
+  auto tiles = [&](int i) { return max(0, start_of(a.q_starts, i + 1, a.q_rows) - start_of(a.q_starts, i, a.q_rows) + Q - 1) / Q; };
   int count = 0;
   for (int i = from; i < to; ++i) count += tiles(i);
   int upto = lanes_before_and_own(count);
@@ -192,9 +195,8 @@ __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(PromptArgs a) {
   int b, tile;
   // last tiles first: they see the most keys
   if (!find_queries<64 * W, 32 * W>(a, a.items - 1 - (id - h * a.items), sh, b, tile)) return;
-  const int q_first = max(a.q_starts[b], 0), nq = (int)min((int64_t)a.q_starts[b + 1], a.q_rows) - q_first;
-  const int k_first = max(a.k_starts[b], 0), nk = (int)min((int64_t)a.k_starts[b + 1], a.k_rows) - k_first;
-  if (32 * W * tile >= nq) return;     // starts beyond the rows
+  const int q_first = start_of(a.q_starts, b, a.q_rows), nq = start_of(a.q_starts, b + 1, a.q_rows) - q_first;
+  const int k_first = start_of(a.k_starts, b, a.k_rows), nk = start_of(a.k_starts, b + 1, a.k_rows) - k_first;
   const int i0 = 32 * W * tile, i = i0 + 32 * wave + l32;          // this lane's query
   const int last = i < nq ? nk - nq + i : -1;                      // the last key that it sees
   const int wave_first = nk - nq + i0 + 32 * wave;                 // what the wave's first query sees
