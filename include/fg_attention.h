@@ -68,7 +68,7 @@ fg_status fg_page_step(const int32_t* lens, const int32_t* add, int32_t batch, i
  * of keys and values (values may be NULL: one kind of rows, as latents are).
  *   x:      bf16 [rows][heads][dim] with strides
  *   cache:  FG_BF16: the same bits; FG_E4M3: with a = max |x[i][h]| the scale a / 448 and
- *           codes rne(x * (448 / a)), 0 where a = 0 (a NaN or an infinity makes the scale NaN or infinite)
+ *           codes rne(448 x / a) of the exact quotient, 0 where a = 0 (a NaN or an infinity makes the scale NaN or infinite)
  *   scale:  fp32 [n_pages][heads][page], FG_E4M3 only
  *   slots:  int64 [rows], distinct; a row whose slot is outside 0..n_pages * page - 1 is skipped
  *   dim a multiple of 8; rows of x and of a bf16 cache start on 16-byte, of an e4m3 cache on 8-byte

@@ -265,6 +265,10 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
   *(u32x4*)(a.cache[w] + p.page * a.c_page[w] + p.at * a.c_tok[w] + h * a.c_head[w] + 16 * e) = v;
 }
 
+// For codes that are those of the exact quotient 448 x / a (a the row's maximum): with 448 x of 11 bits and a of 8 it lies on a border between two codes (5 bits) or at least 2^-13
+// of itself away from one, and the product x (448 / a) is within 2^-22 of it, so rounded to 17 bits first it falls on the right side, or on the border itself.
+__device__ __forceinline__ float bits17(float v) { return __uint_as_float((__float_as_uint(v) + 0x40u) & ~0x7fu); }      // NaN stays: its low bits come from bf16
+
 // 16 lanes a row and head, 8 V elements each. The maximum is taken over bit patterns,
 // whose order is that of the numbers, so that a NaN reaches the scale. A row whose
 // maximum is below 2^-100 is taken by 2^100 first, as 448 / a would leave fp32.
@@ -303,7 +307,7 @@ __global__ __launch_bounds__(256) void append8_kernel(AppendArgs a) {
       float f[4] = {bf16_lo(v[j][2 * k]), bf16_hi(v[j][2 * k]), bf16_lo(v[j][2 * k + 1]), bf16_hi(v[j][2 * k + 1])};
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        f[t] = f[t] * up * inv;
+        f[t] = bits17(f[t] * up * inv);
         f[t] = f[t] > 448.0f ? 448.0f : f[t] < -448.0f ? -448.0f : f[t];
       }
       const int word = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);

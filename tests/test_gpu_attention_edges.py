@@ -8,6 +8,7 @@ from sync_protocols_amd import ops
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 BF = torch.bfloat16
+E4M3 = torch.float8_e4m3fn
 
 
 def i32(*v):
@@ -48,3 +49,33 @@ def test_prompt_starts_outside_the_rows_count_as_the_nearest_row(q_starts, k_sta
     A.close(out[qs[0]:qs[-1]], want[qs[0]:qs[-1]], tol[qs[0]:qs[-1]], "out")
     A.close(lse[qs[0]:qs[-1]], wl[qs[0]:qs[-1]], lt[qs[0]:qs[-1]], "lse")
     assert (out[:qs[0]] == 5).all() and (out[qs[-1]:] == 5).all() and (lse[:qs[0]] == 5).all() and (lse[qs[-1]:] == 5).all()
+
+
+# ------------------------------------------------------------------ append
+def codes(x):
+    """e4m3 codes of x * 448 / max |x|. The quotient of bf16 numbers lies on a border between two codes or at least 2^-13 of itself away
+    from one (x 448 has 11 bits, max |x| 8, the border 5), so a quotient in 64 bits decides like an exact one; a border goes to the even code."""
+    a = x.double().abs().amax(-1, keepdim=True)
+    v = (x.double() * 448 / torch.where(a > 0, a, 1)).abs()
+    step = torch.exp2(torch.floor(torch.log2(v.clamp_min(2.0 ** -6))) - 3)
+    return torch.copysign(torch.round(v / step) * step, x.double())          # torch.round: ties to even
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256, 576])
+def test_append_8_bit_codes_are_those_of_the_exact_quotient(dim):
+    """Every code of many rows, quotients on the border between two codes among them."""
+    g = A.gen(dim)
+    rows = 2048
+    x = torch.randn(rows, 1, dim, generator=g).bfloat16()
+    # x = T a / 448 for borders T: a = 7 2^k b makes them numbers of 8 bits
+    a = 7 * torch.randint(16, 19, (rows // 2, 1), generator=g) * torch.exp2(torch.randint(-90, 90, (rows // 2, 1), generator=g).double())
+    border = torch.tensor([17, 19, 21, 23, 25, 27, 29, 31, 1, 3, 5, 7, 9, 11, 13, 15]) * torch.tensor([2.0 ** -4] * 8 + [2.0 ** -10] * 8)
+    pick = border[torch.randint(0, 16, (rows // 2, dim), generator=g)] * torch.exp2(torch.randint(0, 4, (rows // 2, dim), generator=g).double())
+    tied = pick.double() * a / 448
+    tied = torch.where(tied.bfloat16().double() == tied, tied, torch.zeros_like(tied))
+    tied[:, 0] = a[:, 0]
+    x[rows // 2:, 0] = tied.bfloat16()
+    x[5] *= 2.0 ** -120
+    cache, scale = torch.zeros(rows // 16, 16, 1, dim, dtype=E4M3, device=DEV), torch.zeros(rows // 16, 1, 16, device=DEV)
+    ops.kv_append(x.to(DEV), cache, torch.arange(rows, device=DEV), k_scale=scale)
+    assert torch.equal(cache.cpu().double().flatten(0, 1), codes(x))
