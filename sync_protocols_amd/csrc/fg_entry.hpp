@@ -29,7 +29,7 @@ constexpr int kCUs = 256;          // compute units of the part
 
 inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-// Rows of `bytes` bytes, `pitch` apart (one row: any pitch).
+// Rows of `bytes` bytes, `pitch` apart (one row: any pitch). Pitch 0, as a broadcast dimension has: all of them are the one row.
 struct Rows {
   const void* p;
   int64_t rows, bytes, pitch;
@@ -39,7 +39,9 @@ struct Rows {
 inline Rows whole(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
 
 // Do they share a byte? Rows that interleave, as columns of one buffer do, need not.
-inline bool overlap(const Rows& a, const Rows& b) {
+inline bool overlap(Rows a, Rows b) {
+  if (a.pitch == 0) a.rows = 1;
+  if (b.pitch == 0) b.rows = 1;
   if (!a.p || !b.p || a.end() <= b.begin() || b.end() <= a.begin()) return false;
   if (a.rows > b.rows) return overlap(b, a);
   if (a.pitch == b.pitch && a.rows > 1) {

@@ -79,3 +79,25 @@ def test_append_8_bit_codes_are_those_of_the_exact_quotient(dim):
     cache, scale = torch.zeros(rows // 16, 16, 1, dim, dtype=E4M3, device=DEV), torch.zeros(rows // 16, 1, 16, device=DEV)
     ops.kv_append(x.to(DEV), cache, torch.arange(rows, device=DEV), k_scale=scale)
     assert torch.equal(cache.cpu().double().flatten(0, 1), codes(x))
+
+
+# --------------------------------------------------------------- broadcasts
+def test_broadcast_inputs():
+    """Inputs with strides of zero, as expand() makes them, their row in the gap between two rows of the output where that is possible."""
+    g = A.gen(31)
+    lens, table = [20, 33], torch.tensor([[0, 1, -1], [2, 1, 0]], dtype=torch.int32)
+    row = torch.randn(4, 64, generator=g).bfloat16()
+    k, v = torch.randn(3, 16, 2, 64, generator=g).bfloat16(), torch.randn(3, 16, 1, 64, generator=g).bfloat16().expand(3, 16, 2, 64)
+    room = torch.zeros(2, 1024, dtype=BF, device=DEV)
+    room[0, 512:768] = row.flatten().to(DEV)
+    q = room[0, 512:768].view(1, 4, 64).expand(2, 4, 64)
+    out = room[:, :256].unflatten(1, (4, 64))
+    ops.paged_attention(q, k.to(DEV), v[:, :, :1].to(DEV).expand(3, 16, 2, 64), table.to(DEV), i32(*lens), out=out)
+    A.close(out, *A.paged(row.expand(2, 4, 64), k.double(), v.double(), table, lens, 0.125)[:2])
+    cache = torch.zeros(3, 16, 2, 64, dtype=BF, device=DEV)
+    ops.kv_append(row[:1].to(DEV).expand(7, 2, 64), cache, torch.arange(7, device=DEV) * 5)
+    assert (cache.flatten(0, 1)[:35:5].cpu() == row[0]).all() and (cache.flatten(0, 1)[1:35:5] == 0).all()
+    # one row of queries at all positions of a prompt
+    qp, lat, w = prompt_inputs(1, 40, 2, 32)
+    got = ops.latent_prompt(qp.to(DEV).expand(40, 2, 96), lat.to(DEV), w.to(DEV), i32(0, 40), nope=64)
+    A.close(got, *A.prompt(qp.expand(40, 2, 96), lat, w, [0, 40], [0, 40], 64, 96 ** -0.5)[:2])
