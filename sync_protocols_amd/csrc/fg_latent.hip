@@ -60,10 +60,10 @@ void launch_join(const LatentArgs& a, Launches& go) {
 
 template <int M, int P>
 void launch_prompt(const PromptArgs& a, int waves, Launches& go) {
-  const unsigned grid = 8 * (unsigned)(((int64_t)a.items * a.heads + 7) / 8);
+  const dim3 grid = wide_grid(((int64_t)a.items * a.heads + 7) / 8 * 8);          // a multiple of 8, up to 2^31 as wide too
   const size_t lds = 2 * PromptShape<M, P>::STAGE;
-  if (waves == 8) go(prompt_kernel<M, P, 8>, dim3(grid), dim3(512), lds, a);
-  else go(prompt_kernel<M, P, 4>, dim3(grid), dim3(256), lds, a);
+  if (waves == 8) go(prompt_kernel<M, P, 8>, grid, dim3(512), lds, a);
+  else go(prompt_kernel<M, P, 4>, grid, dim3(256), lds, a);
 }
 
 }  // namespace

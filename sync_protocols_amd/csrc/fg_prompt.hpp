@@ -189,8 +189,9 @@ __global__ __launch_bounds__(64 * W, 2) void prompt_kernel(PromptArgs a) {
   const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5, m = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // workgroups go round the 8 dies; a die takes neighbouring items, which share a head's keys, in its L2
-  const int total = gridDim.x, share = (total + 7) / 8, id = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
-  if (id >= a.items * a.heads) return;
+  const uint32_t share = gridDim.x * gridDim.y / 8, at_grid = blockIdx.y * gridDim.x + blockIdx.x;
+  const int id = (int)((at_grid & 7) * share + (at_grid >> 3));
+  if ((uint32_t)id >= (uint32_t)a.items * (uint32_t)a.heads) return;
   const int h = id / a.items;
   int b, tile;
   // last tiles first: they see the most keys

@@ -51,6 +51,19 @@ def test_prompt_starts_outside_the_rows_count_as_the_nearest_row(q_starts, k_sta
     assert (out[:qs[0]] == 5).all() and (out[qs[-1]:] == 5).all() and (lse[:qs[0]] == 5).all() and (lse[qs[-1]:] == 5).all()
 
 
+def test_prompt_of_as_many_requests_and_heads_as_fill_a_grid():
+    """65535 requests with 256 heads: 2^24 workgroups, more than one dimension of a grid holds. The first and the last request have rows."""
+    heads = 256
+    q, lat, w = prompt_inputs(130, 130, heads, 23)
+    starts = torch.full((65536,), 60, dtype=torch.int32, device=DEV)
+    starts[0], starts[-1] = 0, 130
+    got, lse = ops.latent_prompt(q.to(DEV), lat.to(DEV), w.to(DEV), starts, nope=64, lse=True)
+    for h in ([0, 1], [127, 255]):
+        want, tol, wl, lt = A.prompt(q[:, h], lat, w[h], [0, 60, 130], [0, 60, 130], 64, 96 ** -0.5)
+        A.close(got[:, h], want, tol)
+        A.close(lse[:, h], wl, lt)
+
+
 # ------------------------------------------------------------------ append
 def codes(x):
     """e4m3 codes of x * 448 / max |x|. The quotient of bf16 numbers lies on a border between two codes or at least 2^-13 of itself away
