@@ -72,7 +72,8 @@ fg_status fg_page_step(const int32_t* lens, const int32_t* add, int32_t batch, i
  *   scale:  fp32 [n_pages][heads][page], FG_E4M3 only
  *   slots:  int64 [rows], distinct; a row whose slot is outside 0..n_pages * page - 1 is skipped
  *   dim a multiple of 8; rows of x and of a bf16 cache start on 16-byte, of an e4m3 cache on 8-byte
- *   boundaries (strides multiples of 8). Inputs and caches share no memory. */
+ *   boundaries (strides multiples of 8). Inputs and caches share no memory. Caches of keys and values may lie
+ *   within each other if their strides are equal, or page beside page. */
 typedef struct {
   const void* x;                        /* new rows */
   int64_t x_row, x_head;

@@ -23,6 +23,15 @@ Rows rows3(const void* p, int64_t element, int64_t n, int64_t ns, int64_t heads,
   return {p, n, element * ((heads - 1) * hs + dim), element * ns};
 }
 
+// Do the caches of keys and values share memory? Ones of the same strides may lie within each other, as keys and values of a page, a token or a head do;
+// others only if their pages do not.
+bool caches_meet(const fg_append_t& k, const fg_append_t& v, int es, int64_t pages, int64_t page, int64_t heads, int64_t dim) {
+  const bool same = (pages == 1 || k.page_stride == v.page_stride) && (page == 1 || k.row_stride == v.row_stride) && (heads == 1 || k.head_stride == v.head_stride);
+  if (same) return meet({{pages, k.page_stride}, {page, k.row_stride}, {heads, k.head_stride}, {dim, 1}}, ((const char*)v.cache - (const char*)k.cache) / es);
+  auto spans = [&](const fg_append_t& t) { return Rows{t.cache, pages, es * ((page - 1) * t.row_stride + (heads - 1) * t.head_stride + dim), es * t.page_stride}; };
+  return overlap(spans(k), spans(v));
+}
+
 // Workgroups, one round of all places on the compute units: their work is equal, and a second round would only leave more sums. A
 // workgroup may have a single unit of 128 tokens (4 requests of 300 tokens: two at least 8.4 us, one 6.3, and the join of twice
 // the pieces 4.2 instead of 3.7).
@@ -128,7 +137,7 @@ fg_status fg_kv_append(const fg_append_t* keys, const fg_append_t* values, int32
   const Rows s = whole(slots, 8 * rows);
   for (int i = 0; i < n; ++i)
     if (overlaps(cache[i], s, in[0], in[1], scale[0], scale[1]) || overlaps(scale[i], s, in[0], in[1])) return FG_EINVAL;
-  if (n == 2 && (keys->cache == values->cache || overlap(scale[0], scale[1]))) return FG_EINVAL;
+  if (n == 2 && (overlap(scale[0], scale[1]) || caches_meet(*keys, *values, es, n_pages, page, heads, dim))) return FG_EINVAL;
   Launches go{stream};
   const int64_t pieces = e4m3 ? rows * heads * 16 : rows * heads * (dim / 8);
   if ((pieces + 255) / 256 > 0x7fffffff) return FG_EINVAL;

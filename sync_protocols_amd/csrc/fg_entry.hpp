@@ -84,6 +84,25 @@ inline bool distinct(std::initializer_list<Dim> dims) {
   return true;
 }
 
+// Two tensors of the same sizes and strides, whose indices all mean different elements (distinct), the second `by` elements behind the first: do they
+// share one? They do if `by` is a sum of strides, each up to size - 1 times, forwards or back. What the smaller dimensions reach is less than a stride,
+// so only the two multiples of it around `by` come into question.
+inline bool meet(std::initializer_list<Dim> dims, int64_t by) {
+  const Dim* top = nullptr;
+  for (const Dim& x : dims)
+    if (x.size > 1 && (!top || x.stride > top->stride)) top = &x;
+  if (!top) return by == 0;
+  Dim rest[4];
+  int n = 0;
+  for (const Dim& x : dims)
+    if (&x != top) rest[n++] = x;
+  while (n < 4) rest[n++] = {1, 0};
+  const int64_t q = by / top->stride;
+  for (int64_t c = q - 1; c <= q + 1; ++c)
+    if (c < top->size && -c < top->size && meet({rest[0], rest[1], rest[2], rest[3]}, by - c * top->stride)) return true;
+  return false;
+}
+
 // A grid of n workgroups for any n below 2^31: more than 2^20 in two dimensions
 // (a dimension holds fewer than 2^32 threads).
 inline dim3 wide_grid(int64_t n) {

@@ -27,3 +27,18 @@ def test_broadcast_caches_and_outputs_on_them():
     out = P + 6 * GAP
     flat = _cache(out + 64, page_stride=0, row_stride=0, head_stride=0)
     assert _paged(out=out, k=C.byref(flat)) == fg.EINVAL and _latent(out=out, cache=out + 64, page_stride=0, row_stride=0) == fg.EINVAL
+
+
+@pytest.mark.parametrize("by", [16, 128, -128, 512, 8192 - 256, -8192, 8 * 8192 - 512 - 16])
+def test_append_refuses_caches_that_partly_lie_on_each_other(by):
+    """A cache of 8 pages of 16 rows of 4 heads of 64: some columns, heads, rows or pages further on in itself, with the same strides or others."""
+    assert _append(values=dict(cache=P + GAP + by)) == fg.EINVAL
+    assert _append(values=dict(cache=P + GAP + by, row_stride=512, page_stride=8192)) == fg.EINVAL
+    wide = dict(row_stride=512, page_stride=8192)                # rows and their gaps are as long
+    assert _append(wide, dict(cache=P + GAP + 512 - 16, **wide)) == fg.EINVAL and _append(wide, dict(cache=P + GAP + 512 + 16, **wide)) == fg.EINVAL
+
+
+@pytest.mark.parametrize("at", [16, 8192 - 8])
+def test_append_refuses_8_bit_caches_that_partly_lie_on_each_other(at):
+    keys, values = dict(scale=P + 5 * GAP), dict(cache=P + GAP + at, scale=P + 6 * GAP)
+    assert _append(keys, values, t=2) == fg.EINVAL

@@ -2,8 +2,6 @@
 import os
 import subprocess
 
-import pytest
-
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SOURCE = r"""
 #include <cstdio>
@@ -51,5 +49,49 @@ def run(tmp_path, source):
 def test_rows_that_overlap_and_interleave(tmp_path):
     """Any two sets of rows, broadcast ones (pitch 0) and rows that lie on each other among them."""
     r = run(tmp_path, SOURCE)
+    assert r.returncode == 0, r.stdout
+    assert all(int(n) > 10000 for n in r.stdout.split())
+
+
+MEET = r"""
+#include <cstdio>
+#include <random>
+#include <set>
+#include "fg_entry.hpp"
+using namespace fg::ops;
+static std::mt19937 rng(2);
+static int64_t upto(int64_t n) { return (int64_t)(rng() % (n + 1)); }
+int main() {
+  int shared = 0, apart = 0;
+  while (shared + apart < 100000) {
+    Dim d[4];
+    for (Dim& x : d) x = {1 + upto(3), 1 + upto(20)};
+    d[3].stride = 1;
+    if (!distinct({d[0], d[1], d[2], d[3]})) continue;
+    std::set<int64_t> s;
+    for (int64_t n = 0; n < d[0].size * d[1].size * d[2].size * d[3].size; ++n) {
+      int64_t at = 0, left = n;
+      for (const Dim& x : d) at += left % x.size * x.stride, left /= x.size;
+      s.insert(at);
+    }
+    const int64_t by = upto(120) - 60;
+    bool want = false;
+    for (int64_t v : s) want = want || s.count(v + by);
+    if (meet({d[0], d[1], d[2], d[3]}, by) != want) {
+      for (const Dim& x : d) printf("%ld x %ld, ", (long)x.size, (long)x.stride);
+      printf("by %ld: %d\n", (long)by, want);
+      return 1;
+    }
+    (want ? shared : apart) += 1;
+  }
+  printf("%d %d\n", shared, apart);
+  return 0;
+}
+"""
+
+
+def test_tensors_that_lie_within_each_other(tmp_path):
+    """Any distance of two tensors of the same strides, against all their elements."""
+    r = run(tmp_path, MEET)
     assert r.returncode == 0, r.stdout
     assert all(int(n) > 10000 for n in r.stdout.split())

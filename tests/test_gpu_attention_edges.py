@@ -94,6 +94,35 @@ def test_append_8_bit_codes_are_those_of_the_exact_quotient(dim):
     assert torch.equal(cache.cpu().double().flatten(0, 1), codes(x))
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("kind", ["page", "token", "head", "columns", "pages"])
+def test_append_into_caches_that_lie_within_each_other(kind, e4m3):
+    """Keys and values of a page, a token or a head side by side in one buffer, and two caches of other strides page beside page."""
+    n, page, kv, dim = 4, 16, 3, 64
+    g = A.gen(41)
+    x = [torch.randn(20, kv, dim, generator=g).bfloat16() for _ in range(2)]
+    slots = torch.randperm(n * page, generator=g)[:20]
+    room = torch.zeros(n * page * kv * dim * 2, dtype=torch.uint8 if e4m3 else BF, device=DEV)
+    if kind == "page":
+        k, v = room.view(n, 2, page, kv, dim).unbind(1)
+    elif kind == "token":
+        k, v = room.view(n, page, 2, kv, dim).unbind(2)
+    elif kind == "head":
+        k, v = room.view(n, page, kv, 2, dim).unbind(3)
+    elif kind == "columns":
+        k, v = room.view(n, page, kv, 2 * dim).split(dim, -1)
+    else:                    # keys by token, values by head, in the two halves of a page
+        both = room.view(n, 2, page * kv * dim)
+        k, v = both[:, 0].unflatten(1, (page, kv, dim)), both[:, 1].unflatten(1, (kv, page, dim)).transpose(1, 2)
+    typ = E4M3 if e4m3 else BF
+    scales = [torch.zeros(n, kv, page, device=DEV) if e4m3 else None for _ in range(2)]
+    ops.kv_append(x[0].to(DEV), k.view(typ), slots.to(DEV), v=x[1].to(DEV), v_cache=v.view(typ), k_scale=scales[0], v_scale=scales[1])
+    for t, c in zip(x, (k, v)):
+        want = torch.zeros(n * page, kv, dim, dtype=torch.float64)
+        want[slots] = codes(t) if e4m3 else t.double()
+        assert torch.equal(c.view(typ).cpu().double().reshape(n * page, kv, dim), want)
+
+
 # --------------------------------------------------------------- broadcasts
 def test_broadcast_inputs():
     """Inputs with strides of zero, as expand() makes them, their row in the gap between two rows of the output where that is possible."""
