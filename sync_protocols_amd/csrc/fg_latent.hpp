@@ -107,11 +107,16 @@ __device__ __forceinline__ u32x2 read_turned(const char* from) {
 }
 
 // 16 bytes a lane from base + off to LDS at `to`, 64 lanes side by side. In assembly, because the compiler lets transposing reads wait for every
-// direct load that it knows of; these have no result registers, and loads_barrier() waits for them. m0 has no other use in this kernel.
+// direct load that it knows of; these have no result registers, and loads_barrier() waits for them.
+// m0 is named so that nothing of the compiler's own is kept in it; it warns of any reserved register there.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, const char* to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane((int)(uintptr_t)(__attribute__((address_space(3))) const char*)to)),
-               "v"(off), "s"(base));
+               "v"(off), "s"(base)
+               : "m0");
 }
+#pragma clang diagnostic pop
 
 // The rows of a workgroup's pieces, tile after tile, for the direct loads, which run one tile ahead of the products. Page and
 // place of 64 blocks are in the lanes; those of the next ones, or of the next piece, are asked for with the tile before.
