@@ -132,7 +132,7 @@ struct RowTiles {
   __device__ __forceinline__ void fetch(const SplitArgs& s, int lane) {
     const uint32_t tok = (uint32_t)p.begin + T * (uint32_t)t + 16 * (uint32_t)lane, i = tok / (uint32_t)s.page;
     at = (int32_t)(tok - i * (uint32_t)s.page);
-    page = i < (uint32_t)s.width ? s.table[p.b * s.ldt + i] : -1;
+    page = tok < (uint32_t)p.len ? s.table[p.b * s.ldt + i] : -1;          // not behind the last token
   }
   __device__ __forceinline__ void enter(const SplitArgs& s, int lane) {       // the piece p, or the first one after it that has rows
     more = true;

@@ -130,15 +130,16 @@ struct PagedTile {
   }
 };
 
-// A page that is not the cache's, or none, has no tokens. Lane l holds page and place of the l-th block from `block0` on.
+// A page that is not the cache's, or none, has no tokens. Lane l holds page and place of the l-th block from `block0` on; the table is read up to the
+// request's last token (which lies within its width).
 struct BlockList {
   int32_t page, at, block0;
-  __device__ __forceinline__ void fetch(const SplitArgs& s, int b, int block, int lane) {
+  __device__ __forceinline__ void fetch(const SplitArgs& s, int b, int len, int block, int lane) {
     block0 = block;
     const int64_t t = 16 * (int64_t)(block + lane);
     const int64_t i = t / s.page;
     at = (int32_t)(t - i * s.page);
-    page = i < s.width ? s.table[b * s.ldt + i] : -1;
+    page = t < len ? s.table[b * s.ldt + i] : -1;
   }
   template <class P>
   __device__ __forceinline__ Blocks get(const SplitArgs& s, const P& p, int block) const {
@@ -219,7 +220,7 @@ __global__ __launch_bounds__(64 * kPagedWaves) void paged_kernel(PagedArgs a) {
     Blocks now, next;
     auto place = [&](int t) {
       const int block = block0 + 2 * t;
-      if (t == t0 || block - list.block0 >= 64) list.fetch(a.split, p.b, block, lane);
+      if (t == t0 || block - list.block0 >= 64) list.fetch(a.split, p.b, p.len, block, lane);
       return list.get(a.split, p, block);
     };
     if (t0 < t1) {
