@@ -122,7 +122,7 @@ class CapturedDecode:
         self.x = torch.zeros(tokens, hidden, dtype=torch.bfloat16, device=device)
         self.add = torch.zeros(tokens, dtype=torch.int32, device=device)
         self.workspace = attention.workspace(tokens), experts.workspace(tokens)
-        self.weights = [v for o in (attention, experts) for v in vars(o).values()]          # the graph holds their addresses
+        self.weights = [v for o in (attention, experts, attention.pages) for v in vars(o).values()]          # the graph holds their addresses
         side = torch.cuda.Stream(device)
         side.wait_stream(torch.cuda.current_stream(device))
         with torch.cuda.stream(side):          # without new tokens: nothing moves on; the library product's own setup happens here

@@ -1,8 +1,13 @@
 """The attention half's operators on the GPU in calls that are empty, ragged, tied or far out."""
+import gc
+import weakref
+
 import pytest
 import torch
 
 import attention_plain as A
+from sync_protocols_amd import attention_layer as L
+from sync_protocols_amd import decode_layer as D
 from sync_protocols_amd import ops
 
 pytestmark = pytest.mark.gpu
@@ -143,3 +148,25 @@ def test_broadcast_inputs():
     qp, lat, w = prompt_inputs(1, 40, 2, 32)
     got = ops.latent_prompt(qp.to(DEV).expand(40, 2, 96), lat.to(DEV), w.to(DEV), i32(0, 40), nope=64)
     A.close(got, *A.prompt(qp.expand(40, 2, 96), lat, w, [0, 40], [0, 40], 64, 96 ** -0.5)[:2])
+
+
+# ------------------------------------------------------------------ graphs
+@pytest.mark.parametrize("kind", ["paged", "latent"])
+def test_captured_step_keeps_what_its_graph_addresses(kind):
+    """Tables, lengths, ring, caches and weights stay when the program puts others in their place."""
+    pages = L.Pages(2, 4, 8, 16, DEV)
+    attention = L.random_paged(256, 4, 2, 64, pages, group=64) if kind == "paged" else L.random_latent(256, 4, 256, 32, 64, pages, group=64)
+    captured = L.CapturedDecode(attention, D.random_layer(256, 128, 256, 8, 8, 2, group=32, device=DEV), 2)
+    held = {f"{type(o).__name__}.{k}": weakref.ref(v) for o in (attention, pages) for k, v in vars(o).items() if isinstance(v, torch.Tensor)}
+    assert len(held) > 6
+    for o in (attention, pages):
+        for k, v in list(vars(o).items()):
+            if isinstance(v, torch.Tensor):
+                setattr(o, k, v.clone())
+    del v
+    gc.collect()
+    assert [k for k, r in held.items() if r() is None] == []
+    captured.add.fill_(1)
+    captured.replay()
+    torch.cuda.synchronize()
+    assert captured.weights and pages.lens.tolist() == [0, 0]
