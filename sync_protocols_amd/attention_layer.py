@@ -22,13 +22,13 @@ from typing import Optional
 
 import torch
 
-from . import decode_layer, ops
+from . import decode_layer, fg, ops
 
 
 class Pages:
     """Pages of up to `batch` requests of up to `width` pages each, all on the GPU. step()
     takes the new tokens' counts (negative: the request has ended) and returns their slots and
-    positions; `table` and `lens` are what the attention reads. Layers share one."""
+    positions; `table` and `lens` are what the attention reads. Layers may share one: step() is then called once for all of them."""
 
     def __init__(self, batch: int, width: int, n_pages: int, page: int, device="cuda"):
         self.page, self.n_pages = page, n_pages
@@ -113,8 +113,8 @@ class LatentAttention:
 class CapturedDecode:
     """One decoding step of `tokens` requests through the attention and expert halves as one graph launch:
     pages, projections, cache, attention, experts. Fill `x` and `add` (1: a new token, 0: none, negative: ended),
-    call replay(), read `result`; the pages move on by themselves. A request that gets no slot gives a row that
-    means nothing."""
+    call replay(), read `result`; the pages move on by themselves, so no other layer shares them. A request that
+    gets no slot keeps its length in attention.pages.lens and gives a row that means nothing."""
 
     def __init__(self, attention, experts: decode_layer.ExpertLayer, tokens: int):
         hidden, device = experts.gamma.numel(), experts.gamma.device
@@ -141,7 +141,11 @@ class CapturedDecode:
 
 
 def decode_step(attention, experts: decode_layer.ExpertLayer, x: torch.Tensor, add: torch.Tensor, attention_workspace=None, expert_workspace=None):
-    """x bf16 [requests, hidden]; add int32 [requests], 1 for those that have a new token. Both halves of the layer."""
+    """x bf16 [requests, hidden]; add int32 [requests], 1 for those that have a new token. Both halves of a layer that
+    has its pages to itself, as it moves them on: where layers share their pages, call pages.step once and every
+    layer's step with its slots and positions. A request that got its slot has a length one higher than before."""
+    if x.shape[0] != attention.pages.lens.numel():
+        raise fg.FgError(fg.EINVAL, "x must have one row a request of the pages")
     p = attention.pages.step(add, x.shape[0])
     # tokens are numbered over the served requests; here every request has a row, so its slot is looked up
     at = p.starts[:-1].long().clamp_max(x.shape[0] - 1)

@@ -8,7 +8,7 @@ import torch
 import attention_plain as A
 from sync_protocols_amd import attention_layer as L
 from sync_protocols_amd import decode_layer as D
-from sync_protocols_amd import ops
+from sync_protocols_amd import fg, ops
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -170,3 +170,34 @@ def test_captured_step_keeps_what_its_graph_addresses(kind):
     captured.replay()
     torch.cuda.synchronize()
     assert captured.weights and pages.lens.tolist() == [0, 0]
+
+
+# ------------------------------------------------------------------ layers
+def test_step_of_other_rows_than_requests_leaves_the_pages():
+    pages = L.Pages(3, 4, 12, 16, DEV)
+    attention, experts = L.random_paged(256, 4, 2, 64, pages, group=64), D.random_layer(256, 128, 256, 8, 8, 2, group=32, device=DEV)
+    for rows in (0, 2, 4):
+        with pytest.raises(fg.FgError):
+            L.decode_step(attention, experts, torch.zeros(rows, 256, dtype=BF, device=DEV), i32(1, 1, 1))
+        assert pages.lens.tolist() == [0, 0, 0] and pages.ends.tolist() == [0, 12]
+
+
+def test_layers_that_share_their_pages():
+    """One step of the pages, every layer's step with its slots, against layers with pages of their own; a request without a slot is told by its length."""
+    shared = L.Pages(3, 2, 4, 16, DEV)
+    layers = [L.random_paged(256, 4, 2, 64, shared, group=64, seed=1), L.random_latent(256, 4, 256, 32, 64, shared, group=64, seed=2)]
+    alone = [L.random_paged(256, 4, 2, 64, L.Pages(3, 2, 4, 16, DEV), group=64, seed=1), L.random_latent(256, 4, 256, 32, 64, L.Pages(3, 2, 4, 16, DEV), group=64, seed=2)]
+    g = torch.Generator(device=DEV).manual_seed(9)
+    for step in range(20):
+        x = torch.randn(3, 256, device=DEV, generator=g).to(BF)
+        before = shared.lens.clone()
+        p = shared.step(i32(1, 1, 1), 3)
+        served = p.starts[1:] > p.starts[:-1]
+        assert torch.equal(shared.lens - before, served.int())
+        at = p.starts[:-1].long().clamp_max(2)
+        slots, positions = torch.where(served, p.slots[at], -1), torch.where(served, p.positions[at], 0)
+        for a, b in zip(layers, alone):
+            q = b.pages.step(i32(1, 1, 1), 3)
+            assert torch.equal(q.slots, p.slots)
+            assert torch.equal(a.step(x, slots, positions), b.step(x, slots, positions))
+    assert sorted(shared.lens.tolist()) == [16, 16, 20]
