@@ -32,8 +32,9 @@ bool caches_meet(const fg_append_t& k, const fg_append_t& v, int es, int64_t pag
   return overlap(spans(k), spans(v));
 }
 
-// Workgroups, one round of all places on the compute units: their work is equal, and a second round would only leave more sums. A
-// workgroup may have a single unit of 128 tokens (4 requests of 300 tokens: two at least 8.4 us, one 6.3, and the join of twice
+// Workgroups, two a compute unit: one round of its places for one head tile with 64 and 128 columns (3 and 2 fit) and two with 64 (2 fit). With 256
+// columns, or 128 and more head tiles, registers leave one a compute unit, so that these take two rounds and twice the sums to join; the times
+// below are with this target. Their work is equal. A workgroup may have a single unit of 128 tokens (4 requests of 300 tokens: two at least 8.4 us, one 6.3, and the join of twice
 // the pieces 4.2 instead of 3.7).
 constexpr int kPagedPlaces = 2 * kCUs;
 int paged_target(int64_t parts) {
@@ -41,7 +42,8 @@ int paged_target(int64_t parts) {
   return (int)(t < 1 ? 1 : t);
 }
 // 16-head tiles of a workgroup, and the workgroups that this makes of all heads. More tiles read a cache fewer times, but a compute unit holds fewer
-// waves with their sums; with neighbours on one die the second reader mostly finds the rows in its L2. 16 requests, one key head, bf16, us:
+// waves with their sums; with neighbours on one die the second reader mostly finds the rows in its L2. 16 requests, one key head, bf16, us (e4m3
+// caches follow the same rule, not measured by themselves):
 //   dim, heads          16384 tokens each, 1, 2, 4 tiles      65536 tokens each
 //   64, 32              22, 22                                58, 49
 //   64, 64              33, 25, 39                            99, 61, 75

@@ -26,7 +26,8 @@ int head_tiles(int32_t heads) { return heads <= 16 ? 1 : heads <= 32 ? 2 : 4; }
 // Absorbed queries, twice where they are pairs.
 int64_t query_bytes(int64_t batch, int32_t heads, int32_t row) { return batch * heads * row * (heads <= 16 ? 4 : 2); }
 int64_t head_parts(int32_t heads) { return (heads + 16 * head_tiles(heads) - 1) / (16 * head_tiles(heads)); }
-// Workgroups of four waves that share tiles of 64 rows, one a compute unit, or, up to 32 heads, of two waves and 32 rows, two a unit: their LDS fills it.
+// Workgroups of four waves that share tiles of 64 rows, one a compute unit, or, up to 32 heads, of two waves and 32 rows, two a unit: their LDS fills it with rank
+// 512, their registers with rank 256 and two head tiles. With one head tile of rank 256 three would fit; two are taken all the same.
 int latent_tile(int32_t heads) { return head_tiles(heads) > 2 ? 64 : 32; }
 int latent_target(int32_t heads) {
   const int64_t t = kCUs * (64 / latent_tile(heads)) / head_parts(heads);

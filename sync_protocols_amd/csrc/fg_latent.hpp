@@ -11,7 +11,7 @@
 //   S^T[token][head] = C A^T       C: 16 bytes of a row
 //   U^T[dim][head] += C^T W^T      C^T by transposing reads: 4 tokens of a dim in a lane,
 //                                  the tokens of the lane's own scores
-// LDS gives about 100 bytes a clock, so what is read from it has to serve many heads
+// LDS gives at most 128 bytes a clock, so what is read from it has to serve many heads
 // (16 heads a wave, all rows and columns each: 64 requests, 128 heads 122 us; as follows 116, and 105 with the steps noted below): two waves share
 // 16 HW heads, each takes half of the rows for the scores and half of the columns for the sum. Their weights change places through
 // LDS, 16 bytes a lane, as operands of the second product; each wave holds all of A's columns in registers.
@@ -159,8 +159,8 @@ struct RowTiles {
     ++t;
     return seen;
   }
-  // The i-th of its Sh::LOADS loads. A compute unit takes them at 18 bytes a clock (4000 for a tile of 64) and a wave that asks for more waits until
-  // it may, so they are asked for one by one between the products.
+  // The i-th of its Sh::LOADS loads. A wave that asks for more than the unit takes waits until it may, so they are asked for one by one between
+  // the products (340 clocks of a tile's 7600 are left to wait for them).
   uint32_t off[Sh::LOADS];
   __device__ __forceinline__ void set(const LatentArgs& a, int lane) {
 #pragma unroll
