@@ -24,7 +24,8 @@
  * that it sees gives what the formula gives, or NaN. lse is log(sum exp(scale s)) over the tokens seen,
  * by which results of parts of a cache can be joined.
  * Scores, maxima and sums are fp32; a token's weight is rounded to bf16 (2^-8 relative at most) before it
- * multiplies the value, and the result is rounded once.
+ * multiplies the value, and the result is rounded once. Weights are up to 2^8 and are divided by their sum at the
+ * end, so a value times the number of tokens has to stay below 2^120.
  */
 #ifndef FG_ATTENTION_H
 #define FG_ATTENTION_H
