@@ -12,15 +12,9 @@ namespace {
 
 constexpr int64_t kMaxTokens = 0x7fffffff;
 
-bool multiple(int64_t v, int64_t of) { return v >= 0 && v % of == 0; }
-
 // The extent of a cache's tensor, `element` bytes each.
 Rows extent(const void* p, int64_t element, int64_t pages, int64_t ps, int64_t rows, int64_t rs, int64_t heads, int64_t hs, int64_t dim) {
   return whole(p, element * ((pages - 1) * ps + (rows - 1) * rs + (heads - 1) * hs + dim));
-}
-// Rows of a tensor [n][heads][dim] with consecutive columns.
-Rows rows3(const void* p, int64_t element, int64_t n, int64_t ns, int64_t heads, int64_t hs, int64_t dim) {
-  return {p, n, element * ((heads - 1) * hs + dim), element * ns};
 }
 
 // Do the caches of keys and values share memory? Ones of the same strides may lie within each other, as keys and values of a page, a token or a head do;

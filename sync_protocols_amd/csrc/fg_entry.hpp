@@ -28,6 +28,7 @@ struct Launches {
 constexpr int kCUs = 256;          // compute units of the part
 
 inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+inline bool multiple(int64_t v, int64_t of) { return v >= 0 && v % of == 0; }
 
 // Rows of `bytes` bytes, `pitch` apart (one row: any pitch). Pitch 0, as a broadcast dimension has: all of them are the one row.
 struct Rows {
@@ -37,6 +38,10 @@ struct Rows {
   uintptr_t end() const { return begin() + (rows - 1) * pitch + bytes; }
 };
 inline Rows whole(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
+// Rows of a tensor [n][heads][dim] with consecutive columns.
+inline Rows rows3(const void* p, int64_t element, int64_t n, int64_t ns, int64_t heads, int64_t hs, int64_t dim) {
+  return {p, n, element * ((heads - 1) * hs + dim), element * ns};
+}
 
 // Do they share a byte? Rows that interleave, as columns of one buffer do, need not.
 inline bool overlap(Rows a, Rows b) {

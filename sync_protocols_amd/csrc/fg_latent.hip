@@ -11,11 +11,6 @@ namespace {
 
 constexpr int64_t kMax = 0x7fffffff;
 
-bool multiple(int64_t v, int64_t of) { return v >= 0 && v % of == 0; }
-Rows rows3(const void* p, int64_t element, int64_t n, int64_t ns, int64_t heads, int64_t hs, int64_t dim) {
-  return {p, n, element * ((heads - 1) * hs + dim), element * ns};
-}
-
 bool sizes_ok(int32_t heads, int32_t rank, int32_t rope, int32_t nope, float scale) {
   return heads >= 1 && heads <= FG_ATTN_MAX_HEADS && (rank == 256 || rank == 512) && (rope == 32 || rope == 64) && (nope == 64 || nope == 128) &&
          scale > 0.0f && scale < __builtin_inff();
