@@ -266,7 +266,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 }
 
 // For codes that are those of the exact quotient 448 x / a (a the row's maximum): with 448 x of 11 bits and a of 8 it lies on a border between two codes (5 bits) or at least 2^-13
-// of itself away from one, and the product x (448 / a) is within 2^-22 of it, so rounded to 17 bits first it falls on the right side, or on the border itself.
+// of itself away from one, and the product x (448 / a) is within 2^-22 of it, so rounded to 17 bits first it falls on the right side, or on the border itself, and none is above 448.
 __device__ __forceinline__ float bits17(float v) { return __uint_as_float((__float_as_uint(v) + 0x40u) & ~0x7fu); }      // NaN stays: its low bits come from bf16
 
 // 16 lanes a row and head, 8 V elements each. The maximum is taken over bit patterns,
@@ -306,10 +306,7 @@ __global__ __launch_bounds__(256) void append8_kernel(AppendArgs a) {
     for (int k = 0; k < 2; ++k) {
       float f[4] = {bf16_lo(v[j][2 * k]), bf16_hi(v[j][2 * k]), bf16_lo(v[j][2 * k + 1]), bf16_hi(v[j][2 * k + 1])};
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        f[t] = bits17(f[t] * up * inv);
-        f[t] = f[t] > 448.0f ? 448.0f : f[t] < -448.0f ? -448.0f : f[t];
-      }
+      for (int t = 0; t < 4; ++t) f[t] = bits17(f[t] * up * inv);
       const int word = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
       q[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], word, true);
     }
